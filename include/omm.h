@@ -13,6 +13,13 @@
  *   omm_grouped_matmul_dequant  the same over int8/uint8 weights with block
  *                        scales (DequantizeLinear fused into the weight load).
  *
+ * And, around them, the operators of a language model's decode step:
+ *   omm_lora_matmul      a shared projection with low-rank adapters chosen per row.
+ *   omm_moe_route        the expert router: top-k of a softmax.
+ *   omm_moe_layer        the whole expert layer of a few tokens.
+ *   omm_token_logprobs   log probabilities of given tokens, entropy and top
+ *                        alternatives; omm_token_logprobs_grad its gradient.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Tensors are dense and row-major (the last dim is contiguous), described by
@@ -243,6 +250,118 @@ int omm_grouped_matmul_dequant(const omm_tensor* input, const omm_tensor* qweigh
  * omm_grouped_matmul that used `workspace` had an index outside [0, G).
  * Returns OMM_OK or OMM_ERR_NULL / OMM_ERR_HIP. */
 int omm_grouped_matmul_check(const void* workspace, void* stream, int64_t* invalid_count);
+
+/* ------------------------------------------------------------------------
+ * Decode-side operators: what a language model's step does around the
+ * products above.  T is OMM_BF16, OMM_F16 or OMM_F32 (OMM_F64 returns
+ * OMM_ERR_UNSUPPORTED); sums, softmax statistics and intermediate results are
+ * fp32.  Workspaces are device memory of the caller, 256-byte aligned, of at
+ * least the stated size, used only during the call's kernels; they need no
+ * preparation.
+ */
+
+/* ------------------------------------------------------------------------
+ * A shared projection with low-rank adapters chosen per row (requests of many
+ * adapters in one batch):
+ *     Y[m, :] = X[m, :] @ W (+ bias) + scale[g] * (X[m, :] @ A[g]) @ B[g],  g = adapter_indices[m]
+ *   X (M, K); Y (M, N); bias (N) or NULL; all of T.
+ *   trans = 0: W (K, N), A (G, K, R), B (G, R, N) (the layout of
+ *   omm_grouped_matmul's weights); trans != 0: W (N, K), A (G, R, K),
+ *   B (G, N, R) (as linear layers store them).
+ *   adapter_indices (M) OMM_I32 / OMM_I64: a row whose index is outside [0, G)
+ *   (-1 by custom) has no adapter.  adapter_scale (G) OMM_F32 or NULL (1).
+ *   R <= 256 (else OMM_ERR_UNSUPPORTED).  One rounding to T of the whole sum
+ *   up to OMM_LORA_FEW_ROWS rows; above, and for layouts that take the
+ *   element-wise path, the adapter's term (with the bias) is rounded to T once
+ *   before the sum.
+ * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE, OMM_ERR_UNSUPPORTED,
+ * OMM_ERR_WORKSPACE.
+ */
+#define OMM_LORA_FEW_ROWS 64
+size_t omm_lora_matmul_workspace_size(int64_t M, int64_t K, int64_t N, int64_t R, int32_t dtype);
+int omm_lora_matmul(const omm_tensor* X, const omm_tensor* W, const omm_tensor* A, const omm_tensor* B,
+                    const omm_tensor* adapter_indices, const omm_tensor* adapter_scale, const omm_tensor* bias,
+                    int trans, omm_tensor* Y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Expert router: the top_k experts of softmax(logits) per token, as
+ * omm_grouped_matmul's group_indices and the weights of their outputs.
+ *   logits (M, E) of T; indices (M, top_k) OMM_I32 / OMM_I64, by descending
+ *   logit, ties to the lower expert; weights (M, top_k) OMM_F32:
+ *   softmax(logits[m])[indices[m, s]], divided by their sum over s if
+ *   renormalize != 0.
+ *   A logit of -inf excludes its expert: it is selected after every other one
+ *   (lower index first) with weight 0; a token whose logits are all -inf gets
+ *   weights 0.  A NaN logit ranks first and makes the token's weights NaN.
+ *   E <= OMM_MOE_MAX_EXPERTS, top_k <= min(E, OMM_MOE_MAX_TOP_K).
+ * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE (also top_k outside
+ * [0, E]), OMM_ERR_UNSUPPORTED (beyond the limits).
+ */
+#define OMM_MOE_MAX_EXPERTS 512
+#define OMM_MOE_MAX_TOP_K 16
+int omm_moe_route(const omm_tensor* logits, int top_k, int renormalize, omm_tensor* indices, omm_tensor* weights,
+                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * The expert layer of a few tokens (M <= OMM_MOE_LAYER_MAX_TOKENS; longer
+ * batches: omm_moe_route and omm_grouped_matmul), routing included:
+ *     ids, w = route(router_logits[m])            (as omm_moe_route)
+ *     Y[m, :] = sum_s w[m, s] * (act(X[m] @ W_gate[e]) * (X[m] @ W_up[e])) @ W_down[e],  e = ids[m, s]
+ *   X, Y (M, K) of T; router_logits (M, E) of any T of its own.
+ *   trans = 0: W_gate, W_up (E, K, F), W_down (E, F, K) (the layout of
+ *   omm_grouped_matmul's weights); trans != 0: (E, F, K) and (E, K, F) (as
+ *   linear layers store them).  1 <= top_k <= E.
+ *   act: OMM_ACT_SILU x / (1 + e^-x), OMM_ACT_GELU x (1 + erf(x / sqrt 2)) / 2.
+ *   The product of the two branches is held in fp32; one rounding to T at the end.
+ *   Only the experts in use are read, each once per 64 tokens.
+ * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE, OMM_ERR_UNSUPPORTED,
+ * OMM_ERR_WORKSPACE.
+ */
+#define OMM_MOE_LAYER_MAX_TOKENS 64
+#define OMM_ACT_SILU 0
+#define OMM_ACT_GELU 1
+size_t omm_moe_layer_workspace_size(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k);
+int omm_moe_layer(const omm_tensor* X, const omm_tensor* router_logits, int top_k, int renormalize,
+                  const omm_tensor* W_gate, const omm_tensor* W_up, const omm_tensor* W_down, int activation,
+                  int trans, omm_tensor* Y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities of given tokens, entropy and top alternatives.
+ *   logits (M, V) of T, targets (M) OMM_I32 / OMM_I64; with p = softmax(logits[m]):
+ *     logprobs[m] = ln p[targets[m]]; 0 for a target outside [0, V) (ignored rows)
+ *     entropy[m]  = -sum_v p[v] ln p[v]           (NULL: not wanted)
+ *     lse[m]      = ln sum_v e^logits[m, v]       (NULL: not wanted)
+ *     top_ids, top_logprobs (M, top_k): the top_k tokens of largest logit by
+ *     descending logit, ties to the lower token, and their log probabilities
+ *     (ignored, may be NULL, if top_k = 0).
+ *   top_ids is OMM_I32, every other output OMM_F32.  top_k <= min(V,
+ *   OMM_TOKEN_LOGPROBS_MAX_TOP_K).
+ *   A logit of -inf has probability 0 (log probability -inf, no share in the
+ *   entropy); a row of nothing but -inf has lse and log probabilities -inf and
+ *   entropy 0.  A NaN or +inf logit makes the row's results NaN (top_ids then
+ *   ranks NaN first).
+ * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE (also V = 0, top_k
+ * outside [0, V]), OMM_ERR_UNSUPPORTED, OMM_ERR_WORKSPACE.
+ */
+#define OMM_TOKEN_LOGPROBS_MAX_TOP_K 32
+size_t omm_token_logprobs_workspace_size(int64_t M, int64_t V, int64_t top_k);
+int omm_token_logprobs(const omm_tensor* logits, const omm_tensor* targets, int top_k, omm_tensor* logprobs,
+                       omm_tensor* entropy, omm_tensor* lse, omm_tensor* top_ids, omm_tensor* top_logprobs,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of omm_token_logprobs with respect to the logits, for incoming
+ * gradients of logprobs (gl) and, optionally, of entropy (gH):
+ *     grad_logits[m, v] = gl[m] ([v = target] - p[v]) - gH[m] p[v] (ln p[v] + H[m])
+ * with p[v] = e^(logits[m, v] - lse[m]) and H = entropy, both as the forward
+ * call left them (entropy may be NULL if grad_entropy is).  A row whose target
+ * is outside [0, V) has gl = 0; a row of nothing but -inf has gradient 0.
+ * grad_logits (M, V) of T may be the logits tensor itself.
+ * Errors: OMM_ERR_NULL (also grad_entropy without entropy), OMM_ERR_DTYPE,
+ * OMM_ERR_SHAPE, OMM_ERR_UNSUPPORTED.
+ */
+int omm_token_logprobs_grad(const omm_tensor* logits, const omm_tensor* targets, const omm_tensor* lse,
+                            const omm_tensor* entropy, const omm_tensor* grad_logprobs,
+                            const omm_tensor* grad_entropy, omm_tensor* grad_logits, void* stream);
 
 #ifdef __cplusplus
 }

@@ -62,6 +62,18 @@ def lib():
         L.omm_grouped_matmul.argtypes = [P, P, P, P, P, vp, ctypes.c_size_t, vp]
         L.omm_grouped_matmul_check.argtypes = [vp, vp, i64p]
         L.omm_grouped_matmul_dequant.argtypes = [P, P, P, P, ctypes.c_int64, P, P, P, vp, ctypes.c_size_t, vp]
+        i64, sz = ctypes.c_int64, ctypes.c_size_t
+        L.omm_lora_matmul_workspace_size.restype = sz
+        L.omm_lora_matmul_workspace_size.argtypes = [i64] * 4 + [ctypes.c_int32]
+        L.omm_lora_matmul.argtypes = [P] * 7 + [ci, P, vp, sz, vp]
+        L.omm_moe_route.argtypes = [P, ci, ci, P, P, vp]
+        L.omm_moe_layer_workspace_size.restype = sz
+        L.omm_moe_layer_workspace_size.argtypes = [i64] * 5
+        L.omm_moe_layer.argtypes = [P, P, ci, ci, P, P, P, ci, ci, P, vp, sz, vp]
+        L.omm_token_logprobs_workspace_size.restype = sz
+        L.omm_token_logprobs_workspace_size.argtypes = [i64] * 3
+        L.omm_token_logprobs.argtypes = [P, P, ci, P, P, P, P, P, vp, sz, vp]
+        L.omm_token_logprobs_grad.argtypes = [P] * 7 + [vp]
         _lib = L
     return _lib
 
@@ -214,3 +226,116 @@ def grouped_matmul_check(workspace, stream=None):
     _check(lib().omm_grouped_matmul_check(ctypes.c_void_p(workspace.data_ptr()), _stream(stream), ctypes.byref(n)),
            "omm_grouped_matmul_check")
     return n.value
+
+
+# ---------------------------------------------------------------- decode-side operators
+
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+def _ref(x):
+    """Pointer to x's omm_tensor (None stays None)."""
+    return ctypes.byref(describe(x)) if x is not None else None
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    return workspace, ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
+
+
+def lora_matmul_workspace_size(M, K, N, R, dtype):
+    return int(lib().omm_lora_matmul_workspace_size(int(M), int(K), int(N), int(R), _DT[dtype]))
+
+
+def lora_matmul(X, W, A, B, adapter_indices, adapter_scale=None, bias=None, trans=0, Y=None, workspace=None,
+                stream=None):
+    """Y[m] = X[m] @ W (+ bias) + scale[g] * (X[m] @ A[g]) @ B[g], g = adapter_indices[m].
+
+    trans=0: W (K, N), A (G, K, R), B (G, R, N); trans=1: W (N, K), A (G, R, K), B (G, N, R).
+    A row whose index is outside [0, G) has no adapter.  Returns (Y, workspace)."""
+    L = lib()
+    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3:
+        raise ValueError("X and W must be 2-d, A 3-d")
+    M, K, N, R = X.shape[0], X.shape[1], W.shape[0 if trans else 1], A.shape[1 if trans else 2]
+    if Y is None:
+        Y = torch.empty((M, N), dtype=X.dtype, device=X.device)
+    workspace, ws, nws = _workspace(workspace, lora_matmul_workspace_size(M, K, N, R, X.dtype), X.device)
+    _check(L.omm_lora_matmul(_ref(X), _ref(W), _ref(A), _ref(B), _ref(adapter_indices), _ref(adapter_scale),
+                             _ref(bias), int(trans), _ref(Y), ws, nws, _stream(stream)), "omm_lora_matmul")
+    return Y, workspace
+
+
+def moe_route(logits, top_k, renormalize=True, indices=None, weights=None, stream=None):
+    """The top_k experts of softmax(logits) per token, by descending logit (ties: lower index), and
+    their weights (renormalised over the selected ones if renormalize).  Returns (indices, weights):
+    indices int32 as grouped_matmul's group_indices, weights fp32."""
+    L = lib()
+    if indices is None:
+        indices = torch.empty((logits.shape[0], top_k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((logits.shape[0], top_k), dtype=torch.float32, device=logits.device)
+    _check(L.omm_moe_route(_ref(logits), int(top_k), int(renormalize), _ref(indices), _ref(weights),
+                           _stream(stream)), "omm_moe_route")
+    return indices, weights
+
+
+def moe_layer_workspace_size(M, K, F, E, top_k):
+    return int(lib().omm_moe_layer_workspace_size(int(M), int(K), int(F), int(E), int(top_k)))
+
+
+def moe_layer(X, router_logits, top_k, W_gate, W_up, W_down, renormalize=True, activation="silu", trans=0, Y=None,
+              workspace=None, stream=None):
+    """The expert layer of a few tokens (at most 64), routing included:
+    Y[m] = sum_s w[m, s] * (act(X[m] @ W_gate[e]) * (X[m] @ W_up[e])) @ W_down[e].
+
+    trans=0: W_gate, W_up (E, K, F), W_down (E, F, K) as grouped_matmul's weights; trans=1: (E, F, K)
+    and (E, K, F).  activation: "silu" or "gelu" (erf).  Returns (Y, workspace)."""
+    L = lib()
+    if X.dim() != 2 or W_gate.dim() != 3:
+        raise ValueError("X must be 2-d, the weights 3-d")
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
+    M, K, E, F = X.shape[0], X.shape[1], W_gate.shape[0], W_gate.shape[1 if trans else 2]
+    if Y is None:
+        Y = torch.empty_like(X)
+    workspace, ws, nws = _workspace(workspace, moe_layer_workspace_size(M, K, F, E, top_k), X.device)
+    _check(L.omm_moe_layer(_ref(X), _ref(router_logits), int(top_k), int(renormalize), _ref(W_gate), _ref(W_up),
+                           _ref(W_down), ACTIVATIONS[activation], int(trans), _ref(Y), ws, nws, _stream(stream)),
+           "omm_moe_layer")
+    return Y, workspace
+
+
+def token_logprobs_workspace_size(M, V, top_k):
+    return int(lib().omm_token_logprobs_workspace_size(int(M), int(V), int(top_k)))
+
+
+def token_logprobs(logits, targets, top_k=0, workspace=None, stream=None):
+    """Log probabilities of `targets` under softmax(logits), entropy, log-sum-exp and the top_k tokens.
+
+    Returns (logprobs, entropy, lse, top_ids, top_logprobs): fp32 (M), (M), (M), int32 (M, top_k) and
+    fp32 (M, top_k).  A target outside [0, V) gives log probability 0."""
+    L = lib()
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-d")
+    M, V = logits.shape
+    lp, ent, lse = (torch.empty((M,), dtype=torch.float32, device=logits.device) for _ in range(3))
+    ids = torch.empty((M, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+    tlp = torch.empty((M, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+    workspace, ws, nws = _workspace(workspace, token_logprobs_workspace_size(M, V, top_k), logits.device)
+    _check(L.omm_token_logprobs(_ref(logits), _ref(targets), int(top_k), _ref(lp), _ref(ent), _ref(lse), _ref(ids),
+                                _ref(tlp), ws, nws, _stream(stream)), "omm_token_logprobs")
+    return lp, ent, lse, ids, tlp
+
+
+def token_logprobs_grad(logits, targets, lse, grad_logprobs, entropy=None, grad_entropy=None, grad_logits=None,
+                        stream=None):
+    """Gradient of token_logprobs' logprobs (and entropy, if grad_entropy is given) with respect to the
+    logits; grad_logits may be the logits tensor itself."""
+    L = lib()
+    if grad_logits is None:
+        grad_logits = torch.empty_like(logits)
+    _check(L.omm_token_logprobs_grad(_ref(logits), _ref(targets), _ref(lse), _ref(entropy), _ref(grad_logprobs),
+                                     _ref(grad_entropy), _ref(grad_logits), _stream(stream)),
+           "omm_token_logprobs_grad")
+    return grad_logits

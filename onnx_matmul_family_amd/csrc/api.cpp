@@ -696,3 +696,242 @@ int omm_grouped_matmul_check(const void* workspace, void* stream, int64_t* inval
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ decode-side operators
+
+namespace {
+
+// bf16 / fp16 / fp32 -> launcher kind 0 / 1 / 2; fp64 is refused as not
+// implemented, everything else as a wrong type
+int float_kind(int dt, int* kind) {
+    if (dt == OMM_BF16) *kind = 0;
+    else if (dt == OMM_F16) *kind = 1;
+    else if (dt == OMM_F32) *kind = 2;
+    else return dt == OMM_F64 ? OMM_ERR_UNSUPPORTED : OMM_ERR_DTYPE;
+    return OMM_OK;
+}
+
+bool is_index(const omm_tensor* t) { return t->dtype == OMM_I32 || t->dtype == OMM_I64; }
+
+bool has_shape(const omm_tensor* t, int nd, int64_t d0, int64_t d1 = 0, int64_t d2 = 0) {
+    if (t->ndim != nd) return false;
+    const int64_t d[3] = {d0, d1, d2};
+    for (int i = 0; i < nd; ++i)
+        if (t->shape[i] != d[i]) return false;
+    return true;
+}
+
+// an optional fp32 tensor of shape (n)
+int check_f32_vec(const omm_tensor* t, int64_t n) {
+    if (!t) return OMM_OK;
+    int rc;
+    if ((rc = check_tensor(t))) return rc;
+    if (t->dtype != OMM_F32) return OMM_ERR_DTYPE;
+    return has_shape(t, 1, n) ? OMM_OK : OMM_ERR_SHAPE;
+}
+
+int check_workspace(const void* ws, size_t bytes, size_t need) {
+    if (need == 0) return OMM_OK;
+    return !ws || bytes < need || ((uintptr_t)ws & 255) ? OMM_ERR_WORKSPACE : OMM_OK;
+}
+
+constexpr int64_t kMaxBlocks = 0x7fffffffLL;
+
+}  // namespace
+
+extern "C" {
+
+size_t omm_lora_matmul_workspace_size(int64_t M, int64_t K, int64_t N, int64_t R, int32_t dtype) {
+    int kind;
+    if (M <= 0 || K < 0 || N <= 0 || R < 0 || float_kind(dtype, &kind)) return 0;
+    return omm::lora_workspace_bytes(M, K, N, R, kind);
+}
+
+int omm_lora_matmul(const omm_tensor* X, const omm_tensor* W, const omm_tensor* A, const omm_tensor* B,
+                    const omm_tensor* adapter_indices, const omm_tensor* adapter_scale, const omm_tensor* bias,
+                    int trans, omm_tensor* Y, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc, kind;
+    for (const omm_tensor* t : {X, W, A, B, adapter_indices, (const omm_tensor*)Y})
+        if ((rc = check_tensor(t))) return rc;
+    if (bias && (rc = check_tensor(bias))) return rc;
+    const int dt = X->dtype;
+    for (const omm_tensor* t : {W, A, B, (const omm_tensor*)Y})
+        if (t->dtype != dt) return OMM_ERR_DTYPE;
+    if (bias && bias->dtype != dt) return OMM_ERR_DTYPE;
+    if ((rc = float_kind(dt, &kind))) return rc;
+    if (!is_index(adapter_indices)) return OMM_ERR_DTYPE;
+    if (X->ndim != 2 || W->ndim != 2 || A->ndim != 3) return OMM_ERR_SHAPE;
+    const int64_t M = X->shape[0], K = X->shape[1], N = W->shape[trans ? 0 : 1];
+    const int64_t G = A->shape[0], R = A->shape[trans ? 1 : 2];
+    if (W->shape[trans ? 1 : 0] != K || A->shape[trans ? 2 : 1] != K) return OMM_ERR_SHAPE;
+    if (!has_shape(B, 3, G, trans ? N : R, trans ? R : N) || !has_shape(adapter_indices, 1, M)) return OMM_ERR_SHAPE;
+    if ((rc = check_f32_vec(adapter_scale, G))) return rc;
+    if (bias && !has_shape(bias, 1, N)) return OMM_ERR_SHAPE;
+    if (!has_shape(Y, 2, M, N)) return OMM_ERR_SHAPE;
+    if (M == 0 || N == 0) return OMM_OK;
+    if (R > 256 || M * ((N + 255) / 256) > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
+    if ((rc = check_workspace(workspace, workspace_bytes, omm::lora_workspace_bytes(M, K, N, R, kind)))) return rc;
+    omm::LoraArgs a;
+    a.X = X->data;
+    a.W = W->data;
+    a.A = A->data;
+    a.B = B->data;
+    a.idx = adapter_indices->data;
+    a.scale = adapter_scale ? (const float*)adapter_scale->data : nullptr;
+    a.bias = bias ? bias->data : nullptr;
+    a.Y = Y->data;
+    a.M = M;
+    a.K = K;
+    a.N = N;
+    a.R = R;
+    a.G = G;
+    a.trans = trans != 0;
+    a.idx64 = adapter_indices->dtype == OMM_I64;
+    return hip_status(omm::launch_lora(a, kind, workspace, (hipStream_t)stream));
+}
+
+int omm_moe_route(const omm_tensor* logits, int top_k, int renormalize, omm_tensor* indices, omm_tensor* weights,
+                  void* stream) {
+    int rc, kind;
+    for (const omm_tensor* t : {logits, (const omm_tensor*)indices, (const omm_tensor*)weights})
+        if ((rc = check_tensor(t))) return rc;
+    if ((rc = float_kind(logits->dtype, &kind))) return rc;
+    if (!is_index(indices) || weights->dtype != OMM_F32) return OMM_ERR_DTYPE;
+    if (logits->ndim != 2) return OMM_ERR_SHAPE;
+    const int64_t M = logits->shape[0], E = logits->shape[1];
+    if (top_k < 0 || top_k > E) return OMM_ERR_SHAPE;
+    if (!has_shape(indices, 2, M, top_k) || !has_shape(weights, 2, M, top_k)) return OMM_ERR_SHAPE;
+    if (M == 0 || top_k == 0) return OMM_OK;
+    if (E > OMM_MOE_MAX_EXPERTS || top_k > OMM_MOE_MAX_TOP_K || M > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
+    omm::MoeRouteArgs a;
+    a.logits = logits->data;
+    a.ids = indices->data;
+    a.weights = (float*)weights->data;
+    a.M = M;
+    a.E = E;
+    a.k = top_k;
+    a.renormalize = renormalize != 0;
+    a.ids64 = indices->dtype == OMM_I64;
+    return hip_status(omm::launch_moe_route(a, kind, (hipStream_t)stream));
+}
+
+size_t omm_moe_layer_workspace_size(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k) {
+    if (M <= 0 || K <= 0 || F < 0 || E <= 0 || top_k < 0) return 0;
+    return omm::moe_layer_workspace_bytes(M, K, F, E, top_k);
+}
+
+int omm_moe_layer(const omm_tensor* X, const omm_tensor* router_logits, int top_k, int renormalize,
+                  const omm_tensor* W_gate, const omm_tensor* W_up, const omm_tensor* W_down, int activation,
+                  int trans, omm_tensor* Y, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc, kind, lkind;
+    for (const omm_tensor* t : {X, router_logits, W_gate, W_up, W_down, (const omm_tensor*)Y})
+        if ((rc = check_tensor(t))) return rc;
+    const int dt = X->dtype;
+    for (const omm_tensor* t : {W_gate, W_up, W_down, (const omm_tensor*)Y})
+        if (t->dtype != dt) return OMM_ERR_DTYPE;
+    if ((rc = float_kind(dt, &kind)) || (rc = float_kind(router_logits->dtype, &lkind))) return rc;
+    if (X->ndim != 2 || router_logits->ndim != 2 || W_gate->ndim != 3) return OMM_ERR_SHAPE;
+    const int64_t M = X->shape[0], K = X->shape[1], E = W_gate->shape[0], F = W_gate->shape[trans ? 1 : 2];
+    if (W_gate->shape[trans ? 2 : 1] != K || !same_shape(W_gate, W_up)) return OMM_ERR_SHAPE;
+    if (!has_shape(W_down, 3, E, trans ? K : F, trans ? F : K)) return OMM_ERR_SHAPE;
+    if (!has_shape(router_logits, 2, M, E) || !has_shape(Y, 2, M, K)) return OMM_ERR_SHAPE;
+    if (top_k < 1 || top_k > E) return OMM_ERR_SHAPE;
+    if (activation != OMM_ACT_SILU && activation != OMM_ACT_GELU) return OMM_ERR_UNSUPPORTED;
+    if (M == 0 || K == 0) return OMM_OK;
+    if (M > OMM_MOE_LAYER_MAX_TOKENS || E > OMM_MOE_MAX_EXPERTS || top_k > OMM_MOE_MAX_TOP_K ||
+        K > kMaxBlocks || F > kMaxBlocks)
+        return OMM_ERR_UNSUPPORTED;
+    if ((rc = check_workspace(workspace, workspace_bytes, omm::moe_layer_workspace_bytes(M, K, F, E, top_k))))
+        return rc;
+    omm::MoeLayerArgs a;
+    a.X = X->data;
+    a.logits = router_logits->data;
+    a.w_gate = W_gate->data;
+    a.w_up = W_up->data;
+    a.w_down = W_down->data;
+    a.Y = Y->data;
+    a.M = M;
+    a.K = K;
+    a.F = F;
+    a.E = E;
+    a.k = top_k;
+    a.renormalize = renormalize != 0;
+    a.activation = activation;
+    a.trans = trans != 0;
+    return hip_status(omm::launch_moe_layer(a, kind, lkind, workspace, (hipStream_t)stream));
+}
+
+size_t omm_token_logprobs_workspace_size(int64_t M, int64_t V, int64_t top_k) {
+    if (M <= 0 || V <= 0 || V > kMaxBlocks || top_k < 0) return 0;
+    return omm::token_logprobs_workspace_bytes(M, V, top_k);
+}
+
+int omm_token_logprobs(const omm_tensor* logits, const omm_tensor* targets, int top_k, omm_tensor* logprobs,
+                       omm_tensor* entropy, omm_tensor* lse, omm_tensor* top_ids, omm_tensor* top_logprobs,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    int rc, kind;
+    for (const omm_tensor* t : {logits, targets, (const omm_tensor*)logprobs})
+        if ((rc = check_tensor(t))) return rc;
+    if ((rc = float_kind(logits->dtype, &kind))) return rc;
+    if (!is_index(targets)) return OMM_ERR_DTYPE;
+    if (logits->ndim != 2) return OMM_ERR_SHAPE;
+    const int64_t M = logits->shape[0], V = logits->shape[1];
+    if (V < 1 || top_k < 0 || top_k > V || !has_shape(targets, 1, M)) return OMM_ERR_SHAPE;
+    for (const omm_tensor* t : {(const omm_tensor*)logprobs, (const omm_tensor*)entropy, (const omm_tensor*)lse})
+        if ((rc = check_f32_vec(t, M))) return rc;
+    if (top_k > 0) {
+        if ((rc = check_tensor(top_ids)) || (rc = check_tensor(top_logprobs))) return rc;
+        if (top_ids->dtype != OMM_I32 || top_logprobs->dtype != OMM_F32) return OMM_ERR_DTYPE;
+        if (!has_shape(top_ids, 2, M, top_k) || !has_shape(top_logprobs, 2, M, top_k)) return OMM_ERR_SHAPE;
+    }
+    if (M == 0) return OMM_OK;
+    // (at least 512 rows are not split, fewer into at most 64 parts each)
+    if (top_k > OMM_TOKEN_LOGPROBS_MAX_TOP_K || V > kMaxBlocks - 65536 || M > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
+    if ((rc = check_workspace(workspace, workspace_bytes, omm::token_logprobs_workspace_bytes(M, V, top_k))))
+        return rc;
+    omm::TokenLogprobsArgs a;
+    a.logits = logits->data;
+    a.targets = targets->data;
+    a.logprobs = (float*)logprobs->data;
+    a.entropy = entropy ? (float*)entropy->data : nullptr;
+    a.lse = lse ? (float*)lse->data : nullptr;
+    a.top_ids = top_k > 0 ? (int32_t*)top_ids->data : nullptr;
+    a.top_logprobs = top_k > 0 ? (float*)top_logprobs->data : nullptr;
+    a.M = M;
+    a.V = V;
+    a.k = top_k;
+    a.idx64 = targets->dtype == OMM_I64;
+    return hip_status(omm::launch_token_logprobs(a, kind, workspace, (hipStream_t)stream));
+}
+
+int omm_token_logprobs_grad(const omm_tensor* logits, const omm_tensor* targets, const omm_tensor* lse,
+                            const omm_tensor* entropy, const omm_tensor* grad_logprobs,
+                            const omm_tensor* grad_entropy, omm_tensor* grad_logits, void* stream) {
+    int rc, kind;
+    for (const omm_tensor* t : {logits, targets, lse, grad_logprobs, (const omm_tensor*)grad_logits})
+        if ((rc = check_tensor(t))) return rc;
+    if (grad_entropy && !entropy) return OMM_ERR_NULL;
+    if ((rc = float_kind(logits->dtype, &kind))) return rc;
+    if (!is_index(targets) || grad_logits->dtype != logits->dtype) return OMM_ERR_DTYPE;
+    if (logits->ndim != 2) return OMM_ERR_SHAPE;
+    const int64_t M = logits->shape[0], V = logits->shape[1];
+    if (!has_shape(targets, 1, M) || !has_shape(grad_logits, 2, M, V)) return OMM_ERR_SHAPE;
+    for (const omm_tensor* t : {lse, entropy, grad_logprobs, grad_entropy})
+        if ((rc = check_f32_vec(t, M))) return rc;
+    if (M == 0 || V == 0) return OMM_OK;
+    if (V > kMaxBlocks - 65536 || M * ((V + 1023) / 1024) > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
+    omm::TokenLogprobsGradArgs a;
+    a.logits = logits->data;
+    a.targets = targets->data;
+    a.lse = (const float*)lse->data;
+    a.entropy = grad_entropy ? (const float*)entropy->data : nullptr;
+    a.g_logprobs = (const float*)grad_logprobs->data;
+    a.g_entropy = grad_entropy ? (const float*)grad_entropy->data : nullptr;
+    a.dlogits = grad_logits->data;
+    a.M = M;
+    a.V = V;
+    a.idx64 = targets->dtype == OMM_I64;
+    return hip_status(omm::launch_token_logprobs_grad(a, kind, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -100,4 +100,65 @@ hipError_t launch_grouped(const GroupedArgs& a, int dt, void* ws, hipStream_t s)
 hipError_t launch_grouped_dq(const GroupedArgs& a, int dt, void* ws, hipStream_t s);
 hipError_t grouped_invalid_count(const void* ws, hipStream_t s, int64_t* count);
 
+// Decode-side operators.  dt: 0 = bf16, 1 = fp16, 2 = fp32.
+struct TokenLogprobsArgs {
+    const void* logits;     // (M, V)
+    const void* targets;    // (M) int32 or int64
+    float* logprobs;        // (M)
+    float* entropy;         // (M) or nullptr
+    float* lse;             // (M) or nullptr
+    int32_t* top_ids;       // (M, k), k > 0
+    float* top_logprobs;    // (M, k)
+    int64_t M, V;
+    int k, idx64;
+};
+struct TokenLogprobsGradArgs {
+    const void* logits;
+    const void* targets;
+    const float* lse;
+    const float* entropy;     // nullptr if g_entropy is
+    const float* g_logprobs;
+    const float* g_entropy;   // or nullptr
+    void* dlogits;            // (M, V), may be logits itself
+    int64_t M, V;
+    int idx64;
+};
+struct MoeRouteArgs {
+    const void* logits;  // (M, E)
+    void* ids;           // (M, k) int32 or int64
+    float* weights;      // (M, k)
+    int64_t M, E;
+    int k, renormalize, ids64;
+};
+struct MoeLayerArgs {
+    const void* X;        // (M, K)
+    const void* logits;   // (M, E) of kind logits_kind
+    const void* w_gate;   // trans 0: (E, K, F), 1: (E, F, K)
+    const void* w_up;
+    const void* w_down;   // trans 0: (E, F, K), 1: (E, K, F)
+    void* Y;              // (M, K)
+    int64_t M, K, F, E;
+    int k, renormalize, activation, trans;
+};
+struct LoraArgs {
+    const void* X;       // (M, K)
+    const void* W;       // trans 0: (K, N), 1: (N, K)
+    const void* A;       // trans 0: (G, K, R), 1: (G, R, K)
+    const void* B;       // trans 0: (G, R, N), 1: (G, N, R)
+    const void* idx;     // (M) int32 or int64
+    const float* scale;  // (G) or nullptr
+    const void* bias;    // (N) or nullptr
+    void* Y;             // (M, N)
+    int64_t M, K, N, R, G;
+    int trans, idx64;
+};
+size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt);
+hipError_t launch_lora(const LoraArgs& a, int dt, void* ws, hipStream_t s);
+size_t token_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k);
+hipError_t launch_token_logprobs(const TokenLogprobsArgs& a, int dt, void* ws, hipStream_t s);
+hipError_t launch_token_logprobs_grad(const TokenLogprobsGradArgs& a, int dt, hipStream_t s);
+hipError_t launch_moe_route(const MoeRouteArgs& a, int dt, hipStream_t s);
+size_t moe_layer_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t k);
+hipError_t launch_moe_layer(const MoeLayerArgs& a, int dt, int logits_kind, void* ws, hipStream_t s);
+
 }  // namespace omm

@@ -1,0 +1,351 @@
+// Expert router (top-k of a softmax) and the expert layer of a few tokens.
+//
+//   route:  ids[m] = the k experts of largest logit (ties to the lower index),
+//           w[m, s] = softmax(logits[m])[ids[m, s]], or renormalised over the k.
+//   layer:  Y[m] = sum_s w[m, s] (act(X[m] Wg[e]) * (X[m] Wu[e])) Wd[e],  e = ids[m, s].
+//
+// The layer is two kernels.  The first routes (each workgroup the few tokens
+// by itself: no kernel, no round trip through memory before the weights
+// start to stream), takes the j-th expert in use and computes
+// h = w act(gate) * up for every token that chose it, in fp32 to the
+// workspace.  The second multiplies h by the down weights.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kernels.hpp"
+#include "row_select.hpp"
+
+namespace omm {
+
+namespace {
+
+constexpr int kMaxE = 512;    // experts (8 logits a lane); checked by the caller
+constexpr int kMaxTop = 16;   // selections a token
+constexpr int kMaxTok = 64;   // tokens of a layer call: one lane each
+
+// ------------------------------------------------------------------ routing
+// One wave, one token.  Lane l holds the logits of experts l, l + 64, ...
+// k rounds of "largest key, lowest index".  Lane s < k returns selection s.
+template <int DT, int NE>
+__device__ __forceinline__ void route_token(const typename elem_of<DT>::type* logits, int E, int k, int renorm,
+                                            int lane, int& id, float& w) {
+    uint32_t key[NE];
+    float x[NE];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int e = i * 64 + lane;
+        x[i] = e < E ? elem_f32<DT>(logits[e]) : -__builtin_inff();
+        key[i] = e < E ? order_key(x[i]) : 0;
+    }
+    uint32_t first = 0;
+    id = 0;
+    for (int s = 0; s < k; ++s) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) mx = max(mx, key[i]);
+        mx = wave_max(mx);
+        if (s == 0) first = mx;
+        int e = 0;
+#pragma unroll
+        for (int i = NE - 1; i >= 0; --i) {
+            const uint64_t b = __ballot(key[i] == mx);
+            if (b) e = i * 64 + __ffsll((unsigned long long)b) - 1;
+        }
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            if (e == i * 64 + lane) key[i] = 0;
+        if (lane == s) {
+            id = e;
+            top = mx;
+        }
+    }
+    const float mxv = key_value(first);
+    const bool none = mxv == -__builtin_inff();  // every expert masked: all weights 0
+    float p = lane < k ? expf(key_value(top) - mxv) : 0.0f;
+    float sum;
+    if (renorm) {
+        sum = wave_sum(p);
+    } else {
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            if (i * 64 + lane < E) z += expf(x[i] - mxv);
+        sum = wave_sum(z);
+    }
+    w = none ? 0.0f : p / sum;
+}
+
+template <int DT>
+__device__ __forceinline__ void route_any(const void* logits, int64_t m, int E, int k, int renorm, int lane, int& id,
+                                          float& w) {
+    const typename elem_of<DT>::type* row = (const typename elem_of<DT>::type*)logits + m * (int64_t)E;
+    if (E <= 64) route_token<DT, 1>(row, E, k, renorm, lane, id, w);
+    else if (E <= 128) route_token<DT, 2>(row, E, k, renorm, lane, id, w);
+    else if (E <= 256) route_token<DT, 4>(row, E, k, renorm, lane, id, w);
+    else route_token<DT, 8>(row, E, k, renorm, lane, id, w);
+}
+
+__device__ __forceinline__ void route_kind(int kind, const void* logits, int64_t m, int E, int k, int renorm, int lane,
+                                           int& id, float& w) {
+    if (kind == 0) route_any<0>(logits, m, E, k, renorm, lane, id, w);
+    else if (kind == 1) route_any<1>(logits, m, E, k, renorm, lane, id, w);
+    else route_any<2>(logits, m, E, k, renorm, lane, id, w);
+}
+
+struct RouteArgs {
+    const void* logits;
+    void* ids;
+    float* weights;
+    int64_t M;
+    int E, k, renorm, ids64;
+};
+
+template <int DT, int NE>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (m >= a.M) return;
+    int id;
+    float w;
+    route_token<DT, NE>((const typename elem_of<DT>::type*)a.logits + m * a.E, a.E, a.k, a.renorm, lane, id, w);
+    if (lane < a.k) {
+        if (a.ids64) ((int64_t*)a.ids)[m * a.k + lane] = id;
+        else ((int32_t*)a.ids)[m * a.k + lane] = id;
+        a.weights[m * a.k + lane] = w;
+    }
+}
+
+template <int DT>
+void route_launch(const RouteArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)((a.M + 3) / 4));
+    if (a.E <= 64) route_kernel<DT, 1><<<grid, 256, 0, s>>>(a);
+    else if (a.E <= 128) route_kernel<DT, 2><<<grid, 256, 0, s>>>(a);
+    else if (a.E <= 256) route_kernel<DT, 4><<<grid, 256, 0, s>>>(a);
+    else route_kernel<DT, 8><<<grid, 256, 0, s>>>(a);
+}
+
+// ------------------------------------------------------------------ layer
+struct LayerArgs {
+    const void* X;         // (M, K)
+    const void* logits;    // (M, E)
+    const void* wg;        // trans 0: (E, K, F), 1: (E, F, K)
+    const void* wu;
+    const void* wd;        // trans 0: (E, F, K), 1: (E, K, F)
+    void* Y;               // (M, K)
+    int32_t* ids;          // workspace: (M, k) selections
+    float* h;              // workspace: (M k, F), weighted
+    float* part;           // workspace: (M k, K)
+    int64_t K, F;
+    int M, E, k, renorm, act, trans, logits_kind;
+};
+
+__device__ __forceinline__ float activate(float g, int act) {
+    if (act == 0) return g / (1.0f + expf(-g));                    // SiLU
+    return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));     // GELU (erf)
+}
+
+// The tokens of the j-th expert in use (in ascending expert order)
+struct ExpertRows {
+    int32_t id[kMaxTok * kMaxTop];
+    float w[kMaxTok * kMaxTop];
+    uint32_t used[kMaxE / 32];
+    int32_t tok[kMaxTok], slot[kMaxTok];
+    int e, n, active;
+};
+
+// From r.id (and a __syncthreads after it was written) to the rows of the j-th
+// expert in use: r.e (-1: fewer experts in use), r.tok / r.slot / r.n.  All
+// threads call it; it ends with a __syncthreads.
+template <int NT>
+__device__ __forceinline__ void expert_rows(ExpertRows& r, int M, int k, int j, int tid) {
+    for (int i = tid; i < kMaxE / 32; i += NT) r.used[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < M * k; i += NT) atomicOr(&r.used[r.id[i] >> 5], 1u << (r.id[i] & 31));
+    __syncthreads();
+    if (tid < 64) {
+        const uint32_t word = tid < kMaxE / 32 ? r.used[tid] : 0;
+        int before = __popc(word);  // inclusive prefix of the counts
+#pragma unroll
+        for (int d = 1; d < kMaxE / 32; d <<= 1) {
+            const int o = __shfl_up(before, d, 64);
+            if (tid >= d) before += o;
+        }
+        const int total = __shfl(before, kMaxE / 32 - 1, 64);
+        before -= __popc(word);
+        const bool here = tid < kMaxE / 32 && j >= before && j < before + __popc(word);
+        int e = -1;
+        if (here) {
+            uint32_t v = word;
+            for (int i = before; i < j; ++i) v &= v - 1;
+            e = tid * 32 + __ffs(v) - 1;
+        }
+        e = wave_max(e);
+        int slot = -1;
+        if (e >= 0 && tid < M)
+            for (int s = 0; s < k; ++s)
+                if (r.id[tid * k + s] == e) slot = s;
+        const uint64_t has = __ballot(slot >= 0);
+        if (slot >= 0) {
+            const int i = __popcll(has & ((1ull << tid) - 1));
+            r.tok[i] = tid;
+            r.slot[i] = slot;
+        }
+        if (tid == 0) {
+            r.e = e;
+            r.n = __popcll(has);
+            r.active = total;
+        }
+    }
+    __syncthreads();
+}
+
+// Element-wise forms: any sizes, alignments and types.  A workgroup computes
+// 64 columns of one expert, lane = column, k split over its 4 waves.
+template <int DT>
+__global__ __launch_bounds__(256) void moe_up_any_kernel(LayerArgs a) {
+    typedef typename elem_of<DT>::type E;
+    __shared__ ExpertRows r;
+    __shared__ float red[4][2][8][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int m = wave; m < a.M; m += 4) {
+        int id;
+        float w;
+        route_kind(a.logits_kind, a.logits, m, a.E, a.k, a.renorm, lane, id, w);
+        if (lane < a.k) {
+            r.id[m * a.k + lane] = id;
+            r.w[m * a.k + lane] = w;
+        }
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = tid; i < a.M * a.k; i += 256) a.ids[i] = r.id[i];
+    expert_rows<256>(r, a.M, a.k, (int)blockIdx.y, tid);
+    if (r.e < 0) return;
+    const int64_t f = (int64_t)blockIdx.x * 64 + lane;
+    const int64_t sk = a.trans ? 1 : a.F, sf = a.trans ? a.K : 1;
+    const int64_t base = (int64_t)r.e * a.K * a.F + (f < a.F ? f : 0) * sf;
+    const E* wg = (const E*)a.wg + base;
+    const E* wu = (const E*)a.wu + base;
+    const int64_t kc = (a.K + 3) / 4, k0 = wave * kc, k1 = k0 + kc < a.K ? k0 + kc : a.K;
+    for (int t0 = 0; t0 < r.n; t0 += 8) {
+        float g[8] = {}, u[8] = {};
+        const E* x[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) x[t] = (const E*)a.X + (int64_t)r.tok[min(t0 + t, r.n - 1)] * a.K;
+        for (int64_t k = k0; k < k1; ++k) {
+            const float vg = elem_f32<DT>(wg[k * sk]), vu = elem_f32<DT>(wu[k * sk]);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float xv = elem_f32<DT>(x[t][k]);
+                g[t] = fmaf(xv, vg, g[t]);
+                u[t] = fmaf(xv, vu, u[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            red[wave][0][t][lane] = g[t];
+            red[wave][1][t][lane] = u[t];
+        }
+        __syncthreads();
+        for (int i = tid; i < 8 * 64; i += 256) {
+            const int t = i >> 6, c = i & 63;
+            const int64_t fc = (int64_t)blockIdx.x * 64 + c;
+            if (t0 + t < r.n && fc < a.F) {
+                const float gv = red[0][0][t][c] + red[1][0][t][c] + red[2][0][t][c] + red[3][0][t][c];
+                const float uv = red[0][1][t][c] + red[1][1][t][c] + red[2][1][t][c] + red[3][1][t][c];
+                const int p = r.tok[t0 + t] * a.k + r.slot[t0 + t];
+                a.h[(int64_t)p * a.F + fc] = activate(gv, a.act) * uv * r.w[p];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// A workgroup computes 64 columns of one token: its experts one after another
+template <int DT>
+__global__ __launch_bounds__(256) void moe_down_any_kernel(LayerArgs a) {
+    typedef typename elem_of<DT>::type E;
+    __shared__ float red[4][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t n = (int64_t)blockIdx.x * 64 + lane, m = blockIdx.y;
+    const int64_t sf = a.trans ? 1 : a.K, sn = a.trans ? a.F : 1;
+    const int64_t fc = (a.F + 3) / 4, f0 = wave * fc, f1 = f0 + fc < a.F ? f0 + fc : a.F;
+    float acc = 0.0f;
+    for (int s = 0; s < a.k; ++s) {
+        const int64_t p = m * a.k + s;
+        const E* wd = (const E*)a.wd + (int64_t)a.ids[p] * a.K * a.F + (n < a.K ? n : 0) * sn;
+        const float* h = a.h + p * a.F;
+        for (int64_t f = f0; f < f1; ++f) acc = fmaf(h[f], elem_f32<DT>(wd[f * sf]), acc);
+    }
+    red[wave][lane] = acc;
+    __syncthreads();
+    if (wave == 0 && n < a.K)
+        ((E*)a.Y)[m * a.K + n] = f32_elem<DT>(red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane]);
+}
+
+template <int DT>
+void layer_any(const LayerArgs& a, hipStream_t s) {
+    const int pairs = a.M * a.k, jmax = pairs < a.E ? pairs : a.E;
+    const dim3 gu((unsigned)((a.F + 63) / 64), (unsigned)jmax);
+    moe_up_any_kernel<DT><<<gu, 256, 0, s>>>(a);
+    const dim3 gd((unsigned)((a.K + 63) / 64), (unsigned)a.M);
+    moe_down_any_kernel<DT><<<gd, 256, 0, s>>>(a);
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+hipError_t launch_moe_route(const MoeRouteArgs& r, int dt, hipStream_t s) {
+    RouteArgs a;
+    a.logits = r.logits;
+    a.ids = r.ids;
+    a.weights = r.weights;
+    a.M = r.M;
+    a.E = (int)r.E;
+    a.k = r.k;
+    a.renorm = r.renormalize;
+    a.ids64 = r.ids64;
+    if (dt == 0) route_launch<0>(a, s);
+    else if (dt == 1) route_launch<1>(a, s);
+    else route_launch<2>(a, s);
+    return hipGetLastError();
+}
+
+size_t moe_layer_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t k) {
+    (void)E;
+    return align256((size_t)M * k * 4) + align256((size_t)M * k * F * 4) + align256((size_t)M * k * K * 4);
+}
+
+hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void* ws, hipStream_t s) {
+    LayerArgs a;
+    a.X = l.X;
+    a.logits = l.logits;
+    a.wg = l.w_gate;
+    a.wu = l.w_up;
+    a.wd = l.w_down;
+    a.Y = l.Y;
+    a.K = l.K;
+    a.F = l.F;
+    a.M = (int)l.M;
+    a.E = (int)l.E;
+    a.k = l.k;
+    a.renorm = l.renormalize;
+    a.act = l.activation;
+    a.trans = l.trans;
+    a.logits_kind = logits_kind;
+    char* w = (char*)ws;
+    a.ids = (int32_t*)w;
+    w += align256((size_t)l.M * l.k * 4);
+    a.h = (float*)w;
+    w += align256((size_t)l.M * l.k * l.F * 4);
+    a.part = (float*)w;
+    log_choice("moe_layer: element-wise");
+    if (dt == 0) layer_any<0>(a, s);
+    else if (dt == 1) layer_any<1>(a, s);
+    else layer_any<2>(a, s);
+    return hipGetLastError();
+}
+
+}  // namespace omm

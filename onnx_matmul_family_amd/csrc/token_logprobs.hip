@@ -1,0 +1,455 @@
+// Log probabilities of given tokens, entropy and top alternatives of rows of
+// logits, in one pass over them, and the gradient.
+//
+// Per row x[0..V):  m = max x,  s = sum e^(x-m),  t = sum e^(x-m) (x-m):
+//   lse = m + ln s,  logprob = (x[target] - m) - ln s,  entropy = ln s - t / s.
+// All three are kept online: a new maximum m' = m + d rescales s by e^-d and
+// turns t into e^-d (t - d s).  (t and d are held in units of log2.)
+//
+// The k largest come from the same pass: a lane's running maximum is the
+// largest of the elements that it has seen, so the k-th largest lane maximum
+// of any one wave is a lower bound T of the row part's k-th largest element.
+// Only lanes whose maximum reaches T read their elements a second time (from
+// L2) and list those >= T; the list is ranked by (value, lower index).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kernels.hpp"
+#include "row_select.hpp"
+
+namespace omm {
+
+namespace {
+
+constexpr int kTopMax = 32;      // top_k bound (checked by the caller)
+constexpr int kCand = 1024;      // candidates that fit the list; more go by rounds
+constexpr int kSplitMax = 64;    // row parts; one lane of the join each
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_inff();
+
+struct Stat {
+    float m, s, t;
+};
+
+// 2^((a-b) log2 e) with a <= b; a = -inf gives 0 for any b
+__device__ __forceinline__ float d_log2(float a, float b) { return (a - b) * kLog2e; }
+
+// Finite stand-in for a running maximum of -inf (nothing but -inf so far):
+// x - 0 = -inf, whose exponential is 0, where -inf - -inf would be NaN.
+__device__ __forceinline__ float safe_max(float m) { return m == kNegInf ? 0.0f : m; }
+
+__device__ __forceinline__ Stat merge(Stat a, Stat b) {
+    Stat r;
+    r.m = fmaxf(a.m, b.m);
+    const float ms = safe_max(r.m);
+    const float da = d_log2(a.m, ms), db = d_log2(b.m, ms);
+    const float ea = __builtin_amdgcn_exp2f(da), eb = __builtin_amdgcn_exp2f(db);
+    r.s = a.s * ea + b.s * eb;
+    // a part that is all -inf has t = s = 0; the clamp keeps 0 * -inf out
+    r.t = ea * (a.t + a.s * fmaxf(da, -200.0f)) + eb * (b.t + b.s * fmaxf(db, -200.0f));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void update(Stat& st, const float* f, int pos, int& best) {
+    float mv = f[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) mv = fmaxf(mv, f[i]);
+    if (mv > st.m) {
+        const float d = d_log2(st.m, mv);  // -inf for the first finite value
+        const float e = __builtin_amdgcn_exp2f(d);
+        st.t = e * (st.t + st.s * fmaxf(d, -200.0f));
+        st.s *= e;
+        st.m = mv;
+        best = pos;
+    }
+    const float ms = safe_max(st.m);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float d = (f[i] - ms) * kLog2e;
+        const float e = __builtin_amdgcn_exp2f(d);  // NaN and +inf - +inf reach s
+        st.s += e;
+        st.t = fmaf(e, fmaxf(d, -200.0f), st.t);  // e = 0 below -200
+    }
+}
+
+// One row part [v0, v1) seen by NT threads: an unaligned head of < kVec
+// elements (one a thread), whole 16-byte vectors, a tail (one a thread).
+template <int DT>
+struct Part {
+    typedef typename elem_of<DT>::type E;
+    const E* row;
+    int v0, v1;    // element range
+    int head, nv;  // head elements, vectors
+    __device__ __forceinline__ Part(const E* r, int a, int b) : row(r), v0(a), v1(b) {
+        const int mis = (int)(((uintptr_t)(r + a) & 15) / sizeof(E));
+        head = mis ? min(kVec<DT> - mis, b - a) : 0;
+        nv = (b - a - head) / kVec<DT>;
+    }
+    __device__ __forceinline__ int tail0() const { return v0 + head + nv * kVec<DT>; }
+    __device__ __forceinline__ u32x4_t vec(int j) const {
+        return *(const u32x4_t*)(row + v0 + head + (int64_t)j * kVec<DT>);
+    }
+};
+
+// Calls f(value, index) for every element that thread `tid` of NT owns
+template <int DT, int NT, typename F>
+__device__ __forceinline__ void for_own(const Part<DT>& p, int tid, F f) {
+    if (tid < p.head) f(elem_f32<DT>(p.row[p.v0 + tid]), p.v0 + tid);
+    for (int j = tid; j < p.nv; j += NT) {
+        float x[kVec<DT>];
+        unpack16<DT>(p.vec(j), x);
+#pragma unroll
+        for (int i = 0; i < kVec<DT>; ++i) f(x[i], p.v0 + p.head + j * kVec<DT> + i);
+    }
+    const int q = p.tail0() + tid;
+    if (q < p.v1) f(elem_f32<DT>(p.row[q]), q);
+}
+
+// Outputs of a row (splits == 1) or of a row part (ws)
+struct LpArgs {
+    const void* logits;
+    const void* targets;  // int32 / int64
+    float* logprobs;
+    float* entropy;  // or nullptr
+    float* lse;      // or nullptr
+    int32_t* top_ids;
+    float* top_lp;
+    // parts: stats (m, s, t, 0) per (row, split), then k keys each
+    float4* part_stat;
+    uint64_t* part_key;
+    int64_t M;
+    int V, k, splits, chunk, idx64;
+};
+
+__device__ __forceinline__ int64_t load_target(const LpArgs& a, int64_t m) {
+    return a.idx64 ? ((const int64_t*)a.targets)[m] : (int64_t)((const int32_t*)a.targets)[m];
+}
+
+// lse, entropy and the target's log probability of a whole row
+template <int DT>
+__device__ __forceinline__ void write_row(const LpArgs& a, int64_t m, Stat st, float log_s) {
+    const typename elem_of<DT>::type* row = (const typename elem_of<DT>::type*)a.logits + m * (int64_t)a.V;
+    const int64_t t = load_target(a, m);
+    const bool empty = st.m == kNegInf && st.s == 0.0f;  // every logit is -inf
+    float lp = 0.0f;  // a target outside [0, V) is ignored
+    if (t >= 0 && t < a.V) {
+        const float x = elem_f32<DT>(row[t]);
+        lp = empty ? kNegInf : (x - st.m) - log_s;
+    }
+    a.logprobs[m] = lp;
+    if (a.lse) a.lse[m] = empty ? kNegInf : st.m + log_s;
+    if (a.entropy) a.entropy[m] = empty ? 0.0f : log_s - st.t * kLn2 / st.s;
+}
+
+__device__ __forceinline__ float top_logprob(uint64_t key, Stat st, float log_s) {
+    if (st.s != st.s) return st.s;  // a NaN in the row
+    const float x = key_value((uint32_t)(key >> 32));
+    return x == kNegInf ? kNegInf : (x - st.m) - log_s;
+}
+
+template <int DT, int NT>
+__global__ __launch_bounds__(NT) void logprobs_kernel(LpArgs a) {
+    typedef typename elem_of<DT>::type E;
+    constexpr int NW = NT / 64;
+    __shared__ Stat sh_stat[NW];
+    __shared__ uint32_t sh_thr[NW];
+    __shared__ uint64_t sh_cand[kCand];
+    __shared__ uint64_t sh_red[NW];
+    __shared__ uint64_t sh_top[kTopMax];
+    __shared__ int sh_n;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t m = blockIdx.x / a.splits;
+    const int sp = (int)(blockIdx.x - m * a.splits);
+    const int v0 = min(a.V, sp * a.chunk), v1 = min(a.V, v0 + a.chunk);
+    const Part<DT> p((const E*)a.logits + m * (int64_t)a.V, v0, v1);
+
+    Stat st = {kNegInf, 0.0f, 0.0f};
+    int best = 0;
+    if (tid < p.head) {
+        const float f = elem_f32<DT>(p.row[p.v0 + tid]);
+        update<1>(st, &f, 0, best);
+    }
+    for (int j = tid; j < p.nv; j += NT) {
+        float x[kVec<DT>];
+        unpack16<DT>(p.vec(j), x);
+        update<kVec<DT>>(st, x, j, best);
+    }
+    if (p.tail0() + tid < p.v1) {
+        const float f = elem_f32<DT>(p.row[p.tail0() + tid]);
+        update<1>(st, &f, 0, best);
+    }
+    const float own_max = st.m;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        const Stat o = {__shfl_xor(st.m, d, 64), __shfl_xor(st.s, d, 64), __shfl_xor(st.t, d, 64)};
+        st = merge(st, o);
+    }
+    if (lane == 0) sh_stat[wave] = st;
+
+    const uint32_t own_key = order_key(own_max);
+    if (a.k > 0) {
+        // the wave's k-th largest lane maximum, bit by bit: the largest T with
+        // at least k lanes >= T
+        uint32_t T = 0;
+        const int k = min(a.k, 64);
+        for (int b = 31; b >= 0; --b) {
+            const uint32_t c = T | (1u << b);
+            if (__popcll(__ballot(own_key >= c)) >= k) T = c;
+        }
+        if (lane == 0) sh_thr[wave] = T;
+        if (tid == 0) sh_n = 0;
+    }
+    __syncthreads();
+    st = sh_stat[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) st = merge(st, sh_stat[w]);
+
+    if (a.k > 0) {
+        uint32_t T = sh_thr[0];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) T = max(T, sh_thr[w]);
+        const bool nan_row = st.s != st.s;  // NaN is above every value, fmaxf has not seen it
+        int n = kCand + 1;
+        if (!nan_row) {
+            if (own_key >= T)
+                for_own<DT, NT>(p, tid, [&](float x, int v) {
+                    const uint32_t key = order_key(x);
+                    if (key >= T) {
+                        const int i = atomicAdd(&sh_n, 1);
+                        if (i < kCand) sh_cand[i] = order_key64(key, (uint32_t)v);
+                    }
+                });
+            __syncthreads();
+            n = sh_n;
+        }
+        const int kk = min(a.k, v1 - v0);
+        if (n <= kCand) {  // rank the list: every key is of its own, so ranks are too
+            for (int i = tid; i < n; i += NT) {
+                const uint64_t key = sh_cand[i];
+                int r = 0;
+                for (int j = 0; j < n; ++j) r += sh_cand[j] > key;
+                if (r < kk) sh_top[r] = key;
+            }
+            __syncthreads();
+        } else {  // many equal values, or NaN: the largest key below the last one, k times
+            uint64_t last = ~0ull;
+            for (int r = 0; r < kk; ++r) {
+                uint64_t mx = 0;
+                for_own<DT, NT>(p, tid, [&](float x, int v) {
+                    const uint64_t key = order_key64(order_key(x), (uint32_t)v);
+                    if (key < last && key > mx) mx = key;
+                });
+                mx = wave_max(mx);
+                if (lane == 0) sh_red[wave] = mx;
+                __syncthreads();
+                mx = sh_red[0];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) mx = sh_red[w] > mx ? sh_red[w] : mx;
+                if (tid == 0) sh_top[r] = mx;
+                last = mx;
+                __syncthreads();
+            }
+        }
+        if (tid < a.k) {
+            const uint64_t key = tid < kk ? sh_top[tid] : 0;  // 0: the part has fewer than k elements
+            if (a.splits > 1) {
+                a.part_key[(m * a.splits + sp) * a.k + tid] = key;
+            } else {
+                a.top_ids[m * a.k + tid] = (int32_t)key64_index(key);
+                a.top_lp[m * a.k + tid] = top_logprob(key, st, logf(st.s));
+            }
+        }
+    }
+    if (tid == 0) {
+        if (a.splits > 1)
+            a.part_stat[m * a.splits + sp] = make_float4(st.m, st.s, st.t, 0.0f);
+        else
+            write_row<DT>(a, m, st, logf(st.s));
+    }
+}
+
+// One wave a row: lane i holds part i; its keys are in descending order, so
+// the k largest of all parts are k rounds of "largest head, advance".
+template <int DT>
+__global__ __launch_bounds__(64) void logprobs_join_kernel(LpArgs a) {
+    const int lane = threadIdx.x;
+    const int64_t m = blockIdx.x;
+    Stat st = {kNegInf, 0.0f, 0.0f};
+    if (lane < a.splits) {
+        const float4 v = a.part_stat[m * a.splits + lane];
+        st = {v.x, v.y, v.z};
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        const Stat o = {__shfl_xor(st.m, d, 64), __shfl_xor(st.s, d, 64), __shfl_xor(st.t, d, 64)};
+        st = merge(st, o);
+    }
+    const float log_s = logf(st.s);
+    if (lane == 0) write_row<DT>(a, m, st, log_s);
+    if (a.k == 0) return;
+    const uint64_t* keys = a.part_key + (m * a.splits + lane) * a.k;
+    int h = 0;
+    uint64_t head = lane < a.splits ? keys[0] : 0, mine = 0;
+    for (int r = 0; r < a.k; ++r) {
+        const uint64_t mx = wave_max(head);
+        if (lane == r) mine = mx;
+        if (head == mx) head = ++h < a.k ? keys[h] : 0;  // keys are distinct: one lane
+    }
+    if (lane < a.k) {
+        a.top_ids[m * a.k + lane] = (int32_t)key64_index(mine);
+        a.top_lp[m * a.k + lane] = top_logprob(mine, st, log_s);
+    }
+}
+
+struct LpGradArgs {
+    const void* logits;
+    const void* targets;
+    const float* lse;
+    const float* entropy;     // or nullptr
+    const float* g_logprobs;
+    const float* g_entropy;   // or nullptr
+    void* dlogits;
+    int64_t M;
+    int V, chunks, chunk, idx64;
+};
+
+// dx[v] = gl ([v = target] - p) - gH p (ln p + H),  p = e^(x - lse)
+struct GradRow {
+    float gl, gh, H, lse;
+    int t;
+    __device__ __forceinline__ float operator()(float x, int v) const {
+        const float l = x - lse;
+        const float p = __builtin_amdgcn_exp2f(l * kLog2e);
+        // p = 0 below -200: the clamp keeps 0 * -inf (a masked logit) out
+        float d = -p * fmaf(gh, fmaxf(l, -200.0f) + H, gl);
+        return v == t ? d + gl : d;
+    }
+};
+
+template <int DT, int NT>
+__global__ __launch_bounds__(NT) void logprobs_grad_kernel(LpGradArgs a) {
+    typedef typename elem_of<DT>::type E;
+    const int tid = threadIdx.x;
+    const int64_t m = blockIdx.x / a.chunks;
+    const int c = (int)(blockIdx.x - m * a.chunks);
+    const int v0 = min(a.V, c * a.chunk), v1 = min(a.V, v0 + a.chunk);
+    const E* row = (const E*)a.logits + m * (int64_t)a.V;
+    E* out = (E*)a.dlogits + m * (int64_t)a.V;
+    GradRow g;
+    const int64_t t = a.idx64 ? ((const int64_t*)a.targets)[m] : (int64_t)((const int32_t*)a.targets)[m];
+    g.t = t >= 0 && t < a.V ? (int)t : -1;
+    g.gl = g.t >= 0 ? a.g_logprobs[m] : 0.0f;
+    g.gh = a.g_entropy ? a.g_entropy[m] : 0.0f;
+    g.H = a.g_entropy ? a.entropy[m] : 0.0f;
+    g.lse = a.lse[m];
+    if (g.lse == kNegInf) {  // every logit is -inf: p = 0 everywhere
+        g.gl = g.gh = g.H = g.lse = 0.0f;
+    }
+    const Part<DT> p(row, v0, v1);
+    // logits and gradient are stored alike, but may start at different alignments
+    const bool vec_out = (((uintptr_t)(out + v0 + p.head)) & 15) == 0;
+    if (tid < p.head) out[v0 + tid] = f32_elem<DT>(g(elem_f32<DT>(row[v0 + tid]), v0 + tid));
+    for (int j = tid; j < p.nv; j += NT) {
+        float x[kVec<DT>];
+        unpack16<DT>(p.vec(j), x);
+        const int v = v0 + p.head + j * kVec<DT>;
+#pragma unroll
+        for (int i = 0; i < kVec<DT>; ++i) x[i] = g(x[i], v + i);
+        if (vec_out) {
+            u32x4_t o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DT == 2)
+                    o[i] = __float_as_uint(x[i]);
+                else
+                    o[i] = pack2<DT>(x[2 * i], x[2 * i + 1]);
+            }
+            *(u32x4_t*)(out + v) = o;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec<DT>; ++i) out[v + i] = f32_elem<DT>(x[i]);
+        }
+    }
+    const int q = p.tail0() + tid;
+    if (q < v1) out[q] = f32_elem<DT>(g(elem_f32<DT>(row[q]), q));
+}
+
+// Row parts: enough workgroups to fill the chip when there are few rows, but
+// no part under 4096 elements.
+void plan_splits(int64_t M, int64_t V, int* splits, int* chunk) {
+    int64_t s = 1;
+    if (M < 512) s = (1024 + M - 1) / M;
+    const int64_t most = (V + 4095) / 4096;
+    if (s > most) s = most;
+    if (s > kSplitMax) s = kSplitMax;
+    if (s < 1) s = 1;
+    int64_t c = (V + s - 1) / s;
+    c = (c + 63) / 64 * 64;
+    *chunk = (int)c;
+    *splits = (int)((V + c - 1) / c);
+}
+
+}  // namespace
+
+size_t token_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k) {
+    if (M <= 0 || V <= 0) return 0;
+    int splits, chunk;
+    plan_splits(M, V, &splits, &chunk);
+    if (splits <= 1) return 0;
+    return (size_t)M * splits * (16 + 8 * (size_t)k);
+}
+
+hipError_t launch_token_logprobs(const TokenLogprobsArgs& t, int dt, void* ws, hipStream_t s) {
+    LpArgs a;
+    a.logits = t.logits;
+    a.targets = t.targets;
+    a.logprobs = t.logprobs;
+    a.entropy = t.entropy;
+    a.lse = t.lse;
+    a.top_ids = t.top_ids;
+    a.top_lp = t.top_logprobs;
+    a.M = t.M;
+    a.V = (int)t.V;
+    a.k = t.k;
+    a.idx64 = t.idx64;
+    plan_splits(t.M, t.V, &a.splits, &a.chunk);
+    a.part_stat = (float4*)ws;
+    a.part_key = (uint64_t*)((char*)ws + (size_t)t.M * a.splits * 16);
+    log_choice("token_logprobs: %d part(s) of %d a row", a.splits, a.chunk);
+    const dim3 grid((unsigned)(t.M * a.splits));
+    if (dt == 0) logprobs_kernel<0, 256><<<grid, 256, 0, s>>>(a);
+    else if (dt == 1) logprobs_kernel<1, 256><<<grid, 256, 0, s>>>(a);
+    else logprobs_kernel<2, 256><<<grid, 256, 0, s>>>(a);
+    if (a.splits > 1) {
+        const dim3 jg((unsigned)t.M);
+        if (dt == 0) logprobs_join_kernel<0><<<jg, 64, 0, s>>>(a);
+        else if (dt == 1) logprobs_join_kernel<1><<<jg, 64, 0, s>>>(a);
+        else logprobs_join_kernel<2><<<jg, 64, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_token_logprobs_grad(const TokenLogprobsGradArgs& t, int dt, hipStream_t s) {
+    LpGradArgs a;
+    a.logits = t.logits;
+    a.targets = t.targets;
+    a.lse = t.lse;
+    a.entropy = t.entropy;
+    a.g_logprobs = t.g_logprobs;
+    a.g_entropy = t.g_entropy;
+    a.dlogits = t.dlogits;
+    a.M = t.M;
+    a.V = (int)t.V;
+    a.idx64 = t.idx64;
+    a.chunk = 16384;
+    a.chunks = (int)((t.V + a.chunk - 1) / a.chunk);
+    const dim3 grid((unsigned)(t.M * a.chunks));
+    if (dt == 0) logprobs_grad_kernel<0, 256><<<grid, 256, 0, s>>>(a);
+    else if (dt == 1) logprobs_grad_kernel<1, 256><<<grid, 256, 0, s>>>(a);
+    else logprobs_grad_kernel<2, 256><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace omm
