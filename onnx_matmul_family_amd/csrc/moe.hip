@@ -14,6 +14,7 @@
 
 #include "kernels.hpp"
 #include "row_select.hpp"
+#include "stream_core.hpp"
 
 namespace omm {
 
@@ -293,6 +294,202 @@ void layer_any(const LayerArgs& a, hipStream_t s) {
     moe_down_any_kernel<DT><<<gd, 256, 0, s>>>(a);
 }
 
+// ------------------------------------------------------------------ streamed forms (bf16 / fp16)
+constexpr int NWS = 8;  // waves of a workgroup; they split the contraction
+constexpr int kRedFloats = NWS * 8 * kFragPad;
+
+// contraction steps of 32 of one wave: even counts where a 128-byte line of a
+// weight column holds two
+__device__ __forceinline__ void wave_steps(int kn, int trans, int wave, int& s0, int& s1) {
+    const int steps = (kn + 31) / 32;
+    int per = (steps + NWS - 1) / NWS;
+    if (trans) per = (per + 1) & ~1;
+    s0 = min(steps, wave * per);
+    s1 = min(steps, s0 + per);
+}
+
+// h of one expert and 64 columns: 64 gate columns and the 64 up columns beside
+// them are the wave's 8 fragments, so that act(gate) * up needs no other
+// workgroup.  TRANS = 0: lanes 0-7 of 16 load gate, 8-15 up; TRANS = 1:
+// fragments 0-3 are gate, 4-7 up.
+template <int DT, int TRANS, int NG>
+__device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r, int t0, float* red, int tid) {
+    const int lane = tid & 63, wave = tid >> 6, i = lane & 15, q8 = (lane >> 4) * 8;
+    const int F = (int)a.F, K = (int)a.K, c0 = blockIdx.x * 64;
+    const int64_t eoff = (int64_t)r.e * a.K * a.F;
+    const uint16_t* wg = (const uint16_t*)a.wg + eoff;
+    const uint16_t* wu = (const uint16_t*)a.wu + eoff;
+    StreamW<TRANS> w;
+    w.ld = F;
+    if constexpr (TRANS) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w.p[j] = (j < 4 ? wg : wu) + (int64_t)min(c0 + 16 * (j & 3) + i, F - 1) * K + q8;
+    } else {
+        w.p[0] = (i < 8 ? wg : wu) + min(c0 + 8 * (i & 7), F - 8) + (int64_t)q8 * F;
+    }
+    StreamX16<NG> x;  // rows past the last are the last one: their results are not used
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        x.p[g] = (const uint16_t*)a.X + (int64_t)r.tok[min(t0 + 16 * g + i, r.n - 1)] * K + q8;
+    f32x4_t acc[8][NG] = {};
+    int s0, s1;
+    wave_steps(K, TRANS, wave, s0, s1);
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, q8, acc);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        if (g) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *(f32x4_t*)&red[red_index(wave, j, lane, 0)] = acc[j][g];
+        __syncthreads();
+        for (int o = tid; o < 16 * 64; o += 64 * NWS) {
+            const int c = o & 63, row = o >> 6, t = t0 + 16 * g + row;
+            if (t >= r.n || c0 + c >= F) continue;
+            int j, l, rr, j2, l2, rr2;
+            red_pos<TRANS>(c, row, j, l, rr);
+            red_pos<TRANS>(c + 64, row, j2, l2, rr2);
+            float gv = 0.0f, uv = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NWS; ++v) {
+                gv += red[red_index(v, j, l, rr)];
+                uv += red[red_index(v, j2, l2, rr2)];
+            }
+            const int p = r.tok[t] * a.k + r.slot[t];
+            a.h[(int64_t)p * F + c0 + c] = activate(gv, a.act) * uv * r.w[p];
+        }
+    }
+}
+
+template <int DT, int TRANS>
+__global__ __launch_bounds__(64 * NWS) void moe_up_kernel(LayerArgs a) {
+    __shared__ ExpertRows r;
+    __shared__ __attribute__((aligned(16))) float red[kRedFloats];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int m = wave; m < a.M; m += NWS) {
+        int id;
+        float w;
+        route_kind(a.logits_kind, a.logits, m, a.E, a.k, a.renorm, lane, id, w);
+        if (lane < a.k) {
+            r.id[m * a.k + lane] = id;
+            r.w[m * a.k + lane] = w;
+        }
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = tid; i < a.M * a.k; i += 64 * NWS) a.ids[i] = r.id[i];
+    expert_rows<64 * NWS>(r, a.M, a.k, (int)blockIdx.y, tid);
+    if (r.e < 0) return;
+    for (int t0 = 0; t0 < r.n; t0 += 32) {
+        if (t0) __syncthreads();
+        if (r.n - t0 <= 16) up_rows<DT, TRANS, 1>(a, r, t0, red, tid);
+        else up_rows<DT, TRANS, 2>(a, r, t0, red, tid);
+    }
+}
+
+// part of one expert and 128 output columns
+template <int DT, int TRANS, int NG>
+__device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertRows& r, int t0, float* red, int tid) {
+    const int lane = tid & 63, wave = tid >> 6, i = lane & 15, q8 = (lane >> 4) * 8;
+    const int F = (int)a.F, N = (int)a.K, c0 = blockIdx.x * 128;
+    const uint16_t* wd = (const uint16_t*)a.wd + (int64_t)r.e * a.K * a.F;
+    StreamW<TRANS> w;
+    w.ld = N;
+    if constexpr (TRANS) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w.p[j] = wd + (int64_t)min(c0 + 16 * j + i, N - 1) * F + q8;
+    } else {
+        w.p[0] = wd + min(c0 + 8 * i, N - 8) + (int64_t)q8 * N;
+    }
+    int s0, s1;
+    wave_steps(F, TRANS, wave, s0, s1);
+    StreamX32<DT, NG> x;
+    float undo[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int t = min(t0 + 16 * g + i, r.n - 1);
+        x.p[g] = a.h + (int64_t)(r.tok[t] * a.k + r.slot[t]) * F + q8;
+        undo[g] = 1.0f;
+        if constexpr (DT == 1) {  // the row's largest value over this wave's range -> [2^13, 2^14)
+            float mx = 0.0f;
+            for (int s = s0; s < s1; ++s)
+                if (s * 32 + q8 < F)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x.p[g][s * 32 + e]));
+            mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            int ex = 0;
+            if (mx > 0.0f && mx < __builtin_inff()) ex = max(-100, min(100, 14 - ilogbf(mx) - 1));
+            x.scale[g] = ldexpf(1.0f, ex);
+            undo[g] = ldexpf(1.0f, -ex);
+        }
+    }
+    f32x4_t acc[8][NG] = {};
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, F, q8, acc);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        if (g) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (DT == 1) acc[j][g] *= undo[g];
+            *(f32x4_t*)&red[red_index(wave, j, lane, 0)] = acc[j][g];
+        }
+        __syncthreads();
+        for (int o = tid; o < 16 * 128; o += 64 * NWS) {
+            const int c = o & 127, row = o >> 7, t = t0 + 16 * g + row;
+            if (t >= r.n || c0 + c >= N) continue;
+            int j, l, rr;
+            red_pos<TRANS>(c, row, j, l, rr);
+            float v = 0.0f;
+#pragma unroll
+            for (int u = 0; u < NWS; ++u) v += red[red_index(u, j, l, rr)];
+            a.part[(int64_t)(r.tok[t] * a.k + r.slot[t]) * N + c0 + c] = v;
+        }
+    }
+}
+
+template <int DT, int TRANS>
+__global__ __launch_bounds__(64 * NWS) void moe_down_kernel(LayerArgs a) {
+    __shared__ ExpertRows r;
+    __shared__ __attribute__((aligned(16))) float red[kRedFloats];
+    const int tid = threadIdx.x;
+    for (int i = tid; i < a.M * a.k; i += 64 * NWS) r.id[i] = a.ids[i];
+    __syncthreads();
+    expert_rows<64 * NWS>(r, a.M, a.k, (int)blockIdx.y, tid);
+    if (r.e < 0) return;
+    for (int t0 = 0; t0 < r.n; t0 += 32) {
+        if (t0) __syncthreads();
+        if (r.n - t0 <= 16) down_rows<DT, TRANS, 1>(a, r, t0, red, tid);
+        else down_rows<DT, TRANS, 2>(a, r, t0, red, tid);
+    }
+}
+
+// Y[m] = sum over the token's experts, in selection order
+template <int DT>
+__global__ __launch_bounds__(256) void moe_join_kernel(LayerArgs a) {
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= a.K) return;
+    const int64_t m = blockIdx.y;
+    float v = 0.0f;
+    for (int s = 0; s < a.k; ++s) v += a.part[(m * a.k + s) * a.K + n];
+    ((uint16_t*)a.Y)[m * a.K + n] = to_bits<DT>(v);
+}
+
+template <int DT, int TRANS>
+void layer_streamed(const LayerArgs& a, hipStream_t s) {
+    const int pairs = a.M * a.k, jmax = pairs < a.E ? pairs : a.E;
+    const dim3 gu((unsigned)((a.F + 63) / 64), (unsigned)jmax), gd((unsigned)((a.K + 127) / 128), (unsigned)jmax);
+    moe_up_kernel<DT, TRANS><<<gu, 64 * NWS, 0, s>>>(a);
+    moe_down_kernel<DT, TRANS><<<gd, 64 * NWS, 0, s>>>(a);
+    const dim3 gj((unsigned)((a.K + 255) / 256), (unsigned)a.M);
+    moe_join_kernel<DT><<<gj, 256, 0, s>>>(a);
+}
+
+// 16-byte loads of whole 8-element groups, and one expert's matrix within 32-bit byte offsets
+bool streamable(const LayerArgs& a) {
+    const uintptr_t p = (uintptr_t)a.X | (uintptr_t)a.wg | (uintptr_t)a.wu | (uintptr_t)a.wd;
+    return (p & 15) == 0 && a.K % 8 == 0 && a.F % 8 == 0 && a.F > 0 && a.K * a.F < (1LL << 30);
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
@@ -341,6 +538,17 @@ hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void
     a.h = (float*)w;
     w += align256((size_t)l.M * l.k * l.F * 4);
     a.part = (float*)w;
+    if (dt < 2 && streamable(a)) {
+        log_choice("moe_layer: streamed");
+        if (dt == 0) {
+            if (a.trans) layer_streamed<0, 1>(a, s);
+            else layer_streamed<0, 0>(a, s);
+        } else {
+            if (a.trans) layer_streamed<1, 1>(a, s);
+            else layer_streamed<1, 0>(a, s);
+        }
+        return hipGetLastError();
+    }
     log_choice("moe_layer: element-wise");
     if (dt == 0) layer_any<0>(a, s);
     else if (dt == 1) layer_any<1>(a, s);
