@@ -45,7 +45,7 @@ __device__ __forceinline__ void route_token(const typename elem_of<DT>::type* lo
         uint32_t mx = 0;
 #pragma unroll
         for (int i = 0; i < NE; ++i) mx = max(mx, key[i]);
-        mx = wave_max(mx);
+        mx = wave_max_u32(mx);
         if (s == 0) first = mx;
         int e = 0;
 #pragma unroll
@@ -295,11 +295,9 @@ void layer_any(const LayerArgs& a, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------ streamed forms (bf16 / fp16)
-constexpr int NWS = 8;  // waves of a workgroup; they split the contraction
-constexpr int kRedFloats = NWS * 8 * kFragPad;
-
-// contraction steps of 32 of one wave: even counts where a 128-byte line of a
-// weight column holds two
+// contraction steps of 32 of one of a workgroup's NWS waves: even counts where
+// a 128-byte line of a weight column holds two
+template <int NWS>
 __device__ __forceinline__ void wave_steps(int kn, int trans, int wave, int& s0, int& s1) {
     const int steps = (kn + 31) / 32;
     int per = (steps + NWS - 1) / NWS;
@@ -312,21 +310,22 @@ __device__ __forceinline__ void wave_steps(int kn, int trans, int wave, int& s0,
 // them are the wave's 8 fragments, so that act(gate) * up needs no other
 // workgroup.  TRANS = 0: lanes 0-7 of 16 load gate, 8-15 up; TRANS = 1:
 // fragments 0-3 are gate, 4-7 up.
-template <int DT, int TRANS, int NG>
+template <int DT, int TRANS, int NG, int NWS>
 __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r, int t0, float* red, int tid) {
-    const int lane = tid & 63, wave = tid >> 6, i = lane & 15, q8 = (lane >> 4) * 8;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, q8 = (lane >> 4) * 8;
     const int F = (int)a.F, K = (int)a.K, c0 = blockIdx.x * 64;
-    const int64_t eoff = (int64_t)r.e * a.K * a.F;
+    const int64_t eoff = (int64_t)__builtin_amdgcn_readfirstlane(r.e) * a.K * a.F;
     const uint16_t* wg = (const uint16_t*)a.wg + eoff;
     const uint16_t* wu = (const uint16_t*)a.wu + eoff;
     StreamW<TRANS> w;
-    w.ld = F;
     if constexpr (TRANS) {
+        w.base[0] = wg;
+        w.base[1] = wu;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w.p[j] = (j < 4 ? wg : wu) + (int64_t)min(c0 + 16 * (j & 3) + i, F - 1) * K + q8;
+        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * (j & 3) + i, F - 1) * K + q8;
     } else {
-        w.p[0] = (i < 8 ? wg : wu) + min(c0 + 8 * (i & 7), F - 8) + (int64_t)q8 * F;
+        w.ld = F;
+        w.p = (i < 8 ? wg : wu) + min(c0 + 8 * (i & 7), F - 8) + (int64_t)q8 * F;
     }
     StreamX16<NG> x;  // rows past the last are the last one: their results are not used
 #pragma unroll
@@ -334,7 +333,7 @@ __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r,
         x.p[g] = (const uint16_t*)a.X + (int64_t)r.tok[min(t0 + 16 * g + i, r.n - 1)] * K + q8;
     f32x4_t acc[8][NG] = {};
     int s0, s1;
-    wave_steps(K, TRANS, wave, s0, s1);
+    wave_steps<NWS>(K, TRANS, wave, s0, s1);
     stream_run<DT, TRANS, NG>(w, x, s0, s1, K, q8, acc);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -360,10 +359,10 @@ __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r,
     }
 }
 
-template <int DT, int TRANS>
-__global__ __launch_bounds__(64 * NWS) void moe_up_kernel(LayerArgs a) {
+template <int DT, int TRANS, int NG, int NWS>
+__global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_up_kernel(LayerArgs a) {
     __shared__ ExpertRows r;
-    __shared__ __attribute__((aligned(16))) float red[kRedFloats];
+    __shared__ __attribute__((aligned(16))) float red[NWS * 8 * kFragPad];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int m = wave; m < a.M; m += NWS) {
         int id;
@@ -379,29 +378,29 @@ __global__ __launch_bounds__(64 * NWS) void moe_up_kernel(LayerArgs a) {
         for (int i = tid; i < a.M * a.k; i += 64 * NWS) a.ids[i] = r.id[i];
     expert_rows<64 * NWS>(r, a.M, a.k, (int)blockIdx.y, tid);
     if (r.e < 0) return;
-    for (int t0 = 0; t0 < r.n; t0 += 32) {
+    for (int t0 = 0; t0 < r.n; t0 += 16 * NG) {
         if (t0) __syncthreads();
-        if (r.n - t0 <= 16) up_rows<DT, TRANS, 1>(a, r, t0, red, tid);
-        else up_rows<DT, TRANS, 2>(a, r, t0, red, tid);
+        up_rows<DT, TRANS, NG, NWS>(a, r, t0, red, tid);
     }
 }
 
 // part of one expert and 128 output columns
-template <int DT, int TRANS, int NG>
+template <int DT, int TRANS, int NG, int NWS>
 __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertRows& r, int t0, float* red, int tid) {
-    const int lane = tid & 63, wave = tid >> 6, i = lane & 15, q8 = (lane >> 4) * 8;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, q8 = (lane >> 4) * 8;
     const int F = (int)a.F, N = (int)a.K, c0 = blockIdx.x * 128;
-    const uint16_t* wd = (const uint16_t*)a.wd + (int64_t)r.e * a.K * a.F;
+    const uint16_t* wd = (const uint16_t*)a.wd + (int64_t)__builtin_amdgcn_readfirstlane(r.e) * a.K * a.F;
     StreamW<TRANS> w;
-    w.ld = N;
     if constexpr (TRANS) {
+        w.base[0] = w.base[1] = wd;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w.p[j] = wd + (int64_t)min(c0 + 16 * j + i, N - 1) * F + q8;
+        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, N - 1) * F + q8;
     } else {
-        w.p[0] = wd + min(c0 + 8 * i, N - 8) + (int64_t)q8 * N;
+        w.ld = N;
+        w.p = wd + min(c0 + 8 * i, N - 8) + (int64_t)q8 * N;
     }
     int s0, s1;
-    wave_steps(F, TRANS, wave, s0, s1);
+    wave_steps<NWS>(F, TRANS, wave, s0, s1);
     StreamX32<DT, NG> x;
     float undo[NG];
 #pragma unroll
@@ -447,19 +446,18 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertRows& 
     }
 }
 
-template <int DT, int TRANS>
-__global__ __launch_bounds__(64 * NWS) void moe_down_kernel(LayerArgs a) {
+template <int DT, int TRANS, int NG, int NWS>
+__global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_down_kernel(LayerArgs a) {
     __shared__ ExpertRows r;
-    __shared__ __attribute__((aligned(16))) float red[kRedFloats];
+    __shared__ __attribute__((aligned(16))) float red[NWS * 8 * kFragPad];
     const int tid = threadIdx.x;
     for (int i = tid; i < a.M * a.k; i += 64 * NWS) r.id[i] = a.ids[i];
     __syncthreads();
     expert_rows<64 * NWS>(r, a.M, a.k, (int)blockIdx.y, tid);
     if (r.e < 0) return;
-    for (int t0 = 0; t0 < r.n; t0 += 32) {
+    for (int t0 = 0; t0 < r.n; t0 += 16 * NG) {
         if (t0) __syncthreads();
-        if (r.n - t0 <= 16) down_rows<DT, TRANS, 1>(a, r, t0, red, tid);
-        else down_rows<DT, TRANS, 2>(a, r, t0, red, tid);
+        down_rows<DT, TRANS, NG, NWS>(a, r, t0, red, tid);
     }
 }
 
@@ -474,14 +472,28 @@ __global__ __launch_bounds__(256) void moe_join_kernel(LayerArgs a) {
     ((uint16_t*)a.Y)[m * a.K + n] = to_bits<DT>(v);
 }
 
-template <int DT, int TRANS>
-void layer_streamed(const LayerArgs& a, hipStream_t s) {
-    const int pairs = a.M * a.k, jmax = pairs < a.E ? pairs : a.E;
+// NG groups of 16 tokens pass an expert's weights at once; an expert with more
+// tokens reads them again (from the caches).
+template <int DT, int TRANS, int NG, int NWS>
+void layer_streamed(const LayerArgs& a, int jmax, hipStream_t s) {
     const dim3 gu((unsigned)((a.F + 63) / 64), (unsigned)jmax), gd((unsigned)((a.K + 127) / 128), (unsigned)jmax);
-    moe_up_kernel<DT, TRANS><<<gu, 64 * NWS, 0, s>>>(a);
-    moe_down_kernel<DT, TRANS><<<gd, 64 * NWS, 0, s>>>(a);
+    moe_up_kernel<DT, TRANS, NG, NWS><<<gu, 64 * NWS, 0, s>>>(a);
+    moe_down_kernel<DT, TRANS, NG, NWS><<<gd, 64 * NWS, 0, s>>>(a);
     const dim3 gj((unsigned)((a.K + 255) / 256), (unsigned)a.M);
     moe_join_kernel<DT><<<gj, 256, 0, s>>>(a);
+}
+
+template <int DT, int TRANS>
+void layer_pick(const LayerArgs& a, hipStream_t s) {
+    const int pairs = a.M * a.k, jmax = pairs < a.E ? pairs : a.E;
+    // two groups only where an expert has more than 8 tokens on average
+    if (a.M > 16 && pairs > 8 * a.E) {
+        layer_streamed<DT, TRANS, 2, 8>(a, jmax, s);
+    } else if ((a.F + 63) / 64 * jmax <= 512) {
+        layer_streamed<DT, TRANS, 1, 8>(a, jmax, s);
+    } else {
+        layer_streamed<DT, TRANS, 1, 4>(a, jmax, s);
+    }
 }
 
 // 16-byte loads of whole 8-element groups, and one expert's matrix within 32-bit byte offsets
@@ -540,12 +552,11 @@ hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void
     a.part = (float*)w;
     if (dt < 2 && streamable(a)) {
         log_choice("moe_layer: streamed");
-        if (dt == 0) {
-            if (a.trans) layer_streamed<0, 1>(a, s);
-            else layer_streamed<0, 0>(a, s);
-        } else {
-            if (a.trans) layer_streamed<1, 1>(a, s);
-            else layer_streamed<1, 0>(a, s);
+        switch (dt * 2 + a.trans) {
+            case 0: layer_pick<0, 0>(a, s); break;
+            case 1: layer_pick<0, 1>(a, s); break;
+            case 2: layer_pick<1, 0>(a, s); break;
+            default: layer_pick<1, 1>(a, s); break;
         }
         return hipGetLastError();
     }

@@ -74,10 +74,36 @@ __device__ __forceinline__ T wave_max(T v) {
     }
     return v;
 }
+
+// Sum and maximum over a wave with DPP row shifts and broadcasts: six VALU
+// steps, where a shuffle is an LDS round trip each (routing one token through
+// 8 selections: ~0.4 us against ~1.5 us).  All 64 lanes must be active; the
+// result is in every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t old, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = max(v, dpp_u32<0x111, 0xf>(v, v));  // row_shr:1, 2, 4, 8
+    v = max(v, dpp_u32<0x112, 0xf>(v, v));
+    v = max(v, dpp_u32<0x114, 0xf>(v, v));
+    v = max(v, dpp_u32<0x118, 0xf>(v, v));
+    v = max(v, dpp_u32<0x142, 0xa>(v, v));  // row_bcast:15
+    v = max(v, dpp_u32<0x143, 0xc>(v, v));  // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __uint_as_float(dpp_u32<CTRL, ROWS>(0u, __float_as_uint(v)));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
+    v = dpp_add<0x111, 0xf>(v);
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);
+    v = dpp_add<0x143, 0xc>(v);
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
 }  // namespace omm

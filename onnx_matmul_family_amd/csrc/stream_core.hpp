@@ -32,22 +32,27 @@ __device__ __forceinline__ f32x4_t mfma16x16x32(u32x4_t a, u32x4_t b, f32x4_t c)
                                                       __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
-// One lane's weights.  p[j] (TRANS = 1: the lane's column of fragment j;
-// TRANS = 0: p[0] only, the lane's 8 columns) already includes the lane's
-// contraction offset 8 (l / 16); ld is the row stride (TRANS = 0).
+// One lane's weights.  TRANS = 1: off[j], elements from base[j / 4] to the
+// lane's column of fragment j; TRANS = 0: p, the lane's 8 columns, and ld, the
+// row stride.  Both include the lane's contraction offset 8 (l / 16).  Bases,
+// ld and kb are uniform over the wave (scalar registers).
 template <int TRANS>
 struct StreamW {
-    const uint16_t* p[TRANS ? 8 : 1];
+    const uint16_t* base[2];
+    uint32_t off[8];
+    __device__ __forceinline__ void load(u32x4_t (&w)[8], int kb) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = *(const u32x4_t*)(base[j >> 2] + kb + off[j]);
+    }
+};
+template <>
+struct StreamW<0> {
+    const uint16_t* p;
     int64_t ld;
     __device__ __forceinline__ void load(u32x4_t (&w)[8], int kb) const {
-        if constexpr (TRANS) {
+        const uint16_t* q = p + (int64_t)kb * ld;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = *(const u32x4_t*)(p[j] + kb);
-        } else {
-            const uint16_t* q = p[0] + (int64_t)kb * ld;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) w[t] = *(const u32x4_t*)(q + t * ld);
-        }
+        for (int t = 0; t < 8; ++t) w[t] = *(const u32x4_t*)(q + t * ld);
     }
 };
 
