@@ -136,9 +136,10 @@ struct LayerArgs {
     void* Y;               // (M, K)
     int32_t* ids;          // workspace: (M, k) selections
     float* h;              // workspace: (M k, F), weighted
-    float* part;           // workspace: (M k, K)
+    float* part;           // workspace: (splits, M k, K)
+    uint32_t* done;        // workspace: finished workgroups of each 128 output columns
     int64_t K, F;
-    int M, E, k, renorm, act, trans, logits_kind;
+    int M, E, k, renorm, act, trans, logits_kind, splits;
 };
 
 __device__ __forceinline__ float activate(float g, int act) {
@@ -298,11 +299,12 @@ void layer_any(const LayerArgs& a, hipStream_t s) {
 // contraction steps of 32 of one of a workgroup's NWS waves: even counts where
 // a 128-byte line of a weight column holds two
 template <int NWS>
-__device__ __forceinline__ void wave_steps(int kn, int trans, int wave, int& s0, int& s1) {
-    const int steps = (kn + 31) / 32;
-    int per = (steps + NWS - 1) / NWS;
+__device__ __forceinline__ void wave_steps(int kn, int trans, int wave, int& s0, int& s1, int splits = 1,
+                                           int split = 0) {
+    const int steps = (kn + 31) / 32, n = NWS * splits;
+    int per = (steps + n - 1) / n;
     if (trans) per = (per + 1) & ~1;
-    s0 = min(steps, wave * per);
+    s0 = min(steps, (split * NWS + wave) * per);
     s1 = min(steps, s0 + per);
 }
 
@@ -374,8 +376,10 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_up_kernel(Laye
         }
     }
     __syncthreads();
-    if (blockIdx.x == 0 && blockIdx.y == 0)
+    if (blockIdx.x == 0 && blockIdx.y == 0) {  // for the second kernel
         for (int i = tid; i < a.M * a.k; i += 64 * NWS) a.ids[i] = r.id[i];
+        for (int i = tid; i < (a.K + 127) / 128; i += 64 * NWS) a.done[i] = 0;
+    }
     expert_rows<64 * NWS>(r, a.M, a.k, (int)blockIdx.y, tid);
     if (r.e < 0) return;
     for (int t0 = 0; t0 < r.n; t0 += 16 * NG) {
@@ -400,7 +404,8 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertRows& 
         w.p = wd + min(c0 + 8 * i, N - 8) + (int64_t)q8 * N;
     }
     int s0, s1;
-    wave_steps<NWS>(F, TRANS, wave, s0, s1);
+    const int sp = blockIdx.z;
+    wave_steps<NWS>(F, TRANS, wave, s0, s1, a.splits, sp);
     StreamX32<DT, NG> x;
     float undo[NG];
 #pragma unroll
@@ -441,7 +446,9 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertRows& 
             float v = 0.0f;
 #pragma unroll
             for (int u = 0; u < NWS; ++u) v += red[red_index(u, j, l, rr)];
-            a.part[(int64_t)(r.tok[t] * a.k + r.slot[t]) * N + c0 + c] = v;
+            // written past this XCD's L2: another one's workgroup may sum them
+            __hip_atomic_store(&a.part[((int64_t)sp * a.M * a.k + r.tok[t] * a.k + r.slot[t]) * N + c0 + c], v,
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
     }
 }
@@ -459,28 +466,58 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_down_kernel(La
         if (t0) __syncthreads();
         down_rows<DT, TRANS, NG, NWS>(a, r, t0, red, tid);
     }
-}
-
-// Y[m] = sum over the token's experts, in selection order
-template <int DT>
-__global__ __launch_bounds__(256) void moe_join_kernel(LayerArgs a) {
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.K) return;
-    const int64_t m = blockIdx.y;
-    float v = 0.0f;
-    for (int s = 0; s < a.k; ++s) v += a.part[(m * a.k + s) * a.K + n];
-    ((uint16_t*)a.Y)[m * a.K + n] = to_bits<DT>(v);
+    // The last workgroup of these 128 columns sums the experts: every wave's
+    // stores have reached memory before the workgroup is counted, and the
+    // count was zeroed by the first kernel.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    __shared__ int last;
+    if (tid == 0)
+        last = __hip_atomic_fetch_add(&a.done[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               (uint32_t)(r.active * a.splits - 1);
+    __syncthreads();
+    if (!last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    const int64_t pairs = (int64_t)a.M * a.k;
+    for (int o = tid; o < a.M * 32; o += 64 * NWS) {
+        const int m = o >> 5, n = blockIdx.x * 128 + (o & 31) * 4;
+        if (n >= a.K) continue;
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int sp = 0; sp < a.splits; ++sp) {
+            const float* q = a.part + (sp * pairs + (int64_t)m * a.k) * a.K + n;
+            // (kMaxTop at most; unrolled so that the loads of four go out together)
+            for (int s0 = 0; s0 < a.k; s0 += 4) {
+                f32x4_t u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[i] = *(const f32x4_t*)(q + (int64_t)min(s0 + i, a.k - 1) * a.K);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (s0 + i < a.k) v += u[i];
+            }
+        }
+        const u32x2_t y = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+        *(u32x2_t*)((uint16_t*)a.Y + (int64_t)m * a.K + n) = y;
+    }
 }
 
 // NG groups of 16 tokens pass an expert's weights at once; an expert with more
 // tokens reads them again (from the caches).
 template <int DT, int TRANS, int NG, int NWS>
 void layer_streamed(const LayerArgs& a, int jmax, hipStream_t s) {
-    const dim3 gu((unsigned)((a.F + 63) / 64), (unsigned)jmax), gd((unsigned)((a.K + 127) / 128), (unsigned)jmax);
+    const dim3 gu((unsigned)((a.F + 63) / 64), (unsigned)jmax);
+    const dim3 gd((unsigned)((a.K + 127) / 128), (unsigned)jmax, (unsigned)a.splits);
     moe_up_kernel<DT, TRANS, NG, NWS><<<gu, 64 * NWS, 0, s>>>(a);
     moe_down_kernel<DT, TRANS, NG, NWS><<<gd, 64 * NWS, 0, s>>>(a);
-    const dim3 gj((unsigned)((a.K + 255) / 256), (unsigned)a.M);
-    moe_join_kernel<DT><<<gj, 256, 0, s>>>(a);
+}
+
+// Workgroups that share one expert's 128 output columns by splitting F: as many
+// as fill the chip, each wave with two steps of 32 or more.
+int down_splits(int64_t M, int64_t K, int64_t F, int64_t E, int64_t k) {
+    const int64_t jmax = M * k < E ? M * k : E, groups = (K + 127) / 128 * jmax;
+    int64_t s = (256 + groups - 1) / groups;
+    if (s > F / 512) s = F / 512;
+    if (s > 4) s = 4;
+    return s < 1 ? 1 : (int)s;
 }
 
 template <int DT, int TRANS>
@@ -499,7 +536,7 @@ void layer_pick(const LayerArgs& a, hipStream_t s) {
 // 16-byte loads of whole 8-element groups, and one expert's matrix within 32-bit byte offsets
 bool streamable(const LayerArgs& a) {
     const uintptr_t p = (uintptr_t)a.X | (uintptr_t)a.wg | (uintptr_t)a.wu | (uintptr_t)a.wd;
-    return (p & 15) == 0 && a.K % 8 == 0 && a.F % 8 == 0 && a.F > 0 && a.K * a.F < (1LL << 30);
+    return (p & 15) == 0 && ((uintptr_t)a.Y & 7) == 0 && a.K % 8 == 0 && a.F % 8 == 0 && a.F > 0 && a.K * a.F < (1LL << 30);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -523,8 +560,8 @@ hipError_t launch_moe_route(const MoeRouteArgs& r, int dt, hipStream_t s) {
 }
 
 size_t moe_layer_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t k) {
-    (void)E;
-    return align256((size_t)M * k * 4) + align256((size_t)M * k * F * 4) + align256((size_t)M * k * K * 4);
+    return align256((size_t)M * k * 4) + align256((size_t)M * k * F * 4) +
+           align256((size_t)M * k * K * 4 * down_splits(M, K, F, E, k)) + align256((size_t)(K + 127) / 128 * 4);
 }
 
 hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void* ws, hipStream_t s) {
@@ -550,6 +587,9 @@ hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void
     a.h = (float*)w;
     w += align256((size_t)l.M * l.k * l.F * 4);
     a.part = (float*)w;
+    a.splits = down_splits(l.M, l.K, l.F, l.E, l.k);
+    w += align256((size_t)l.M * l.k * l.K * 4 * a.splits);
+    a.done = (uint32_t*)w;
     if (dt < 2 && streamable(a)) {
         log_choice("moe_layer: streamed");
         switch (dt * 2 + a.trans) {
