@@ -28,17 +28,21 @@ constexpr int kMaxTok = 64;   // tokens of a layer call: one lane each
 // One wave, one token.  Lane l holds the logits of experts l, l + 64, ...
 // k rounds of "largest key, lowest index".  Lane s < k returns selection s.
 template <int DT, int NE>
-__device__ __forceinline__ void route_token(const typename elem_of<DT>::type* logits, int E, int k, int renorm,
-                                            int lane, int& id, float& w) {
-    uint32_t key[NE];
-    float x[NE];
-    uint32_t top = 0;
+__device__ __forceinline__ void load_logits(const typename elem_of<DT>::type* logits, int E, int lane,
+                                            float (&x)[NE]) {
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = i * 64 + lane;
         x[i] = e < E ? elem_f32<DT>(logits[e]) : -__builtin_inff();
-        key[i] = e < E ? order_key(x[i]) : 0;
     }
+}
+template <int NE>
+__device__ __forceinline__ void route_token(const float (&x)[NE], int E, int k, int renorm, int lane, int& id,
+                                            float& w) {
+    uint32_t key[NE];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) key[i] = i * 64 + lane < E ? order_key(x[i]) : 0;
     uint32_t first = 0;
     id = 0;
     for (int s = 0; s < k; ++s) {
@@ -77,23 +81,6 @@ __device__ __forceinline__ void route_token(const typename elem_of<DT>::type* lo
     w = none ? 0.0f : p / sum;
 }
 
-template <int DT>
-__device__ __forceinline__ void route_any(const void* logits, int64_t m, int E, int k, int renorm, int lane, int& id,
-                                          float& w) {
-    const typename elem_of<DT>::type* row = (const typename elem_of<DT>::type*)logits + m * (int64_t)E;
-    if (E <= 64) route_token<DT, 1>(row, E, k, renorm, lane, id, w);
-    else if (E <= 128) route_token<DT, 2>(row, E, k, renorm, lane, id, w);
-    else if (E <= 256) route_token<DT, 4>(row, E, k, renorm, lane, id, w);
-    else route_token<DT, 8>(row, E, k, renorm, lane, id, w);
-}
-
-__device__ __forceinline__ void route_kind(int kind, const void* logits, int64_t m, int E, int k, int renorm, int lane,
-                                           int& id, float& w) {
-    if (kind == 0) route_any<0>(logits, m, E, k, renorm, lane, id, w);
-    else if (kind == 1) route_any<1>(logits, m, E, k, renorm, lane, id, w);
-    else route_any<2>(logits, m, E, k, renorm, lane, id, w);
-}
-
 struct RouteArgs {
     const void* logits;
     void* ids;
@@ -109,7 +96,9 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     if (m >= a.M) return;
     int id;
     float w;
-    route_token<DT, NE>((const typename elem_of<DT>::type*)a.logits + m * a.E, a.E, a.k, a.renorm, lane, id, w);
+    float x[NE];
+    load_logits<DT, NE>((const typename elem_of<DT>::type*)a.logits + m * a.E, a.E, lane, x);
+    route_token<NE>(x, a.E, a.k, a.renorm, lane, id, w);
     if (lane < a.k) {
         if (a.ids64) ((int64_t*)a.ids)[m * a.k + lane] = id;
         else ((int32_t*)a.ids)[m * a.k + lane] = id;
@@ -127,6 +116,13 @@ void route_launch(const RouteArgs& a, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------ layer
+// The (token, selection) pairs of one expert in use, as the first kernel
+// leaves them to the second
+struct ExpertList {
+    int32_t e, n, active, unused;
+    int32_t pair[kMaxTok];
+};
+
 struct LayerArgs {
     const void* X;         // (M, K)
     const void* logits;    // (M, E)
@@ -134,7 +130,9 @@ struct LayerArgs {
     const void* wu;
     const void* wd;        // trans 0: (E, F, K), 1: (E, K, F)
     void* Y;               // (M, K)
-    int32_t* ids;          // workspace: (M, k) selections
+    int32_t* ids;          // workspace: (M, k) selections (element-wise form)
+    ExpertList* lists;     // workspace: (min(E, M k)) (streamed form)
+    float* hmax;           // workspace: (M k, ceil(F / 64)) largest |h| (fp16)
     float* h;              // workspace: (M k, F), weighted
     float* part;           // workspace: (splits, M k, K)
     uint32_t* done;        // workspace: finished workgroups of each 128 output columns
@@ -155,6 +153,41 @@ struct ExpertRows {
     int32_t tok[kMaxTok], slot[kMaxTok];
     int e, n, active;
 };
+
+// Routes the call's tokens, NW waves taking one each in turn; a wave's next
+// logits are on their way while it ranks the present ones.
+template <int DT, int NE, int NW>
+__device__ __forceinline__ void route_tokens(const LayerArgs& a, ExpertRows& r, int lane, int wave) {
+    const typename elem_of<DT>::type* logits = (const typename elem_of<DT>::type*)a.logits;
+    float x[NE], nx[NE] = {};
+    if (wave < a.M) load_logits<DT, NE>(logits + wave * a.E, a.E, lane, x);
+    for (int m = wave; m < a.M; m += NW) {
+        if (m + NW < a.M) load_logits<DT, NE>(logits + (m + NW) * a.E, a.E, lane, nx);
+        int id;
+        float w;
+        route_token<NE>(x, a.E, a.k, a.renorm, lane, id, w);
+        if (lane < a.k) {
+            r.id[m * a.k + lane] = id;
+            r.w[m * a.k + lane] = w;
+        }
+#pragma unroll
+        for (int i = 0; i < NE; ++i) x[i] = nx[i];
+    }
+}
+template <int DT, int NW>
+__device__ __forceinline__ void route_tokens(const LayerArgs& a, ExpertRows& r, int lane, int wave) {
+    if (a.E <= 64) route_tokens<DT, 1, NW>(a, r, lane, wave);
+    else if (a.E <= 128) route_tokens<DT, 2, NW>(a, r, lane, wave);
+    else if (a.E <= 256) route_tokens<DT, 4, NW>(a, r, lane, wave);
+    else route_tokens<DT, 8, NW>(a, r, lane, wave);
+}
+// (the logits may be of another type than the weights)
+template <int NW>
+__device__ __forceinline__ void route_all(const LayerArgs& a, ExpertRows& r, int lane, int wave) {
+    if (a.logits_kind == 0) route_tokens<0, NW>(a, r, lane, wave);
+    else if (a.logits_kind == 1) route_tokens<1, NW>(a, r, lane, wave);
+    else route_tokens<2, NW>(a, r, lane, wave);
+}
 
 // From r.id (and a __syncthreads after it was written) to the rows of the j-th
 // expert in use: r.e (-1: fewer experts in use), r.tok / r.slot / r.n.  All
@@ -210,15 +243,7 @@ __global__ __launch_bounds__(256) void moe_up_any_kernel(LayerArgs a) {
     __shared__ ExpertRows r;
     __shared__ float red[4][2][8][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int m = wave; m < a.M; m += 4) {
-        int id;
-        float w;
-        route_kind(a.logits_kind, a.logits, m, a.E, a.k, a.renorm, lane, id, w);
-        if (lane < a.k) {
-            r.id[m * a.k + lane] = id;
-            r.w[m * a.k + lane] = w;
-        }
-    }
+    route_all<4>(a, r, lane, wave);
     __syncthreads();
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int i = tid; i < a.M * a.k; i += 256) a.ids[i] = r.id[i];
@@ -345,7 +370,7 @@ __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r,
         __syncthreads();
         for (int o = tid; o < 16 * 64; o += 64 * NWS) {
             const int c = o & 63, row = o >> 6, t = t0 + 16 * g + row;
-            if (t >= r.n || c0 + c >= F) continue;
+            if (t >= r.n) continue;  // a wave has one row
             int j, l, rr, j2, l2, rr2;
             red_pos<TRANS>(c, row, j, l, rr);
             red_pos<TRANS>(c + 64, row, j2, l2, rr2);
@@ -356,7 +381,12 @@ __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r,
                 uv += red[red_index(v, j2, l2, rr2)];
             }
             const int p = r.tok[t] * a.k + r.slot[t];
-            a.h[(int64_t)p * F + c0 + c] = activate(gv, a.act) * uv * r.w[p];
+            const float h = c0 + c < F ? activate(gv, a.act) * uv * r.w[p] : 0.0f;
+            if (c0 + c < F) a.h[(int64_t)p * F + c0 + c] = h;
+            if constexpr (DT == 1) {
+                const uint32_t mx = wave_max_u32(__float_as_uint(fabsf(h)));
+                if (c == 0) a.hmax[(int64_t)p * gridDim.x + blockIdx.x] = __uint_as_float(mx);
+            }
         }
     }
 }
@@ -366,21 +396,20 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_up_kernel(Laye
     __shared__ ExpertRows r;
     __shared__ __attribute__((aligned(16))) float red[NWS * 8 * kFragPad];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int m = wave; m < a.M; m += NWS) {
-        int id;
-        float w;
-        route_kind(a.logits_kind, a.logits, m, a.E, a.k, a.renorm, lane, id, w);
-        if (lane < a.k) {
-            r.id[m * a.k + lane] = id;
-            r.w[m * a.k + lane] = w;
+    route_all<NWS>(a, r, lane, wave);
+    __syncthreads();
+    if (blockIdx.x == 0 && blockIdx.y == 0)  // for the second kernel, as the list below
+        for (int i = tid; i < (a.K + 127) / 128; i += 64 * NWS) a.done[i] = 0;
+    expert_rows<64 * NWS>(r, a.M, a.k, (int)blockIdx.y, tid);
+    if (blockIdx.x == 0 && tid < 64) {
+        ExpertList& l = a.lists[blockIdx.y];
+        if (tid < r.n) l.pair[tid] = r.tok[tid] * a.k + r.slot[tid];
+        if (tid == 0) {
+            l.e = r.e;
+            l.n = r.n;
+            l.active = r.active;
         }
     }
-    __syncthreads();
-    if (blockIdx.x == 0 && blockIdx.y == 0) {  // for the second kernel
-        for (int i = tid; i < a.M * a.k; i += 64 * NWS) a.ids[i] = r.id[i];
-        for (int i = tid; i < (a.K + 127) / 128; i += 64 * NWS) a.done[i] = 0;
-    }
-    expert_rows<64 * NWS>(r, a.M, a.k, (int)blockIdx.y, tid);
     if (r.e < 0) return;
     for (int t0 = 0; t0 < r.n; t0 += 16 * NG) {
         if (t0) __syncthreads();
@@ -390,7 +419,7 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_up_kernel(Laye
 
 // part of one expert and 128 output columns
 template <int DT, int TRANS, int NG, int NWS>
-__device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertRows& r, int t0, float* red, int tid) {
+__device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& r, int t0, float* red, int tid) {
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, q8 = (lane >> 4) * 8;
     const int F = (int)a.F, N = (int)a.K, c0 = blockIdx.x * 128;
     const uint16_t* wd = (const uint16_t*)a.wd + (int64_t)__builtin_amdgcn_readfirstlane(r.e) * a.K * a.F;
@@ -410,19 +439,15 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertRows& 
     float undo[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const int t = min(t0 + 16 * g + i, r.n - 1);
-        x.p[g] = a.h + (int64_t)(r.tok[t] * a.k + r.slot[t]) * F + q8;
+        const int p = r.pair[min(t0 + 16 * g + i, r.n - 1)];
+        x.p[g] = a.h + (int64_t)p * F + q8;
         undo[g] = 1.0f;
         if constexpr (DT == 1) {  // the row's largest value over this wave's range -> [2^13, 2^14)
+            const int slabs = (F + 63) / 64;
             float mx = 0.0f;
-            for (int s = s0; s < s1; ++s)
-                if (s * 32 + q8 < F)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x.p[g][s * 32 + e]));
-            mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            for (int b = s0 >> 1; b < (s1 + 1) >> 1; ++b) mx = fmaxf(mx, a.hmax[(int64_t)p * slabs + b]);
             int ex = 0;
-            if (mx > 0.0f && mx < __builtin_inff()) ex = max(-100, min(100, 14 - ilogbf(mx) - 1));
+            if (mx > 0.0f && mx < __builtin_inff()) ex = max(-100, min(100, 13 - ilogbf(mx)));
             x.scale[g] = ldexpf(1.0f, ex);
             undo[g] = ldexpf(1.0f, -ex);
         }
@@ -447,7 +472,7 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertRows& 
 #pragma unroll
             for (int u = 0; u < NWS; ++u) v += red[red_index(u, j, l, rr)];
             // written past this XCD's L2: another one's workgroup may sum them
-            __hip_atomic_store(&a.part[((int64_t)sp * a.M * a.k + r.tok[t] * a.k + r.slot[t]) * N + c0 + c], v,
+            __hip_atomic_store(&a.part[((int64_t)sp * a.M * a.k + r.pair[t]) * N + c0 + c], v,
                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
     }
@@ -455,12 +480,11 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertRows& 
 
 template <int DT, int TRANS, int NG, int NWS>
 __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_down_kernel(LayerArgs a) {
-    __shared__ ExpertRows r;
+    __shared__ ExpertList r;
     __shared__ __attribute__((aligned(16))) float red[NWS * 8 * kFragPad];
     const int tid = threadIdx.x;
-    for (int i = tid; i < a.M * a.k; i += 64 * NWS) r.id[i] = a.ids[i];
+    if (tid < (int)(sizeof(ExpertList) / 4)) ((int32_t*)&r)[tid] = ((const int32_t*)&a.lists[blockIdx.y])[tid];
     __syncthreads();
-    expert_rows<64 * NWS>(r, a.M, a.k, (int)blockIdx.y, tid);
     if (r.e < 0) return;
     for (int t0 = 0; t0 < r.n; t0 += 16 * NG) {
         if (t0) __syncthreads();
@@ -515,7 +539,7 @@ void layer_streamed(const LayerArgs& a, int jmax, hipStream_t s) {
 int down_splits(int64_t M, int64_t K, int64_t F, int64_t E, int64_t k) {
     const int64_t jmax = M * k < E ? M * k : E, groups = (K + 127) / 128 * jmax;
     int64_t s = (256 + groups - 1) / groups;
-    if (s > F / 512) s = F / 512;
+    if (s > F / 256) s = F / 256;
     if (s > 4) s = 4;
     return s < 1 ? 1 : (int)s;
 }
@@ -560,8 +584,10 @@ hipError_t launch_moe_route(const MoeRouteArgs& r, int dt, hipStream_t s) {
 }
 
 size_t moe_layer_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t k) {
+    const size_t jmax = (size_t)(M * k < E ? M * k : E);
     return align256((size_t)M * k * 4) + align256((size_t)M * k * F * 4) +
-           align256((size_t)M * k * K * 4 * down_splits(M, K, F, E, k)) + align256((size_t)(K + 127) / 128 * 4);
+           align256((size_t)M * k * K * 4 * down_splits(M, K, F, E, k)) + align256((size_t)(K + 127) / 128 * 4) + align256(jmax * sizeof(ExpertList)) +
+           align256((size_t)M * k * ((F + 63) / 64) * 4);
 }
 
 hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void* ws, hipStream_t s) {
@@ -590,6 +616,10 @@ hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void
     a.splits = down_splits(l.M, l.K, l.F, l.E, l.k);
     w += align256((size_t)l.M * l.k * l.K * 4 * a.splits);
     a.done = (uint32_t*)w;
+    w += align256((size_t)(l.K + 127) / 128 * 4);
+    a.lists = (ExpertList*)w;
+    w += align256((size_t)(l.M * l.k < l.E ? l.M * l.k : l.E) * sizeof(ExpertList));
+    a.hmax = (float*)w;
     if (dt < 2 && streamable(a)) {
         log_choice("moe_layer: streamed");
         switch (dt * 2 + a.trans) {
