@@ -6,6 +6,7 @@
 
 #include "kernels.hpp"
 #include "row_select.hpp"
+#include "stream_core.hpp"
 
 namespace omm {
 
@@ -20,8 +21,12 @@ struct LoraK {
     const void* bias;    // (N) or nullptr
     float* T;            // workspace: (M, R), scaled
     void* D;             // workspace: (M, N)
+    const void* W;       // streamed form: as the caller's
+    void* Y;
+    float* part;         // workspace: (splits, M, N)
+    uint32_t* done;      // workspace: finished workgroups of each 128 columns
     int64_t M, K, N, G;
-    int R, trans, idx64;
+    int R, trans, idx64, splits;
 };
 
 __device__ __forceinline__ int64_t row_adapter(const LoraK& a, int64_t m) {
@@ -64,12 +69,239 @@ __global__ __launch_bounds__(256) void lora_delta_any_kernel(LoraK a, int64_t nb
     ((E*)a.D)[m * a.N + n] = f32_elem<DT>(acc);
 }
 
+// ------------------------------------------------------------------ few rows (at most 64)
+// T[m, r] = scale[g] sum_k X[m, k] A[g, k, r], one workgroup a row (or a part of
+// its r): the rows of a decode batch have adapters of their own, so A is read
+// once a row whatever the tiling, on the vector ALU.
+//   TRANS = 1: a wave an r, 16 bytes of k a lane.
+//   TRANS = 0: a thread takes V columns of every (1024 / tpr)-th k (tpr threads
+//     a row of R, a power of two); sums over k by shuffles, then LDS.
+// It also zeroes the counters of the kernel that follows it.
+template <int DT, int TRANS, int V>
+__global__ __launch_bounds__(TRANS ? 256 : 1024) void lora_shrink_kernel(LoraK a, int tpr) {
+    typedef typename elem_of<DT>::type E;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t m = blockIdx.y;
+    if (m == 0 && blockIdx.x == 0)
+        for (int64_t i = tid; i < (a.N + 127) / 128; i += blockDim.x) a.done[i] = 0;
+    const int64_t g = row_adapter(a, m);
+    if (g < 0 || a.R == 0) return;
+    const E* x = (const E*)a.X + m * a.K;
+    const float scale = a.scale ? a.scale[g] : 1.0f;
+    const int K = (int)a.K;
+    if constexpr (TRANS) {
+        const int r = blockIdx.x * 4 + wave;
+        if (r >= a.R) return;
+        const E* w = (const E*)a.A + (g * a.R + r) * a.K;
+        float acc = 0.0f;
+        const int kv = K / V;
+#pragma unroll 4
+        for (int c = lane; c < kv; c += 64) {
+            float xv[V], wv[V];
+            unpack16<DT>(load16(x + c * V), xv);
+            unpack16<DT>(load16(w + c * V), wv);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc = fmaf(xv[i], wv[i], acc);
+        }
+        const int k = kv * V + lane;
+        if (k < K) acc = fmaf(elem_f32<DT>(x[k]), elem_f32<DT>(w[k]), acc);
+        acc = wave_sum(acc);
+        if (lane == 0) a.T[m * a.R + r] = acc * scale;
+    } else {
+        __shared__ float red[16][64][V];
+        const int rb = tid & (tpr - 1), kk = tid / tpr, kn = 1024 / tpr;
+        const int start = min(rb * V, a.R - V);  // the last group may overlap the one before
+        const bool mine = rb * V < a.R;
+        float acc[V] = {};
+        if (mine) {
+            const E* w = (const E*)a.A + g * a.K * a.R + start;
+#pragma unroll 4
+            for (int k = kk; k < K; k += kn) {
+                const float xv = elem_f32<DT>(x[k]);
+                float wv[V];
+                if constexpr (V == 1)
+                    wv[0] = elem_f32<DT>(w[(int64_t)k * a.R]);
+                else
+                    unpack16<DT>(load16(w + (int64_t)k * a.R), wv);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(xv, wv[i], acc[i]);
+            }
+        }
+        for (int d = tpr; d < 64; d <<= 1)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += __shfl_xor(acc[i], d, 64);
+        if (lane < tpr)
+#pragma unroll
+            for (int i = 0; i < V; ++i) red[wave][lane][i] = acc[i];
+        __syncthreads();
+        if (tid < a.R) {
+            const int b = tid / V, i = tid - min(b * V, a.R - V);
+            float v = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) v += red[u][b][i];
+            a.T[m * a.R + tid] = v * scale;
+        }
+    }
+}
+
+// sum_r T[m, r] B[g, r, n] of a row with adapter g
+template <int DT, int TRANS>
+__device__ __forceinline__ float lora_expand(const LoraK& a, const float* t, int64_t g, int64_t n) {
+    typedef typename elem_of<DT>::type E;
+    constexpr int V = kQ<DT>;
+    float acc = 0.0f;
+    const int rv = a.R / V * V;
+    const E* b = (const E*)a.B + g * a.R * a.N + (TRANS ? n * a.R : n);
+    for (int r = 0; r < rv; r += V) {
+        float bv[V];
+        if constexpr (TRANS) {
+            unpack16<DT>(load16(b + r), bv);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) bv[i] = elem_f32<DT>(b[(int64_t)(r + i) * a.N]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc = fmaf(t[r + i], bv[i], acc);
+    }
+    for (int r = rv; r < a.R; ++r) acc = fmaf(t[r], elem_f32<DT>(b[TRANS ? r : (int64_t)r * a.N]), acc);
+    return acc;
+}
+
+// Y of 128 columns: X W streamed (8 waves split the workgroup's part of K),
+// the adapters' share of the rows m = split mod splits, and, in the last
+// workgroup of the columns to finish, the sum over the parts.
+template <int DT, int TRANS, int NG>
+__global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
+    typedef typename elem_of<DT>::type E;
+    __shared__ __attribute__((aligned(16))) float red[8 * 8 * kFragPad];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
+    const int q = (lane >> 4) * kQ<DT>, sp = blockIdx.y;
+    const int M = (int)a.M, K = (int)a.K, N = (int)a.N, c0 = blockIdx.x * 128;
+    StreamW<DT, TRANS> w;
+    const E* wp = (const E*)a.W;
+    if constexpr (TRANS) {
+        w.base[0] = w.base[1] = wp;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, N - 1) * K + q;
+    } else {
+        w.ld = N;
+        if constexpr (DT == 2) {
+            w.p[0] = wp + group_start<DT>(c0, 4 * i, N) + (int64_t)q * N;
+            w.p[1] = wp + group_start<DT>(c0, 64 + 4 * i, N) + (int64_t)q * N;
+        } else {
+            w.p[0] = wp + group_start<DT>(c0, 8 * i, N) + (int64_t)q * N;
+        }
+    }
+    StreamX<DT, NG> x;  // rows past the last are the last one: their results are not used
+#pragma unroll
+    for (int g = 0; g < NG; ++g) x.p[g] = (const E*)a.X + (int64_t)min(16 * g + i, M - 1) * K + q;
+    f32x4_t acc[8][NG] = {};
+    int s0, s1;
+    wave_steps<DT, 8>(K, TRANS, wave, s0, s1, a.splits, sp);
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, q, acc);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        if (g) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *(f32x4_t*)&red[red_index(wave, j, lane, 0)] = acc[j][g];
+        __syncthreads();
+        for (int o = tid; o < 16 * 128; o += 512) {
+            const int c = o & 127, row = __builtin_amdgcn_readfirstlane(o >> 7), m = 16 * g + row;  // a wave has one row
+            const int n = c0 + c;
+            if (m >= M || n >= N) continue;
+            int j, l, rr;
+            red_pos<DT, TRANS>(c, c0 + (c & ~(kQ<DT> - 1)) - group_start<DT>(c0, c, N), row, j, l, rr);
+            float v = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += red[red_index(u, j, l, rr)];
+            if (m % a.splits == sp) {
+                const int64_t ad = row_adapter(a, m);
+                if (ad >= 0) v += lora_expand<DT, TRANS>(a, a.T + m * a.R, ad, n);
+            }
+            if (a.splits == 1) {
+                if (a.bias) v += elem_f32<DT>(((const E*)a.bias)[n]);
+                ((E*)a.Y)[(int64_t)m * N + n] = f32_elem<DT>(v);
+            } else {
+                // written past this XCD's L2: another one's workgroup may sum them
+                __hip_atomic_store(&a.part[((int64_t)sp * M + m) * N + n], v, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+    }
+    if (a.splits == 1) return;
+    // every wave's stores have reached memory before the workgroup is counted
+    // (the kernel before this one zeroed the count)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    __shared__ int last;
+    if (tid == 0)
+        last = __hip_atomic_fetch_add(&a.done[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               (uint32_t)(a.splits - 1);
+    __syncthreads();
+    if (!last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    for (int o = tid; o < M * 32; o += 512) {
+        const int m = o >> 5;
+        if (c0 + (o & 31) * 4 >= N) continue;
+        const int n = min(c0 + (o & 31) * 4, N - 4);  // whole loads, as N >= 4; the last group may overlap
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float* p = a.part + (int64_t)m * N + n;
+#pragma unroll 4
+        for (int u = 0; u < a.splits; ++u) v += __builtin_bit_cast(f32x4_t, load16(p + (int64_t)u * M * N));
+        if (a.bias)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += elem_f32<DT>(((const E*)a.bias)[n + e]);
+        store4<DT>(a.Y, (int64_t)m * N + n, v);
+    }
+}
+
+constexpr int64_t kFew = 64;
+
+// Workgroups that share 128 columns by splitting K: enough for two on each CU,
+// each wave with two steps of 32 or more.
+int stream_splits(int64_t K, int64_t N) {
+    const int64_t groups = (N + 127) / 128;
+    int64_t s = (512 + groups - 1) / groups;
+    if (s > K / 512) s = K / 512;
+    if (s > 16) s = 16;
+    return s < 1 ? 1 : (int)s;
+}
+
+// few rows, whole groups of 8 columns, W within 32-bit byte offsets
+bool streamable(int64_t M, int64_t K, int64_t N, int dt) {
+    return M <= kFew && K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
+}
+
+template <int DT, int TRANS>
+void lora_streamed(const LoraK& a, hipStream_t s) {
+    constexpr int V = kQ<DT>;
+    if constexpr (TRANS) {
+        lora_shrink_kernel<DT, 1, V><<<dim3((unsigned)((a.R + 3) / 4 + !a.R), (unsigned)a.M), 256, 0, s>>>(a, 0);
+    } else {
+        const int v = a.R >= V ? V : 1;
+        int tpr = 1;
+        while (tpr * v < a.R) tpr *= 2;
+        const dim3 grid(1, (unsigned)a.M);
+        if (v == V) lora_shrink_kernel<DT, 0, V><<<grid, 1024, 0, s>>>(a, tpr);
+        else lora_shrink_kernel<DT, 0, 1><<<grid, 1024, 0, s>>>(a, tpr);
+    }
+    const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)a.splits);
+    if (a.M <= 16) lora_stream_kernel<DT, TRANS, 1><<<grid, 512, 0, s>>>(a);
+    else if (a.M <= 32) lora_stream_kernel<DT, TRANS, 2><<<grid, 512, 0, s>>>(a);
+    else if (a.M <= 48) lora_stream_kernel<DT, TRANS, 3><<<grid, 512, 0, s>>>(a);
+    else lora_stream_kernel<DT, TRANS, 4><<<grid, 512, 0, s>>>(a);
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt) {
-    (void)K;
+    if (streamable(M, K, N, dt)) {
+        const int sp = stream_splits(K, N);
+        return align256((size_t)M * R * 4) + (sp > 1 ? align256((size_t)sp * M * N * 4) : 0) +
+               align256((size_t)(N + 127) / 128 * 4);
+    }
     return align256((size_t)M * R * 4) + align256((size_t)M * N * (dt == 2 ? 4 : 2));
 }
 
@@ -90,6 +322,23 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
     a.R = (int)l.R;
     a.trans = l.trans;
     a.idx64 = l.idx64;
+    if (streamable(l.M, l.K, l.N, dt)) {
+        a.W = l.W;
+        a.Y = l.Y;
+        a.splits = stream_splits(l.K, l.N);
+        a.part = (float*)a.D;
+        a.done = (uint32_t*)((char*)a.D + (a.splits > 1 ? align256((size_t)a.splits * l.M * l.N * 4) : 0));
+        log_choice("lora_matmul: streamed, K in %d part(s)", a.splits);
+        switch (dt * 2 + a.trans) {
+            case 0: lora_streamed<0, 0>(a, s); break;
+            case 1: lora_streamed<0, 1>(a, s); break;
+            case 2: lora_streamed<1, 0>(a, s); break;
+            case 3: lora_streamed<1, 1>(a, s); break;
+            case 4: lora_streamed<2, 0>(a, s); break;
+            default: lora_streamed<2, 1>(a, s); break;
+        }
+        return hipGetLastError();
+    }
     const int64_t nblk = (l.N + 255) / 256;
     const dim3 gs((unsigned)l.M), gd((unsigned)(l.M * nblk));
     if (dt == 0) {

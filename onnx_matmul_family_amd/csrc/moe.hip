@@ -12,6 +12,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kernels.hpp"
 #include "row_select.hpp"
 #include "stream_core.hpp"
@@ -320,48 +322,43 @@ void layer_any(const LayerArgs& a, hipStream_t s) {
     moe_down_any_kernel<DT><<<gd, 256, 0, s>>>(a);
 }
 
-// ------------------------------------------------------------------ streamed forms (bf16 / fp16)
-// contraction steps of 32 of one of a workgroup's NWS waves: even counts where
-// a 128-byte line of a weight column holds two
-template <int NWS>
-__device__ __forceinline__ void wave_steps(int kn, int trans, int wave, int& s0, int& s1, int splits = 1,
-                                           int split = 0) {
-    const int steps = (kn + 31) / 32, n = NWS * splits;
-    int per = (steps + n - 1) / n;
-    if (trans) per = (per + 1) & ~1;
-    s0 = min(steps, (split * NWS + wave) * per);
-    s1 = min(steps, s0 + per);
-}
-
+// ------------------------------------------------------------------ streamed forms
 // h of one expert and 64 columns: 64 gate columns and the 64 up columns beside
 // them are the wave's 8 fragments, so that act(gate) * up needs no other
-// workgroup.  TRANS = 0: lanes 0-7 of 16 load gate, 8-15 up; TRANS = 1:
-// fragments 0-3 are gate, 4-7 up.
+// workgroup.  TRANS = 0: lanes 0-7 of 16 load gate, 8-15 up (fp32: fragments
+// 0-3 and 4-7); TRANS = 1: fragments 0-3 are gate, 4-7 up.
 template <int DT, int TRANS, int NG, int NWS>
 __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r, int t0, float* red, int tid) {
-    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, q8 = (lane >> 4) * 8;
+    typedef typename elem_of<DT>::type E;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
+    const int q = (lane >> 4) * kQ<DT>;
     const int F = (int)a.F, K = (int)a.K, c0 = blockIdx.x * 64;
     const int64_t eoff = (int64_t)__builtin_amdgcn_readfirstlane(r.e) * a.K * a.F;
-    const uint16_t* wg = (const uint16_t*)a.wg + eoff;
-    const uint16_t* wu = (const uint16_t*)a.wu + eoff;
-    StreamW<TRANS> w;
+    const E* wg = (const E*)a.wg + eoff;
+    const E* wu = (const E*)a.wu + eoff;
+    StreamW<DT, TRANS> w;
     if constexpr (TRANS) {
         w.base[0] = wg;
         w.base[1] = wu;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * (j & 3) + i, F - 1) * K + q8;
+        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * (j & 3) + i, F - 1) * K + q;
     } else {
         w.ld = F;
-        w.p = (i < 8 ? wg : wu) + min(c0 + 8 * (i & 7), F - 8) + (int64_t)q8 * F;
+        if constexpr (DT == 2) {
+            w.p[0] = wg + group_start<DT>(c0, 4 * i, F) + (int64_t)q * F;
+            w.p[1] = wu + group_start<DT>(c0, 4 * i, F) + (int64_t)q * F;
+        } else {
+            w.p[0] = (i < 8 ? wg : wu) + group_start<DT>(c0, 8 * (i & 7), F) + (int64_t)q * F;
+        }
     }
-    StreamX16<NG> x;  // rows past the last are the last one: their results are not used
+    StreamX<DT, NG> x;  // rows past the last are the last one: their results are not used
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-        x.p[g] = (const uint16_t*)a.X + (int64_t)r.tok[min(t0 + 16 * g + i, r.n - 1)] * K + q8;
+        x.p[g] = (const E*)a.X + (int64_t)r.tok[min(t0 + 16 * g + i, r.n - 1)] * K + q;
     f32x4_t acc[8][NG] = {};
     int s0, s1;
-    wave_steps<NWS>(K, TRANS, wave, s0, s1);
-    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, q8, acc);
+    wave_steps<DT, NWS>(K, TRANS, wave, s0, s1);
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, q, acc);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g) __syncthreads();
@@ -372,8 +369,9 @@ __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r,
             const int c = o & 63, row = o >> 6, t = t0 + 16 * g + row;
             if (t >= r.n) continue;  // a wave has one row
             int j, l, rr, j2, l2, rr2;
-            red_pos<TRANS>(c, row, j, l, rr);
-            red_pos<TRANS>(c + 64, row, j2, l2, rr2);
+            const int shift = c0 + (c & ~(kQ<DT> - 1)) - group_start<DT>(c0, c, F);
+            red_pos<DT, TRANS>(c, shift, row, j, l, rr);
+            red_pos<DT, TRANS>(c + 64, shift, row, j2, l2, rr2);
             float gv = 0.0f, uv = 0.0f;
 #pragma unroll
             for (int v = 0; v < NWS; ++v) {
@@ -420,27 +418,34 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_up_kernel(Laye
 // part of one expert and 128 output columns
 template <int DT, int TRANS, int NG, int NWS>
 __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& r, int t0, float* red, int tid) {
-    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, q8 = (lane >> 4) * 8;
+    typedef typename elem_of<DT>::type E;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
+    const int q = (lane >> 4) * kQ<DT>;
     const int F = (int)a.F, N = (int)a.K, c0 = blockIdx.x * 128;
-    const uint16_t* wd = (const uint16_t*)a.wd + (int64_t)__builtin_amdgcn_readfirstlane(r.e) * a.K * a.F;
-    StreamW<TRANS> w;
+    const E* wd = (const E*)a.wd + (int64_t)__builtin_amdgcn_readfirstlane(r.e) * a.K * a.F;
+    StreamW<DT, TRANS> w;
     if constexpr (TRANS) {
         w.base[0] = w.base[1] = wd;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, N - 1) * F + q8;
+        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, N - 1) * F + q;
     } else {
         w.ld = N;
-        w.p = wd + min(c0 + 8 * i, N - 8) + (int64_t)q8 * N;
+        if constexpr (DT == 2) {
+            w.p[0] = wd + group_start<DT>(c0, 4 * i, N) + (int64_t)q * N;
+            w.p[1] = wd + group_start<DT>(c0, 64 + 4 * i, N) + (int64_t)q * N;
+        } else {
+            w.p[0] = wd + group_start<DT>(c0, 8 * i, N) + (int64_t)q * N;
+        }
     }
     int s0, s1;
     const int sp = blockIdx.z;
-    wave_steps<NWS>(F, TRANS, wave, s0, s1, a.splits, sp);
-    StreamX32<DT, NG> x;
+    wave_steps<DT, NWS>(F, TRANS, wave, s0, s1, a.splits, sp);
+    typename std::conditional<DT == 2, StreamX<2, NG>, StreamX32<DT, NG>>::type x;
     float undo[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         const int p = r.pair[min(t0 + 16 * g + i, r.n - 1)];
-        x.p[g] = a.h + (int64_t)p * F + q8;
+        x.p[g] = a.h + (int64_t)p * F + q;
         undo[g] = 1.0f;
         if constexpr (DT == 1) {  // the row's largest value over this wave's range -> [2^13, 2^14)
             const int slabs = (F + 63) / 64;
@@ -453,7 +458,7 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
         }
     }
     f32x4_t acc[8][NG] = {};
-    stream_run<DT, TRANS, NG>(w, x, s0, s1, F, q8, acc);
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, F, q, acc);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g) __syncthreads();
@@ -467,7 +472,7 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
             const int c = o & 127, row = o >> 7, t = t0 + 16 * g + row;
             if (t >= r.n || c0 + c >= N) continue;
             int j, l, rr;
-            red_pos<TRANS>(c, row, j, l, rr);
+            red_pos<DT, TRANS>(c, c0 + (c & ~(kQ<DT> - 1)) - group_start<DT>(c0, c, N), row, j, l, rr);
             float v = 0.0f;
 #pragma unroll
             for (int u = 0; u < NWS; ++u) v += red[red_index(u, j, l, rr)];
@@ -506,21 +511,22 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_down_kernel(La
     for (int o = tid; o < a.M * 32; o += 64 * NWS) {
         const int m = o >> 5, n = blockIdx.x * 128 + (o & 31) * 4;
         if (n >= a.K) continue;
+        const int64_t n4 = min((int64_t)n, a.K - 4);  // whole loads, as K >= 4; the last group may overlap
         f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int sp = 0; sp < a.splits; ++sp) {
-            const float* q = a.part + (sp * pairs + (int64_t)m * a.k) * a.K + n;
+            const float* q = a.part + (sp * pairs + (int64_t)m * a.k) * a.K + n4;
             // (kMaxTop at most; unrolled so that the loads of four go out together)
             for (int s0 = 0; s0 < a.k; s0 += 4) {
                 f32x4_t u[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = *(const f32x4_t*)(q + (int64_t)min(s0 + i, a.k - 1) * a.K);
+                for (int i = 0; i < 4; ++i)
+                    u[i] = __builtin_bit_cast(f32x4_t, load16(q + (int64_t)min(s0 + i, a.k - 1) * a.K));
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (s0 + i < a.k) v += u[i];
             }
         }
-        const u32x2_t y = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-        *(u32x2_t*)((uint16_t*)a.Y + (int64_t)m * a.K + n) = y;
+        store4<DT>(a.Y, (int64_t)m * a.K + n4, v);
     }
 }
 
@@ -557,10 +563,9 @@ void layer_pick(const LayerArgs& a, hipStream_t s) {
     }
 }
 
-// 16-byte loads of whole 8-element groups, and one expert's matrix within 32-bit byte offsets
-bool streamable(const LayerArgs& a) {
-    const uintptr_t p = (uintptr_t)a.X | (uintptr_t)a.wg | (uintptr_t)a.wu | (uintptr_t)a.wd;
-    return (p & 15) == 0 && ((uintptr_t)a.Y & 7) == 0 && a.K % 8 == 0 && a.F % 8 == 0 && a.F > 0 && a.K * a.F < (1LL << 30);
+// whole groups of 8 columns, and one expert's matrix within 32-bit byte offsets
+bool streamable(const LayerArgs& a, int dt) {
+    return a.K >= 8 && a.F >= 8 && a.K * a.F < (dt == 2 ? 1LL << 29 : 1LL << 30);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -620,13 +625,15 @@ hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void
     a.lists = (ExpertList*)w;
     w += align256((size_t)(l.M * l.k < l.E ? l.M * l.k : l.E) * sizeof(ExpertList));
     a.hmax = (float*)w;
-    if (dt < 2 && streamable(a)) {
+    if (streamable(a, dt)) {
         log_choice("moe_layer: streamed");
         switch (dt * 2 + a.trans) {
             case 0: layer_pick<0, 0>(a, s); break;
             case 1: layer_pick<0, 1>(a, s); break;
             case 2: layer_pick<1, 0>(a, s); break;
-            default: layer_pick<1, 1>(a, s); break;
+            case 3: layer_pick<1, 1>(a, s); break;
+            case 4: layer_pick<2, 0>(a, s); break;
+            default: layer_pick<2, 1>(a, s); break;
         }
         return hipGetLastError();
     }

@@ -1,12 +1,13 @@
-// Products of a few rows with a streamed weight matrix (bf16 / fp16): the
-// weights pass from memory to the matrix unit once, with no LDS staging.
+// Products of a few rows with a streamed weight matrix: the weights pass from
+// memory to the matrix unit once, with no LDS staging.
 //
 // A wave computes 8 fragments of 16 weight columns against groups of 16 rows,
-// over a range of the contraction axis in steps of 32, with
-// v_mfma_f32_16x16x32: the weights are the instruction's first operand (lane
-// l: column l % 16 of the fragment, contraction 8 (l / 16) .. + 7), the rows
-// its second, so lane l's results are row l % 16, columns 4 (l / 16) + r.
+// over a range of the contraction axis.  The weights are the instruction's
+// first operand, the rows its second, so lane l's results are row l % 16,
+// columns 4 (l / 16) + r of a fragment.
 //
+// bf16 / fp16, v_mfma_f32_16x16x32, steps of 32 (lane l: column l % 16,
+// contraction 8 (l / 16) .. + 7):
 //   TRANS = 1: weights (columns, contraction), contraction contiguous.  A
 //     fragment's operand is one 16-byte load a lane.
 //   TRANS = 0: weights (contraction, columns), columns contiguous.  A lane
@@ -14,13 +15,65 @@
 //     whose j-th columns, paired over the rows with v_perm (half an
 //     instruction an element), are its operand of fragment j.  "Column l % 16"
 //     of fragment j is then column 8 (l % 16) + j.
+// fp32, v_mfma_f32_16x16x4, steps of 16 (an instruction takes one value of
+// each lane, so a step is four of them; contraction 4 (l / 16) + t in the t-th):
+//   TRANS = 1: as above, 4 values a load, the t-th for the t-th instruction.
+//   TRANS = 0: a lane loads 4 columns of each of 4 contraction rows, twice (64
+//     columns apart); fragment j takes the (j % 4)-th value, "column l % 16" is
+//     column 64 (j / 4) + 4 (l % 16) + j % 4.
+//
+// Rows and columns need no alignment beyond their elements' (the loads are
+// 16 bytes wide all the same), sizes no multiples: a TRANS = 0 lane whose
+// columns pass the last one starts at the last whole group instead, and the
+// tail of the contraction is loaded element by element.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "device_common.hpp"
+#include "row_select.hpp"
 
 namespace omm {
+
+// 16 bytes at any multiple of the element size
+typedef u32x4_t u32x4_u2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_u4 __attribute__((aligned(4)));
+template <typename E>
+__device__ __forceinline__ u32x4_t load16(const E* p) {
+    if constexpr (sizeof(E) == 2)
+        return *(const u32x4_u2*)p;
+    else
+        return *(const u32x4_u4*)p;
+}
+// the first n elements of those 16 bytes, zeros after them
+template <typename E>
+__device__ __forceinline__ u32x4_t load16_first(const E* p, int n) {
+    u32x4_t v = {0, 0, 0, 0};
+    if (n >= (int)(16 / sizeof(E))) return load16(p);
+#pragma unroll
+    for (int i = 0; i < (int)(16 / sizeof(E)); ++i) {
+        if (i >= n) continue;
+        if constexpr (sizeof(E) == 2)
+            v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+        else
+            v[i] = __float_as_uint(p[i]);
+    }
+    return v;
+}
+
+// four fp32 values rounded to T at elements i .. i + 3 of p
+template <int DT>
+__device__ __forceinline__ void store4(void* p, int64_t i, f32x4_t v) {
+    if constexpr (DT == 2) {
+        *(u32x4_u4*)((float*)p + i) = __builtin_bit_cast(u32x4_t, v);
+    } else {
+        typedef u32x2_t u32x2_u2 __attribute__((aligned(2)));
+        *(u32x2_u2*)((uint16_t*)p + i) = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+    }
+}
+
+template <int DT> constexpr int kStep = DT == 2 ? 16 : 32;  // contraction of a step
+template <int DT> constexpr int kQ = DT == 2 ? 4 : 8;       // of one lane
 
 template <int DT>
 __device__ __forceinline__ f32x4_t mfma16x16x32(u32x4_t a, u32x4_t b, f32x4_t c) {
@@ -33,29 +86,46 @@ __device__ __forceinline__ f32x4_t mfma16x16x32(u32x4_t a, u32x4_t b, f32x4_t c)
 }
 
 // One lane's weights.  TRANS = 1: off[j], elements from base[j / 4] to the
-// lane's column of fragment j; TRANS = 0: p, the lane's 8 columns, and ld, the
-// row stride.  Both include the lane's contraction offset 8 (l / 16).  Bases,
-// ld and kb are uniform over the wave (scalar registers).
-template <int TRANS>
+// lane's column of fragment j; TRANS = 0: p, the lane's columns (fp32: p[1] of
+// the upper 64), and ld, the row stride.  Both include the lane's contraction
+// offset kQ (l / 16).  Bases, ld and kb are uniform over the wave (scalar
+// registers).  tail: only the first n (0 .. kQ) of the lane's contraction.
+template <int DT, int TRANS>
 struct StreamW {
-    const uint16_t* base[2];
+    typedef typename elem_of<DT>::type E;
+    const E* base[2];
     uint32_t off[8];
     __device__ __forceinline__ void load(u32x4_t (&w)[8], int kb) const {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = *(const u32x4_t*)(base[j >> 2] + kb + off[j]);
+        for (int j = 0; j < 8; ++j) w[j] = load16(base[j >> 2] + kb + off[j]);
+    }
+    __device__ __forceinline__ void tail(u32x4_t (&w)[8], int kb, int n) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = load16_first(base[j >> 2] + kb + off[j], n);
     }
 };
-template <>
-struct StreamW<0> {
-    const uint16_t* p;
+template <int DT>
+struct StreamW<DT, 0> {
+    typedef typename elem_of<DT>::type E;
+    const E* p[DT == 2 ? 2 : 1];
     int64_t ld;
+    __device__ __forceinline__ const E* at(int kb, int t) const {
+        if constexpr (DT == 2)
+            return p[t >> 2] + (int64_t)kb * ld + (t & 3) * ld;
+        else
+            return p[0] + (int64_t)kb * ld + t * ld;
+    }
     __device__ __forceinline__ void load(u32x4_t (&w)[8], int kb) const {
-        const uint16_t* q = p + (int64_t)kb * ld;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) w[t] = *(const u32x4_t*)(q + t * ld);
+        for (int t = 0; t < 8; ++t) w[t] = load16(at(kb, t));
+    }
+    __device__ __forceinline__ void tail(u32x4_t (&w)[8], int kb, int n) const {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) w[t] = (t & (kQ<DT> - 1)) < n ? load16(at(kb, t)) : u32x4_t{0, 0, 0, 0};
     }
 };
 
+// bf16 / fp16: a lane's operand of fragment j
 template <int TRANS>
 __device__ __forceinline__ u32x4_t stream_frag(const u32x4_t (&w)[8], int j) {
     if constexpr (TRANS) {
@@ -69,22 +139,52 @@ __device__ __forceinline__ u32x4_t stream_frag(const u32x4_t (&w)[8], int j) {
     }
 }
 
-// The rows as stored: 16-bit values in the operand layout
-template <int NG>
-struct StreamX16 {
+// The rows as stored, in the operand layout
+template <int DT, int NG>
+struct StreamX {
     static constexpr int RAW = 1, PARTS = 1;
-    const uint16_t* p[NG];  // the lane's row of each group, offset by 8 (l / 16)
+    typedef typename elem_of<DT>::type E;
+    const E* p[NG];  // the lane's row of each group, offset by kQ (l / 16)
     __device__ __forceinline__ void load(u32x4_t (&r)[NG][1], int kb) const {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) r[g][0] = *(const u32x4_t*)(p[g] + kb);
+        for (int g = 0; g < NG; ++g) r[g][0] = load16(p[g] + kb);
+    }
+    __device__ __forceinline__ void tail(u32x4_t (&r)[NG][1], int kb, int n) const {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) r[g][0] = load16_first(p[g] + kb, n);
     }
     __device__ __forceinline__ void operand(const u32x4_t (&r)[1], int, u32x4_t (&o)[1]) const { o[0] = r[0]; }
 };
 
-// fp32 rows as the sum of two 16-bit halves (16 bits of the significand for
-// bf16, 22 for fp16): two products instead of one, which the streamed weights
-// leave room for, and the rows are not rounded to T.  fp16 rows are scaled by
-// a power of two per row (scale[g]; the caller divides it out) into its range.
+// Eight fp32 values as two halves of T whose sum holds them to 16 bits of the
+// significand (bf16) or 22 (fp16, whose caller has scaled them into its range).
+// The first bf16 half is cut off, not rounded: a value near the largest float
+// stays finite.  An infinity is its own first half.
+template <int DT>
+__device__ __forceinline__ void split_halves(const u32x4_t (&r)[2], float scale, u32x4_t& hi, u32x4_t& lo) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t ua = r[i >> 1][(i & 1) * 2], ub = r[i >> 1][(i & 1) * 2 + 1];
+        float a = __uint_as_float(ua), b = __uint_as_float(ub), ah, bh;
+        if constexpr (DT == 1) {
+            a *= scale;
+            b *= scale;
+            hi[i] = pack2<DT>(a, b);
+            ah = from_bits<DT>((uint16_t)hi[i]);
+            bh = from_bits<DT>((uint16_t)(hi[i] >> 16));
+        } else {
+            hi[i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+            ah = __uint_as_float(ua & 0xffff0000u);
+            bh = __uint_as_float(ub & 0xffff0000u);
+        }
+        lo[i] = pack2<DT>(a == ah ? 0.0f : a - ah, b == bh ? 0.0f : b - bh);
+    }
+}
+
+// fp32 rows against bf16 / fp16 weights, as the sum of two 16-bit halves: two
+// products instead of one, which the streamed weights leave room for, and the
+// rows are not rounded to T.  fp16 rows are scaled by a power of two per row
+// (scale[g]; the caller divides it out).
 template <int DT, int NG>
 struct StreamX32 {
     static constexpr int RAW = 2, PARTS = 2;
@@ -93,24 +193,19 @@ struct StreamX32 {
     __device__ __forceinline__ void load(u32x4_t (&r)[NG][2], int kb) const {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            r[g][0] = *(const u32x4_t*)(p[g] + kb);
-            r[g][1] = *(const u32x4_t*)(p[g] + kb + 4);
+            r[g][0] = load16(p[g] + kb);
+            r[g][1] = load16(p[g] + kb + 4);
+        }
+    }
+    __device__ __forceinline__ void tail(u32x4_t (&r)[NG][2], int kb, int n) const {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            r[g][0] = load16_first(p[g] + kb, n);
+            r[g][1] = load16_first(p[g] + kb + 4, n - 4);
         }
     }
     __device__ __forceinline__ void operand(const u32x4_t (&r)[2], int g, u32x4_t (&o)[2]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float a = __uint_as_float(r[i >> 1][(i & 1) * 2]), b = __uint_as_float(r[i >> 1][(i & 1) * 2 + 1]);
-            if constexpr (DT == 1) {
-                a *= scale[g];
-                b *= scale[g];
-            }
-            const uint32_t hi = pack2<DT>(a, b);
-            const float ah = from_bits<DT>((uint16_t)hi), bh = from_bits<DT>((uint16_t)(hi >> 16));
-            o[0][i] = hi;
-            // an infinity is its own first half
-            o[1][i] = pack2<DT>(a == ah ? 0.0f : a - ah, b == bh ? 0.0f : b - bh);
-        }
+        split_halves<DT>(r, scale[g], o[0], o[1]);
     }
 };
 
@@ -122,35 +217,47 @@ __device__ __forceinline__ void stream_step(const u32x4_t (&w)[8], const u32x4_t
     for (int g = 0; g < NG; ++g) x.operand(r[g], g, o[g]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const u32x4_t f = stream_frag<TRANS>(w, j);
+        if constexpr (DT == 2) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int h = 0; h < X::PARTS; ++h) acc[j][g] = mfma16x16x32<DT>(f, o[g][h], acc[j][g]);
+                for (int g = 0; g < NG; ++g) {
+                    const uint32_t wv = TRANS ? w[j][t] : w[(j >> 2) * 4 + t][j & 3];
+                    acc[j][g] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(wv), __uint_as_float(o[g][0][t]),
+                                                                     acc[j][g], 0, 0, 0);
+                }
+        } else {
+            const u32x4_t f = stream_frag<TRANS>(w, j);
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int h = 0; h < X::PARTS; ++h) acc[j][g] = mfma16x16x32<DT>(f, o[g][h], acc[j][g]);
+        }
     }
 }
 
-// acc += steps [s0, s1) of 32 of a contraction of length kn (a multiple of 8;
-// the last step may be partial: lanes past kn take zeros).  q8 = 8 (l / 16).
+// acc += steps [s0, s1) of kStep of a contraction of length kn (the last step
+// may be partial: the lanes take zeros past kn).  q = kQ (l / 16).
 // Two register sets: the loads of a step are in flight while the one before
 // it multiplies.
 template <int DT, int TRANS, int NG, typename X>
-__device__ __forceinline__ void stream_run(const StreamW<TRANS>& w, const X& x, int s0, int s1, int kn, int q8,
+__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS>& w, const X& x, int s0, int s1, int kn, int q,
                                            f32x4_t (&acc)[8][NG]) {
-    const int full = min(s1, kn >> 5);
+    constexpr int ST = kStep<DT>;
+    const int full = min(s1, kn / ST);
     u32x4_t wa[8], wb[8], xa[NG][X::RAW], xb[NG][X::RAW];
     int s = s0;
     if (s < full) {
-        w.load(wa, s * 32);
-        x.load(xa, s * 32);
+        w.load(wa, s * ST);
+        x.load(xa, s * ST);
     }
     for (; s + 2 <= full; s += 2) {
-        w.load(wb, s * 32 + 32);
-        x.load(xb, s * 32 + 32);
+        w.load(wb, s * ST + ST);
+        x.load(xb, s * ST + ST);
         stream_step<DT, TRANS, NG>(wa, xa, x, acc);
         if (s + 2 < full) {
-            w.load(wa, s * 32 + 64);
-            x.load(xa, s * 32 + 64);
+            w.load(wa, s * ST + 2 * ST);
+            x.load(xa, s * ST + 2 * ST);
         }
         stream_step<DT, TRANS, NG>(wb, xb, x, acc);
     }
@@ -158,20 +265,31 @@ __device__ __forceinline__ void stream_run(const StreamW<TRANS>& w, const X& x, 
         stream_step<DT, TRANS, NG>(wa, xa, x, acc);
         ++s;
     }
-    if (s < s1 && s * 32 < kn) {  // partial last step
-        const u32x4_t z = {0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) wa[j] = z;
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int h = 0; h < X::RAW; ++h) xa[g][h] = z;
-        if (s * 32 + q8 < kn) {
-            w.load(wa, s * 32);
-            x.load(xa, s * 32);
-        }
+    if (s < s1 && s * ST < kn) {  // partial last step
+        const int n = max(0, min(kQ<DT>, kn - s * ST - q));
+        w.tail(wa, s * ST, n);
+        x.tail(xa, s * ST, n);
         stream_step<DT, TRANS, NG>(wa, xa, x, acc);
     }
+}
+
+// first column of the lane group that holds column c0 + c (c in 0 .. span) of
+// an axis of n columns: groups of kQ start at multiples, the last one at n - kQ
+template <int DT>
+__device__ __forceinline__ int group_start(int c0, int c, int n) {
+    return min(c0 + (c & ~(kQ<DT> - 1)), n - kQ<DT>);
+}
+
+// contraction steps of one of a workgroup's NWS waves: even counts where a
+// 128-byte line of a weight column holds two
+template <int DT, int NWS>
+__device__ __forceinline__ void wave_steps(int kn, int trans, int wave, int& s0, int& s1, int splits = 1,
+                                           int split = 0) {
+    const int steps = (kn + kStep<DT> - 1) / kStep<DT>, n = NWS * splits;
+    int per = (steps + n - 1) / n;
+    if (trans) per = (per + 1) & ~1;
+    s0 = min(steps, (split * NWS + wave) * per);
+    s1 = min(steps, s0 + per);
 }
 
 // LDS image of a wave's 8 fragments of one group, for the sum over the waves
@@ -181,11 +299,21 @@ constexpr int kFragPad = 64 * 4 + 4;
 __device__ __forceinline__ int red_index(int wave, int j, int lane, int r) {
     return (wave * 8 + j) * kFragPad + lane * 4 + r;
 }
-// position of (column c of the wave's 128, row of the group) in that image
-template <int TRANS>
-__device__ __forceinline__ void red_pos(int c, int row, int& j, int& lane, int& r) {
-    const int i = TRANS ? c & 15 : c >> 3;
-    j = TRANS ? c >> 4 : c & 7;
+// position of (column c of the wave's 128, row of the group) in that image;
+// shift: how far before its multiple the column's group starts
+template <int DT, int TRANS>
+__device__ __forceinline__ void red_pos(int c, int shift, int row, int& j, int& lane, int& r) {
+    int i;
+    if constexpr (TRANS) {
+        i = c & 15;
+        j = c >> 4;
+    } else if constexpr (DT == 2) {
+        i = (c & 63) >> 2;
+        j = (c >> 6) * 4 + min((c & 3) + shift, 3);
+    } else {
+        i = c >> 3;
+        j = min((c & 7) + shift, 7);
+    }
     lane = (i >> 2) * 16 + row;
     r = i & 3;
 }
