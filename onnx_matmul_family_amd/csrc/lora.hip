@@ -23,7 +23,7 @@ struct LoraK {
     void* D;             // workspace: (M, N)
     const void* W;       // streamed form: as the caller's
     void* Y;
-    float* part;         // workspace: (splits, M, N)
+    float* part;         // workspace: (ceil(N / 128), splits, M, 128)
     uint32_t* done;      // workspace: finished workgroups of each 128 columns
     int64_t M, K, N, G;
     int R, trans, idx64, splits;
@@ -144,27 +144,59 @@ __global__ __launch_bounds__(TRANS ? 256 : 1024) void lora_shrink_kernel(LoraK a
     }
 }
 
-// sum_r T[m, r] B[g, r, n] of a row with adapter g
+// ex[j][c] = sum_r T[m, r] B[g, r, c0 + c] of the rows m = split + j splits.
+//   TRANS = 1: a thread a column, 16 bytes of r a load.
+//   TRANS = 0: a thread 16 bytes of columns, one r a load.
 template <int DT, int TRANS>
-__device__ __forceinline__ float lora_expand(const LoraK& a, const float* t, int64_t g, int64_t n) {
+__device__ __forceinline__ void lora_expand(const LoraK& a, int split, int c0, float (*ex)[128], int tid) {
     typedef typename elem_of<DT>::type E;
-    constexpr int V = kQ<DT>;
-    float acc = 0.0f;
-    const int rv = a.R / V * V;
-    const E* b = (const E*)a.B + g * a.R * a.N + (TRANS ? n * a.R : n);
-    for (int r = 0; r < rv; r += V) {
-        float bv[V];
+    constexpr int V = kQ<DT>, TPR = TRANS ? 128 : 128 / V;  // threads a row
+    const int M = (int)a.M, N = (int)a.N, R = a.R;
+    const int c = TRANS ? tid & 127 : (tid & (TPR - 1)) * V;
+    if (c0 + c >= N) return;
+    const int n = TRANS ? c0 + c : group_start<DT>(c0, c, N);
+    for (int j = tid / TPR, m = split + j * a.splits; m < M; j += 512 / TPR, m = split + j * a.splits) {
+        const int64_t g = row_adapter(a, m);
+        const float* t = a.T + m * R;
+        const E* b = (const E*)a.B + (g < 0 ? 0 : g) * R * a.N + (TRANS ? (int64_t)n * R : n);
+        const int rn = g < 0 ? 0 : R, rv = rn / V * V;
         if constexpr (TRANS) {
-            unpack16<DT>(load16(b + r), bv);
+            float acc = 0.0f;
+#pragma unroll 4
+            for (int r = 0; r < rv; r += V) {
+                float bv[V];
+                unpack16<DT>(load16(b + r), bv);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc = fmaf(t[r + i], bv[i], acc);
+            }
+            for (int r = rv; r < rn; ++r) acc = fmaf(t[r], elem_f32<DT>(b[r]), acc);
+            ex[j][c] = acc;
         } else {
+            float acc[V] = {};
+            auto row = [&](u32x4_t w, float tv) {
+                float bv[V];
+                unpack16<DT>(w, bv);
 #pragma unroll
-            for (int i = 0; i < V; ++i) bv[i] = elem_f32<DT>(b[(int64_t)(r + i) * a.N]);
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(tv, bv[i], acc[i]);
+            };
+            int r = 0;
+            for (; r + 8 <= rn; r += 8) {
+                u32x4_t w[8];
+                float tv[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    w[i] = load16(b + (int64_t)(r + i) * a.N);
+                    tv[i] = t[r + i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) row(w[i], tv[i]);
+            }
+            for (; r < rn; ++r) row(load16(b + (int64_t)r * a.N), t[r]);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (n + i >= c0 + c) ex[j][n + i - c0] = acc[i];
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc = fmaf(t[r + i], bv[i], acc);
     }
-    for (int r = rv; r < a.R; ++r) acc = fmaf(t[r], elem_f32<DT>(b[TRANS ? r : (int64_t)r * a.N]), acc);
-    return acc;
 }
 
 // Y of 128 columns: X W streamed (8 waves split the workgroup's part of K),
@@ -174,6 +206,7 @@ template <int DT, int TRANS, int NG>
 __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
     __shared__ __attribute__((aligned(16))) float red[8 * 8 * kFragPad];
+    __shared__ float ex[16 * NG][128];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
     const int q = (lane >> 4) * kQ<DT>, sp = blockIdx.y;
     const int M = (int)a.M, K = (int)a.K, N = (int)a.N, c0 = blockIdx.x * 128;
@@ -198,7 +231,7 @@ __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
     f32x4_t acc[8][NG] = {};
     int s0, s1;
     wave_steps<DT, 8>(K, TRANS, wave, s0, s1, a.splits, sp);
-    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, q, acc);
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, q, acc, [&] { lora_expand<DT, TRANS>(a, sp, c0, ex, tid); });
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g) __syncthreads();
@@ -206,7 +239,7 @@ __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
         for (int j = 0; j < 8; ++j) *(f32x4_t*)&red[red_index(wave, j, lane, 0)] = acc[j][g];
         __syncthreads();
         for (int o = tid; o < 16 * 128; o += 512) {
-            const int c = o & 127, row = __builtin_amdgcn_readfirstlane(o >> 7), m = 16 * g + row;  // a wave has one row
+            const int c = o & 127, row = o >> 7, m = 16 * g + row;
             const int n = c0 + c;
             if (m >= M || n >= N) continue;
             int j, l, rr;
@@ -214,57 +247,40 @@ __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
             float v = 0.0f;
 #pragma unroll
             for (int u = 0; u < 8; ++u) v += red[red_index(u, j, l, rr)];
-            if (m % a.splits == sp) {
-                const int64_t ad = row_adapter(a, m);
-                if (ad >= 0) v += lora_expand<DT, TRANS>(a, a.T + m * a.R, ad, n);
-            }
+            if (m % a.splits == sp) v += ex[m / a.splits][c];
             if (a.splits == 1) {
                 if (a.bias) v += elem_f32<DT>(((const E*)a.bias)[n]);
                 ((E*)a.Y)[(int64_t)m * N + n] = f32_elem<DT>(v);
             } else {
-                // written past this XCD's L2: another one's workgroup may sum them
-                __hip_atomic_store(&a.part[((int64_t)sp * M + m) * N + n], v, __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
+                part_store(a.part, ((int64_t)blockIdx.x * a.splits + sp) * M + m, c, v);
             }
         }
     }
-    if (a.splits == 1) return;
-    // every wave's stores have reached memory before the workgroup is counted
     // (the kernel before this one zeroed the count)
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    __shared__ int last;
-    if (tid == 0)
-        last = __hip_atomic_fetch_add(&a.done[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               (uint32_t)(a.splits - 1);
-    __syncthreads();
-    if (!last) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    for (int o = tid; o < M * 32; o += 512) {
-        const int m = o >> 5;
-        if (c0 + (o & 31) * 4 >= N) continue;
-        const int n = min(c0 + (o & 31) * 4, N - 4);  // whole loads, as N >= 4; the last group may overlap
-        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-        const float* p = a.part + (int64_t)m * N + n;
-#pragma unroll 4
-        for (int u = 0; u < a.splits; ++u) v += __builtin_bit_cast(f32x4_t, load16(p + (int64_t)u * M * N));
-        if (a.bias)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += elem_f32<DT>(((const E*)a.bias)[n + e]);
-        store4<DT>(a.Y, (int64_t)m * N + n, v);
-    }
+    if (a.splits == 1 || !part_last(&a.done[blockIdx.x], a.splits, tid)) return;
+    part_sums<512>(
+        a.part, M, a.splits, tid, [&](int m, int p) { return ((int64_t)blockIdx.x * a.splits + p) * M + m; },
+        [&](int m, int c, float v0, float v1) {
+            const int n = c0 + c;
+            E* y = (E*)a.Y + (int64_t)m * N + n;
+            if (n < N) y[0] = f32_elem<DT>(v0 + (a.bias ? elem_f32<DT>(((const E*)a.bias)[n]) : 0.0f));
+            if (n + 1 < N) y[1] = f32_elem<DT>(v1 + (a.bias ? elem_f32<DT>(((const E*)a.bias)[n + 1]) : 0.0f));
+        });
 }
 
 constexpr int64_t kFew = 64;
 
-// Workgroups that share 128 columns by splitting K: enough for two on each CU,
-// each wave with two steps of 32 or more.
+// Workgroups that share 128 columns by splitting K: as many as run at once (one
+// a CU), each wave with two steps of 32 or more; of the counts that leave a
+// wave the same steps, the smallest.
 int stream_splits(int64_t K, int64_t N) {
-    const int64_t groups = (N + 127) / 128;
-    int64_t s = (512 + groups - 1) / groups;
-    if (s > K / 512) s = K / 512;
+    const int64_t groups = (N + 127) / 128, steps = (K + 31) / 32;
+    int64_t s = 256 / groups;
+    if (s > steps / 16) s = steps / 16;
     if (s > 16) s = 16;
-    return s < 1 ? 1 : (int)s;
+    if (s < 1) s = 1;
+    const int64_t per = (steps + 8 * s - 1) / (8 * s);
+    return (int)((steps + 8 * per - 1) / (8 * per));
 }
 
 // few rows, whole groups of 8 columns, W within 32-bit byte offsets
@@ -299,7 +315,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt) {
     if (streamable(M, K, N, dt)) {
         const int sp = stream_splits(K, N);
-        return align256((size_t)M * R * 4) + (sp > 1 ? align256((size_t)sp * M * N * 4) : 0) +
+        return align256((size_t)M * R * 4) + (sp > 1 ? align256((size_t)sp * M * ((N + 127) / 128) * 512) : 0) +
                align256((size_t)(N + 127) / 128 * 4);
     }
     return align256((size_t)M * R * 4) + align256((size_t)M * N * (dt == 2 ? 4 : 2));
@@ -327,7 +343,7 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
         a.Y = l.Y;
         a.splits = stream_splits(l.K, l.N);
         a.part = (float*)a.D;
-        a.done = (uint32_t*)((char*)a.D + (a.splits > 1 ? align256((size_t)a.splits * l.M * l.N * 4) : 0));
+        a.done = (uint32_t*)((char*)a.D + (a.splits > 1 ? align256((size_t)a.splits * l.M * ((l.N + 127) / 128) * 512) : 0));
         log_choice("lora_matmul: streamed, K in %d part(s)", a.splits);
         switch (dt * 2 + a.trans) {
             case 0: lora_streamed<0, 0>(a, s); break;

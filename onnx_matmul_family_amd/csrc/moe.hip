@@ -136,7 +136,7 @@ struct LayerArgs {
     ExpertList* lists;     // workspace: (min(E, M k)) (streamed form)
     float* hmax;           // workspace: (M k, ceil(F / 64)) largest |h| (fp16)
     float* h;              // workspace: (M k, F), weighted
-    float* part;           // workspace: (splits, M k, K)
+    float* part;           // workspace: (ceil(K / 128), splits, M k, 128)
     uint32_t* done;        // workspace: finished workgroups of each 128 output columns
     int64_t K, F;
     int M, E, k, renorm, act, trans, logits_kind, splits;
@@ -476,9 +476,7 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
             float v = 0.0f;
 #pragma unroll
             for (int u = 0; u < NWS; ++u) v += red[red_index(u, j, l, rr)];
-            // written past this XCD's L2: another one's workgroup may sum them
-            __hip_atomic_store(&a.part[((int64_t)sp * a.M * a.k + r.pair[t]) * N + c0 + c], v,
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            part_store(a.part, ((int64_t)blockIdx.x * a.splits + sp) * (a.M * a.k) + r.pair[t], c, v);
         }
     }
 }
@@ -495,39 +493,23 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_down_kernel(La
         if (t0) __syncthreads();
         down_rows<DT, TRANS, NG, NWS>(a, r, t0, red, tid);
     }
-    // The last workgroup of these 128 columns sums the experts: every wave's
-    // stores have reached memory before the workgroup is counted, and the
-    // count was zeroed by the first kernel.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    __shared__ int last;
-    if (tid == 0)
-        last = __hip_atomic_fetch_add(&a.done[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               (uint32_t)(r.active * a.splits - 1);
-    __syncthreads();
-    if (!last) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    const int64_t pairs = (int64_t)a.M * a.k;
-    for (int o = tid; o < a.M * 32; o += 64 * NWS) {
-        const int m = o >> 5, n = blockIdx.x * 128 + (o & 31) * 4;
-        if (n >= a.K) continue;
-        const int64_t n4 = min((int64_t)n, a.K - 4);  // whole loads, as K >= 4; the last group may overlap
-        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int sp = 0; sp < a.splits; ++sp) {
-            const float* q = a.part + (sp * pairs + (int64_t)m * a.k) * a.K + n4;
-            // (kMaxTop at most; unrolled so that the loads of four go out together)
-            for (int s0 = 0; s0 < a.k; s0 += 4) {
-                f32x4_t u[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    u[i] = __builtin_bit_cast(f32x4_t, load16(q + (int64_t)min(s0 + i, a.k - 1) * a.K));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (s0 + i < a.k) v += u[i];
-            }
-        }
-        store4<DT>(a.Y, (int64_t)m * a.K + n4, v);
-    }
+    // The last workgroup of these 128 columns sums the experts (the first kernel
+    // zeroed the count).
+    if (!part_last(&a.done[blockIdx.x], r.active * a.splits, tid)) return;
+    const int N = (int)a.K, k = a.k;
+    part_sums<64 * NWS>(
+        a.part, a.M, k * a.splits, tid,
+        [&](int m, int p) {
+            const int sp = p / k;
+            return ((int64_t)blockIdx.x * a.splits + sp) * (a.M * k) + m * k + (p - sp * k);
+        },
+        [&](int m, int c, float v0, float v1) {
+            typedef typename elem_of<DT>::type E;
+            const int n = blockIdx.x * 128 + c;
+            E* y = (E*)a.Y + (int64_t)m * N + n;
+            if (n < N) y[0] = f32_elem<DT>(v0);
+            if (n + 1 < N) y[1] = f32_elem<DT>(v1);
+        });
 }
 
 // NG groups of 16 tokens pass an expert's weights at once; an expert with more
@@ -591,7 +573,7 @@ hipError_t launch_moe_route(const MoeRouteArgs& r, int dt, hipStream_t s) {
 size_t moe_layer_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t k) {
     const size_t jmax = (size_t)(M * k < E ? M * k : E);
     return align256((size_t)M * k * 4) + align256((size_t)M * k * F * 4) +
-           align256((size_t)M * k * K * 4 * down_splits(M, K, F, E, k)) + align256((size_t)(K + 127) / 128 * 4) + align256(jmax * sizeof(ExpertList)) +
+           align256((size_t)M * k * ((K + 127) / 128) * 512 * down_splits(M, K, F, E, k)) + align256((size_t)(K + 127) / 128 * 4) + align256(jmax * sizeof(ExpertList)) +
            align256((size_t)M * k * ((F + 63) / 64) * 4);
 }
 
@@ -619,7 +601,7 @@ hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void
     w += align256((size_t)l.M * l.k * l.F * 4);
     a.part = (float*)w;
     a.splits = down_splits(l.M, l.K, l.F, l.E, l.k);
-    w += align256((size_t)l.M * l.k * l.K * 4 * a.splits);
+    w += align256((size_t)l.M * l.k * ((l.K + 127) / 128) * 512 * a.splits);
     a.done = (uint32_t*)w;
     w += align256((size_t)(l.K + 127) / 128 * 4);
     a.lists = (ExpertList*)w;

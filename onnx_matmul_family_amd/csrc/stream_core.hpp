@@ -61,17 +61,6 @@ __device__ __forceinline__ u32x4_t load16_first(const E* p, int n) {
     return v;
 }
 
-// four fp32 values rounded to T at elements i .. i + 3 of p
-template <int DT>
-__device__ __forceinline__ void store4(void* p, int64_t i, f32x4_t v) {
-    if constexpr (DT == 2) {
-        *(u32x4_u4*)((float*)p + i) = __builtin_bit_cast(u32x4_t, v);
-    } else {
-        typedef u32x2_t u32x2_u2 __attribute__((aligned(2)));
-        *(u32x2_u2*)((uint16_t*)p + i) = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-    }
-}
-
 template <int DT> constexpr int kStep = DT == 2 ? 16 : 32;  // contraction of a step
 template <int DT> constexpr int kQ = DT == 2 ? 4 : 8;       // of one lane
 
@@ -239,10 +228,10 @@ __device__ __forceinline__ void stream_step(const u32x4_t (&w)[8], const u32x4_t
 // acc += steps [s0, s1) of kStep of a contraction of length kn (the last step
 // may be partial: the lanes take zeros past kn).  q = kQ (l / 16).
 // Two register sets: the loads of a step are in flight while the one before
-// it multiplies.
-template <int DT, int TRANS, int NG, typename X>
+// it multiplies.  `meanwhile` runs while the first loads are on their way.
+template <int DT, int TRANS, int NG, typename X, typename F>
 __device__ __forceinline__ void stream_run(const StreamW<DT, TRANS>& w, const X& x, int s0, int s1, int kn, int q,
-                                           f32x4_t (&acc)[8][NG]) {
+                                           f32x4_t (&acc)[8][NG], F meanwhile) {
     constexpr int ST = kStep<DT>;
     const int full = min(s1, kn / ST);
     u32x4_t wa[8], wb[8], xa[NG][X::RAW], xb[NG][X::RAW];
@@ -251,6 +240,7 @@ __device__ __forceinline__ void stream_run(const StreamW<DT, TRANS>& w, const X&
         w.load(wa, s * ST);
         x.load(xa, s * ST);
     }
+    meanwhile();
     for (; s + 2 <= full; s += 2) {
         w.load(wb, s * ST + ST);
         x.load(xb, s * ST + ST);
@@ -271,6 +261,12 @@ __device__ __forceinline__ void stream_run(const StreamW<DT, TRANS>& w, const X&
         x.tail(xa, s * ST, n);
         stream_step<DT, TRANS, NG>(wa, xa, x, acc);
     }
+}
+
+template <int DT, int TRANS, int NG, typename X>
+__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS>& w, const X& x, int s0, int s1, int kn, int q,
+                                           f32x4_t (&acc)[8][NG]) {
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, kn, q, acc, [] {});
 }
 
 // first column of the lane group that holds column c0 + c (c in 0 .. span) of
@@ -316,6 +312,68 @@ __device__ __forceinline__ void red_pos(int c, int shift, int row, int& j, int& 
     }
     lane = (i >> 2) * 16 + row;
     r = i & 3;
+}
+
+// ------------------------------------------------------------------ parts of one result in several workgroups
+// A workgroup leaves its part of a row's 128 columns in parts[row][128], past
+// its own L2 (another one's workgroup may sum it), and counts itself; the last
+// one of a column block to be counted sums the parts.  Whole rows of 512 bytes
+// belong to one column block, and they are read with loads that do not look
+// into this L2 either, so no cache has to be invalidated.
+__device__ __forceinline__ void part_store(float* parts, int64_t row, int c, float v) {
+    __hip_atomic_store(parts + row * 128 + c, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// whether this workgroup is the last of `count` (every thread calls it)
+__device__ __forceinline__ bool part_last(uint32_t* done, uint32_t count, int tid) {
+    __shared__ int last;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores have reached memory
+    __syncthreads();
+    if (tid == 0)
+        last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == count - 1;
+    __syncthreads();
+    return last != 0;
+}
+// Calls out(m, c, v0, v1) with the sums over p in [0, np) of parts[first(m) +
+// step(p)][c], [c + 1] for the M rows and 64 column pairs; a thread has NB * SB
+// loads on their way at once (a round trip to memory takes as long as all of
+// them).  The order of the sum is fixed.
+template <int NT, int NB, int SB, typename Row, typename Out>
+__device__ __forceinline__ void part_sums(const float* parts, int M, int np, int tid, Row row, Out out) {
+    for (int o0 = tid; o0 < M * 64; o0 += NT * NB) {
+        float v[NB][2] = {};
+        for (int p0 = 0; p0 < np; p0 += SB) {
+            uint64_t u[NB][SB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int o = min(o0 + b * NT, M * 64 - 1);
+#pragma unroll
+                for (int i = 0; i < SB; ++i)
+                    u[b][i] = __hip_atomic_load(
+                        (const uint64_t*)(parts + row(o >> 6, min(p0 + i, np - 1)) * 128 + (o & 63) * 2),
+                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < SB; ++i)
+                    if (p0 + i < np) {
+                        v[b][0] += __uint_as_float((uint32_t)u[b][i]);
+                        v[b][1] += __uint_as_float((uint32_t)(u[b][i] >> 32));
+                    }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int o = o0 + b * NT;
+            if (o < M * 64) out(o >> 6, (o & 63) * 2, v[b][0], v[b][1]);
+        }
+    }
+}
+template <int NT, typename Row, typename Out>
+__device__ __forceinline__ void part_sums(const float* parts, int M, int np, int tid, Row row, Out out) {
+    if (M * 64 <= NT)
+        part_sums<NT, 1, 16>(parts, M, np, tid, row, out);
+    else
+        part_sums<NT, 4, 8>(parts, M, np, tid, row, out);
 }
 
 }  // namespace omm
