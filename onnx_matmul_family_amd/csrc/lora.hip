@@ -5,34 +5,13 @@
 #include <stdint.h>
 
 #include "kernels.hpp"
+#include "lora_args.hpp"
 #include "row_select.hpp"
 #include "stream_core.hpp"
 
 namespace omm {
 
 namespace {
-
-struct LoraK {
-    const void* X;
-    const void* A;
-    const void* B;
-    const void* idx;
-    const float* scale;  // (G) or nullptr
-    const void* bias;    // (N) or nullptr
-    float* T;            // workspace: (M, R), scaled
-    void* D;             // workspace: (M, N)
-    const void* W;       // streamed form: as the caller's
-    void* Y;
-    float* part;         // workspace: (ceil(N / 128), splits, M, 128)
-    uint32_t* done;      // workspace: finished workgroups of each 128 columns
-    int64_t M, K, N, G;
-    int R, trans, idx64, splits;
-};
-
-__device__ __forceinline__ int64_t row_adapter(const LoraK& a, int64_t m) {
-    const int64_t g = a.idx64 ? ((const int64_t*)a.idx)[m] : (int64_t)((const int32_t*)a.idx)[m];
-    return g >= 0 && g < a.G ? g : -1;
-}
 
 // T[m, r] = scale[g] sum_k X[m, k] A[g, k, r]: a workgroup a row, a wave an r
 template <int DT>
@@ -52,7 +31,7 @@ __global__ __launch_bounds__(256) void lora_shrink_any_kernel(LoraK a) {
     }
 }
 
-// D[m, n] = bias[n] + sum_r T[m, r] B[g, r, n]
+// Y[m, n] = bias[n] + sum_r T[m, r] B[g, r, n]
 template <int DT>
 __global__ __launch_bounds__(256) void lora_delta_any_kernel(LoraK a, int64_t nblk) {
     typedef typename elem_of<DT>::type E;
@@ -66,7 +45,7 @@ __global__ __launch_bounds__(256) void lora_delta_any_kernel(LoraK a, int64_t nb
         const float* t = a.T + m * a.R;
         for (int r = 0; r < a.R; ++r) acc = fmaf(t[r], elem_f32<DT>(b[r * sr]), acc);
     }
-    ((E*)a.D)[m * a.N + n] = f32_elem<DT>(acc);
+    ((E*)a.Y)[m * a.N + n] = f32_elem<DT>(acc);
 }
 
 // ------------------------------------------------------------------ few rows (at most 64)
@@ -318,19 +297,42 @@ size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt) 
         return align256((size_t)M * R * 4) + (sp > 1 ? align256((size_t)sp * M * ((N + 127) / 128) * 512) : 0) +
                align256((size_t)(N + 127) / 128 * 4);
     }
-    return align256((size_t)M * R * 4) + align256((size_t)M * N * (dt == 2 ? 4 : 2));
+    return lora_rows_workspace_bytes(M, R);
+}
+
+hipError_t lora_add_dense(const LoraK& a, const void* C, int dt, hipStream_t s) {
+    DenseArgs d = {};
+    d.A = a.X;
+    d.B = a.W;
+    d.Y = a.Y;
+    d.C = C;
+    d.M = a.M;
+    d.N = a.N;
+    d.K = a.K;
+    d.lda = a.K;
+    d.ldb = a.trans ? a.K : a.N;
+    d.ldy = a.N;
+    d.nb0 = d.nb1 = 1;
+    d.c_sm = a.N;
+    d.c_sn = 1;
+    d.alpha = 1.0f;
+    d.beta = 1.0f;
+    d.a_kmajor = 1;
+    d.b_kmajor = a.trans;
+    return dt == 2 ? launch_dense_f32(d, s) : launch_dense16(d, dt, s);
 }
 
 hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
-    LoraK a;
+    LoraK a = {};
     a.X = l.X;
+    a.W = l.W;
     a.A = l.A;
     a.B = l.B;
     a.idx = l.idx;
     a.scale = l.scale;
     a.bias = l.bias;
+    a.Y = l.Y;
     a.T = (float*)ws;
-    a.D = (char*)ws + align256((size_t)l.M * l.R * 4);
     a.M = l.M;
     a.K = l.K;
     a.N = l.N;
@@ -339,11 +341,10 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
     a.trans = l.trans;
     a.idx64 = l.idx64;
     if (streamable(l.M, l.K, l.N, dt)) {
-        a.W = l.W;
-        a.Y = l.Y;
         a.splits = stream_splits(l.K, l.N);
-        a.part = (float*)a.D;
-        a.done = (uint32_t*)((char*)a.D + (a.splits > 1 ? align256((size_t)a.splits * l.M * ((l.N + 127) / 128) * 512) : 0));
+        a.part = (float*)((char*)ws + align256((size_t)l.M * l.R * 4));
+        a.done = (uint32_t*)((char*)a.part +
+                             (a.splits > 1 ? align256((size_t)a.splits * l.M * ((l.N + 127) / 128) * 512) : 0));
         log_choice("lora_matmul: streamed, K in %d part(s)", a.splits);
         switch (dt * 2 + a.trans) {
             case 0: lora_streamed<0, 0>(a, s); break;
@@ -355,6 +356,8 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
         }
         return hipGetLastError();
     }
+    if (lora_rows_ok(l.M, l.K, l.N, l.R, l.G, l.trans)) return launch_lora_rows(a, dt, ws, s);
+    log_choice("lora_matmul: element-wise");
     const int64_t nblk = (l.N + 255) / 256;
     const dim3 gs((unsigned)l.M), gd((unsigned)(l.M * nblk));
     if (dt == 0) {
@@ -367,27 +370,8 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
         lora_shrink_any_kernel<2><<<gs, 256, 0, s>>>(a);
         lora_delta_any_kernel<2><<<gd, 256, 0, s>>>(a, nblk);
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    DenseArgs d = {};
-    d.A = l.X;
-    d.B = l.W;
-    d.Y = l.Y;
-    d.C = a.D;
-    d.M = l.M;
-    d.N = l.N;
-    d.K = l.K;
-    d.lda = l.K;
-    d.ldb = l.trans ? l.K : l.N;
-    d.ldy = l.N;
-    d.nb0 = d.nb1 = 1;
-    d.c_sm = l.N;
-    d.c_sn = 1;
-    d.alpha = 1.0f;
-    d.beta = 1.0f;
-    d.a_kmajor = 1;
-    d.b_kmajor = l.trans;
-    return dt == 2 ? launch_dense_f32(d, s) : launch_dense16(d, dt, s);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : lora_add_dense(a, a.Y, dt, s);
 }
 
 }  // namespace omm

@@ -1,0 +1,41 @@
+// Argument block of the lora_matmul kernels (lora.hip: up to 64 rows and the
+// element-wise form; lora_rows.hip: more rows).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace omm {
+
+struct LoraK {
+    const void* X;
+    const void* W;
+    const void* A;
+    const void* B;
+    const void* idx;
+    const float* scale;  // (G) or nullptr
+    const void* bias;    // (N) or nullptr
+    void* Y;
+    int64_t M, K, N, G;
+    int R, trans, idx64, splits;
+    // workspace
+    float* T;        // (M, R), scaled; rows in the order of perm
+    float* part;     // (ceil(N / 128), splits, M, 128)
+    uint32_t* done;  // finished workgroups of each 128 columns
+    int32_t* perm;   // (M) rows in the order of their adapters, or nullptr: as they come
+    float* tmax;     // (M, 2 ceil(R / 128)) largest |T| (fp16)
+};
+
+// the adapter of row m, -1: none
+__device__ __forceinline__ int64_t row_adapter(const LoraK& a, int64_t m) {
+    const int64_t g = a.idx64 ? ((const int64_t*)a.idx)[m] : (int64_t)((const int32_t*)a.idx)[m];
+    return g >= 0 && g < a.G ? g : -1;
+}
+
+// Y = X W + C, C (M, N) of T (may be Y)
+hipError_t lora_add_dense(const LoraK& a, const void* C, int dt, hipStream_t s);
+
+bool lora_rows_ok(int64_t M, int64_t K, int64_t N, int64_t R, int64_t G, int trans);
+size_t lora_rows_workspace_bytes(int64_t M, int64_t R);
+hipError_t launch_lora_rows(LoraK a, int dt, void* ws, hipStream_t s);
+
+}  // namespace omm

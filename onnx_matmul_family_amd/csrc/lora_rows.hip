@@ -1,0 +1,474 @@
+// The projection with per-row adapters for more than 64 rows (prompts):
+//   Y[m] = X[m] W (+ bias) + scale[g] (X[m] A[g]) B[g],   g = idx[m].
+//
+// Rows are taken in the order of their adapters (a stable counting sort, so
+// that results do not depend on scheduling), which makes almost every block of
+// 16 rows one of a single adapter:
+//   lora_sort_kernel         the order
+//   lora_shrink_rows_kernel  T = scale X A in fp32, 16 rows a workgroup
+//   lora_tile_kernel         Y tiles on the LDS-DMA matrix core; as a tile
+//                            leaves, T B is added to its accumulators.  T's
+//                            rows enter as two 16-bit halves, so T is not
+//                            rounded to T's type and neither is T B.
+// Operands that the DMA cannot take (rows not 16-byte aligned) and fp32:
+//   lora_expand_kernel       bias + T B into Y, to which the framework's dense
+//                            product is then added.
+// A block of rows that mixes adapters multiplies each one's B on its own and
+// adds it under a mask: a zero row times another adapter's infinity would be
+// NaN.
+#include "gemm16_core.hpp"
+#include "kernels.hpp"
+#include "lora_args.hpp"
+#include "stream_core.hpp"
+
+namespace omm {
+
+namespace {
+
+using namespace core16;
+
+constexpr int kSortWaves = 16;
+
+__device__ __forceinline__ int row_of(const LoraK& a, int p) { return a.perm ? a.perm[p] : p; }
+
+// Stable counting sort of the rows by adapter (bin 0: none) in one workgroup:
+// each wave counts its contiguous share of the rows per bin, a scan over (bin,
+// wave) gives every wave its place in every bin, and it writes its rows there.
+// 4096 rows of 9 bins take 6 us; the tiles that use the order take 250.
+__global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int bins) {
+    extern __shared__ int hist[];  // [wave][bin]
+    __shared__ int wsum[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int M = (int)a.M, per = (((M + kSortWaves - 1) / kSortWaves) + 63) / 64 * 64;
+    const int m0 = min(M, wave * per), m1 = min(M, m0 + per);
+    for (int i = tid; i < kSortWaves * bins; i += 64 * kSortWaves) hist[i] = 0;
+    __syncthreads();
+    int* mine = hist + wave * bins;
+    // calls f(bin, rows of that bin among the 64, whether this lane is one) for each bin present
+    auto each = [&](int m, auto f) {
+        const int b = m < m1 ? (int)row_adapter(a, m) + 1 : -1;
+        uint64_t todo = __ballot(b >= 0);
+        while (todo) {
+            const int lead = __ffsll((unsigned long long)todo) - 1;
+            const int bin = __builtin_amdgcn_readlane(b, lead);
+            const uint64_t in = __ballot(b == bin);
+            f(bin, in, b == bin);
+            todo &= ~in;
+        }
+    };
+    for (int m = m0 + lane; m - lane < m1; m += 64)
+        each(m, [&](int bin, uint64_t in, bool) {
+            if (lane == 0) mine[bin] += __popcll(in);
+        });
+    __syncthreads();
+    // exclusive scan in the order (bin, wave); one bin a thread (bins <= 1024)
+    int total = 0;
+    if (tid < bins)
+        for (int w = 0; w < kSortWaves; ++w) total += hist[w * bins + tid];
+    int scan = total;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(scan, d, 64);
+        if (lane >= d) scan += o;
+    }
+    if (lane == 63) wsum[wave] = scan;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) scan += wsum[w];
+    scan -= total;
+    if (tid < bins)
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int n = hist[w * bins + tid];
+            hist[w * bins + tid] = scan;
+            scan += n;
+        }
+    __syncthreads();
+    for (int m = m0 + lane; m - lane < m1; m += 64)
+        each(m, [&](int bin, uint64_t in, bool is) {
+            const int at = mine[bin];
+            if (is) a.perm[at + __popcll(in & ((1ull << lane) - 1))] = m;
+            if (lane == 0) mine[bin] = at + __popcll(in);
+        });
+}
+
+// T[p, r] = scale[g] sum_k X[m, k] A[g, k, r] of the 16 rows m at positions p0
+// .. p0 + 15 and (up to) 128 r: 8 waves split K, A and the rows go from memory
+// to the matrix unit.  One pass for each adapter among the rows.
+// fp16: tmax[p][2 (r / 128) + (r / 64) % 2] = max |T[p, r]| (for the halves' scale).
+template <int DT, int TRANS, int NF>
+__global__ __launch_bounds__(512) void lora_shrink_rows_kernel(LoraK a) {
+    typedef typename elem_of<DT>::type E;
+    __shared__ __attribute__((aligned(16))) float red[8 * NF * kFragPad];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
+    const int q = (lane >> 4) * kQ<DT>;
+    const int M = (int)a.M, K = (int)a.K, R = a.R, p0 = blockIdx.x * 16, c0 = blockIdx.y * 128;
+    const int m = row_of(a, min(p0 + i, M - 1));
+    const int ad = p0 + i < M ? (int)row_adapter(a, m) : -1;
+    StreamX<DT, 1> x;
+    x.p[0] = (const E*)a.X + (int64_t)m * K + q;
+    int s0, s1;
+    wave_steps<DT, 8>(K, 1, wave, s0, s1);
+    for (uint32_t todo = (uint32_t)__ballot(ad >= 0) & 0xffffu; todo;) {
+        const int g = __builtin_amdgcn_readlane(ad, __ffs(todo) - 1);
+        const uint32_t in = (uint32_t)__ballot(ad == g) & 0xffffu;
+        todo &= ~in;
+        const E* A = (const E*)a.A + (int64_t)g * K * R;
+        StreamW<DT, TRANS, NF> w;
+        if constexpr (TRANS) {
+            w.base[0] = w.base[1] = A;
+#pragma unroll
+            for (int j = 0; j < NF; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, R - 1) * K + q;
+        } else {
+            w.ld = R;
+            if constexpr (DT == 2) {
+                w.p[0] = A + group_start<DT>(c0, 4 * i, R) + (int64_t)q * R;
+                w.p[1] = A + group_start<DT>(c0, 64 + 4 * i, R) + (int64_t)q * R;
+            } else {
+                w.p[0] = A + group_start<DT>(c0, 8 * i, R) + (int64_t)q * R;
+            }
+        }
+        f32x4_t acc[NF][1] = {};
+        stream_run<DT, TRANS, 1>(w, x, s0, s1, K, q, acc);
+#pragma unroll
+        for (int j = 0; j < NF; ++j) *(f32x4_t*)&red[(wave * NF + j) * kFragPad + lane * 4] = acc[j][0];
+        __syncthreads();
+        const float scale = a.scale ? a.scale[g] : 1.0f;
+        for (int o = tid; o < 16 * 128; o += 512) {
+            const int c = o & 127, row = o >> 7;
+            if (!((in >> row) & 1)) continue;  // a wave has one row
+            float v = 0.0f;
+            if (c0 + c < R) {
+                int j, l, rr;
+                red_pos<DT, TRANS>(c, c0 + (c & ~(kQ<DT> - 1)) - group_start<DT>(c0, c, R), row, j, l, rr);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v += red[(u * NF + j) * kFragPad + l * 4 + rr];
+                v *= scale;
+                a.T[(int64_t)(p0 + row) * R + c0 + c] = v;
+            }
+            if constexpr (DT == 1) {
+                const uint32_t mx = wave_max_u32(__float_as_uint(fabsf(v)));
+                if (lane == 0)
+                    a.tmax[(int64_t)(p0 + row) * 2 * gridDim.y + 2 * blockIdx.y + (c >> 6)] = __uint_as_float(mx);
+            }
+        }
+        if (todo) __syncthreads();
+    }
+}
+
+// largest |T| of a position, and the power of two that takes it to [2^13, 2^14)
+__device__ __forceinline__ float row_max(const LoraK& a, int64_t p) {
+    const int n = 2 * ((a.R + 127) / 128);
+    float mx = 0.0f;
+    for (int b = 0; b < n; ++b) mx = fmaxf(mx, a.tmax[p * n + b]);
+    return mx;
+}
+__device__ __forceinline__ int scale_exp(float mx) {
+    return mx > 0.0f && mx < __builtin_inff() ? max(-100, min(100, 13 - ilogbf(mx))) : 0;
+}
+
+// Y[m, n] = bias[n] + sum_r T[p, r] B[g, r, n], a wave 16 positions and 128 columns
+template <int DT, int TRANS>
+__global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
+    typedef typename elem_of<DT>::type E;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = (lane >> 4) * kQ<DT>;
+    const int M = (int)a.M, N = (int)a.N, R = a.R, c0 = blockIdx.x * 128;
+    const int64_t pw = ((int64_t)blockIdx.y * 4 + wave) * 16;
+    if (pw >= M) return;
+    const int p = (int)min(pw + i, (int64_t)M - 1), m = row_of(a, p);
+    const int ad = (int)row_adapter(a, m);
+    typename std::conditional<DT == 2, StreamX<2, 1>, StreamX32<DT, 1>>::type x;
+    x.p[0] = a.T + (int64_t)p * R + q;
+    float undo = 1.0f;
+    if constexpr (DT == 1) {
+        const int e = ad >= 0 ? scale_exp(row_max(a, p)) : 0;
+        x.scale[0] = ldexpf(1.0f, e);
+        undo = ldexpf(1.0f, -e);
+    }
+    f32x4_t res[8] = {};
+    for (uint32_t todo = (uint32_t)__ballot(ad >= 0) & 0xffffu; todo;) {
+        const int g = __builtin_amdgcn_readlane(ad, __ffs(todo) - 1);
+        todo &= ~(uint32_t)__ballot(ad == g);
+        const E* B = (const E*)a.B + (int64_t)g * R * N;
+        StreamW<DT, TRANS> w;
+        if constexpr (TRANS) {
+            w.base[0] = w.base[1] = B;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, N - 1) * R + q;
+        } else {
+            w.ld = N;
+            if constexpr (DT == 2) {
+                w.p[0] = B + group_start<DT>(c0, 4 * i, N) + (int64_t)q * N;
+                w.p[1] = B + group_start<DT>(c0, 64 + 4 * i, N) + (int64_t)q * N;
+            } else {
+                w.p[0] = B + group_start<DT>(c0, 8 * i, N) + (int64_t)q * N;
+            }
+        }
+        f32x4_t acc[8][1] = {};
+        stream_run<DT, TRANS, 1>(w, x, 0, (R + kStep<DT> - 1) / kStep<DT>, R, q, acc);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) res[j][e] = ad == g ? acc[j][0][e] * undo : res[j][e];
+    }
+    if (pw + i >= M) return;
+    E* y = (E*)a.Y + (int64_t)m * N;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = (lane >> 4) * 4 + e;  // the lane's fragment column
+            int n;
+            if constexpr (TRANS)
+                n = c0 + 16 * j + t;
+            else if constexpr (DT == 2)
+                n = group_start<DT>(c0, 64 * (j >> 2) + 4 * t, N) + (j & 3);
+            else
+                n = group_start<DT>(c0, 8 * t, N) + j;
+            if (n < N) y[n] = f32_elem<DT>(res[j][e] + (a.bias ? elem_f32<DT>(((const E*)a.bias)[n]) : 0.0f));
+        }
+}
+
+// BT x BT tiles of Y over the sorted rows: the dense product's K loop
+// (mainloop_dma16, rows of X gathered through the order), then T B block by
+// block from registers.
+// BKM: W (N, K), B (G, N, R); else W (K, N), B (G, R, N).
+template <int DT, bool BKM, int BT>
+__global__ __launch_bounds__(NT) void lora_tile_kernel(LoraK a, int tiles_m, int tiles_n) {
+    constexpr int BM = BT, BN = BT, TM = BM / 32, TN = BN / 32;
+    constexpr int STAGE = (BM + BN) * KSTEP * 2;
+    __shared__ __attribute__((aligned(1024))) char smem0[STAGE];
+    __shared__ __attribute__((aligned(1024))) char smem1[STAGE];
+    __shared__ int row_s[BM], ad_s[BM];
+    __shared__ float max_s[DT == 1 ? BM : 1];
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int w = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+    int tm, tn;
+    grouped_order(w, tiles_m, tiles_n, 4, tm, tn);
+    const int M = (int)a.M, N = (int)a.N, K = (int)a.K, R = a.R;
+    const int m0 = tm * BM, n0 = tn * BN;
+    for (int r = t; r < BM; r += NT) {
+        const int p = m0 + r, m = p < M ? row_of(a, p) : -1, ad = m < 0 ? -1 : (int)row_adapter(a, m);
+        row_s[r] = m;
+        ad_s[r] = ad;
+        if constexpr (DT == 1) max_s[r] = ad < 0 ? 0.0f : row_max(a, p);
+    }
+    __syncthreads();
+    GatherDma<BM> srcA;
+    srcA.base = (const char*)a.X;
+    srcA.K = K;
+    srcA.lane = lane;
+#pragma unroll
+    for (int j = 0; j < GatherDma<BM>::PER_WAVE; ++j) {
+        const int m = row_s[GatherDma<BM>::row_of(wave, j, lane)];
+        srcA.roff[j] = m >= 0 ? (uint32_t)m * (uint32_t)K * 2u + (GatherDma<BM>::chunk(j, lane) << 4) : DMA_OOB;
+    }
+    DmaSrc<BN, BKM> srcB;
+    srcB.init(a.W, BKM ? K : N, n0, N, K, lane);
+    f32x4_t acc[TM][TN];
+    const int nk = (K + KSTEP - 1) / KSTEP;
+    if (n0 + BN <= N && K % KSTEP == 0)
+        mainloop_dma16<BM, BN, DT, true, BKM, false>(acc, smem0, smem1, srcA, srcB, nk, lane, wm, wn, wave);
+    else
+        mainloop_dma16<BM, BN, DT, true, BKM, true>(acc, smem0, smem1, srcA, srcB, nk, lane, wm, wn, wave);
+
+    // d = T B of block i of the wave (rows 16 i .. + 15, in the accumulators'
+    // layout), one adapter of the block after another.  Lane l: row l % 16, r =
+    // r0 + 8 (l / 16) .. + 7.  The accumulators themselves are only read: an
+    // epilogue that multiplied into them made the compiler spill them.
+    const int i16 = lane & 15, q = (lane >> 4) * 8, row0 = wm * (BM / 2), col0 = wn * (BN / 2);
+    const uint16_t* Bp = (const uint16_t*)a.B;
+    u32x4_t bf[TN];  // B's fragments, kept from block to block where one step covers R
+    int held = -1;
+    auto load_b = [&](int g, int r0, int n) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int col = min(n0 + col0 + 16 * j + i16, N - 1);
+            if constexpr (BKM) {
+                bf[j] = load16_first(Bp + ((int64_t)g * N + col) * R + r0 + q, n);
+            } else {
+                bf[j] = u32x4_t{0, 0, 0, 0};
+                const uint16_t* b = Bp + ((int64_t)g * R + r0 + q) * N + col;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n) bf[j][e >> 1] |= (uint32_t)b[(int64_t)e * N] << (16 * (e & 1));
+                fence_sched();  // 8 loads at a time: all 64 would spill
+            }
+        }
+    };
+    auto delta = [&](int i, f32x4_t (&d)[TN]) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) d[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        const int ad = ad_s[row0 + 16 * i + i16];
+        const float* tp = a.T + (int64_t)min(m0 + row0 + 16 * i + i16, M - 1) * R + q;
+        float scale = 1.0f, undo = 1.0f;
+        if constexpr (DT == 1) {
+            const int e = scale_exp(max_s[row0 + 16 * i + i16]);
+            scale = ldexpf(1.0f, e);
+            undo = ldexpf(1.0f, -e);
+        }
+        for (uint32_t todo = (uint32_t)__ballot(ad >= 0) & 0xffffu; todo;) {
+            const int g = __builtin_amdgcn_readlane(ad, __ffs(todo) - 1);
+            todo &= ~(uint32_t)__ballot(ad == g);
+            f32x4_t v[TN] = {};
+            for (int r0 = 0; r0 < R; r0 += 32) {
+                const int n = max(0, min(8, R - r0 - q));
+                const u32x4_t raw[2] = {load16_first(tp + r0, n), load16_first(tp + r0 + 4, n - 4)};
+                if (held != g) load_b(g, r0, n);
+                if (R <= 32) held = g;
+                u32x4_t hi, lo;
+                split_halves<DT>(raw, scale, hi, lo);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    v[j] = mfma16x16x32<DT>(bf[j], hi, v[j]);
+                    v[j] = mfma16x16x32<DT>(bf[j], lo, v[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[j][e] = ad == g ? v[j][e] * undo : d[j][e];
+        }
+    };
+
+    uint16_t* Y = (uint16_t*)a.Y;
+    const uint16_t* bias = (const uint16_t*)a.bias;
+    if constexpr (BT == 256) {
+        // whole tiles leave through LDS as whole row segments (16-byte chunk c
+        // of row r in slot c ^ (r % 16))
+        if (n0 + BN <= N && N % 8 == 0 && ((uintptr_t)Y & 15) == 0) {
+            __syncthreads();  // every wave is done reading the last stage
+            char* stage = (wave < 2 ? smem0 : smem1) + (wave & 1) * (STAGE / 2);
+            const int h = lane >> 4;
+            static_for<0, TM>([&](auto ic) {
+                constexpr int i = decltype(ic)::value;
+                f32x4_t d[TN];
+                delta(i, d);
+                const int r = 16 * i + i16;
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int n = n0 + col0 + 16 * j + 4 * h, c = 2 * j + (h >> 1);
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e] + d[j][e] + (bias ? from_bits<DT>(bias[n + e]) : 0.0f);
+                    *(u32x2_t*)(stage + r * 256 + ((c ^ i16) << 4) + ((h & 1) << 3)) =
+                        u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+                }
+            });
+            uint16_t* yb = Y + n0 + col0 + 8 * (lane & 15);
+#pragma unroll 8
+            for (int k = 0; k < 4 * TM; ++k) {
+                const int r = 4 * k + (lane >> 4), m = row_s[row0 + r];
+                const u32x4_t d = *(const u32x4_t*)(stage + r * 256 + (((lane & 15) ^ (r % 16)) << 4));
+                if (m >= 0) *(u32x4_t*)(yb + (int64_t)m * N) = d;
+            }
+            return;
+        }
+    }
+    static_for<0, TM>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        f32x4_t d[TN];
+        delta(i, d);
+        const int m = row_s[row0 + 16 * i + i16];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int n = n0 + col0 + 16 * j + 4 * (lane >> 4);
+            if (m < 0 || n >= N) continue;
+            uint16_t* y = Y + (int64_t)m * N + n;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = acc[i][j][e] + d[j][e] + (bias && n + e < N ? from_bits<DT>(bias[n + e]) : 0.0f);
+            if (n + 4 <= N) {
+                typedef u32x2_t u32x2_u2 __attribute__((aligned(2)));
+                *(u32x2_u2*)y = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < N) y[e] = to_bits<DT>(v[e]);
+            }
+        }
+    });
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int DT, int TRANS>
+void shrink(const LoraK& a, hipStream_t s) {
+    const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)((a.R + 127) / 128));
+    if constexpr (TRANS) {
+        if (a.R <= 16) return lora_shrink_rows_kernel<DT, 1, 1><<<grid, 512, 0, s>>>(a);
+        if (a.R <= 32) return lora_shrink_rows_kernel<DT, 1, 2><<<grid, 512, 0, s>>>(a);
+        if (a.R <= 64) return lora_shrink_rows_kernel<DT, 1, 4><<<grid, 512, 0, s>>>(a);
+    }
+    lora_shrink_rows_kernel<DT, TRANS, 8><<<grid, 512, 0, s>>>(a);
+}
+
+template <int DT, int TRANS>
+void expand(const LoraK& a, hipStream_t s) {
+    const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)((a.M + 63) / 64));
+    lora_expand_kernel<DT, TRANS><<<grid, 256, 0, s>>>(a);
+}
+
+template <int DT, int TRANS>
+hipError_t rows_run(const LoraK& a, hipStream_t s) {
+    if (a.perm && a.R > 0 && a.G > 0)
+        lora_sort_kernel<<<1, 64 * kSortWaves, kSortWaves * (a.G + 1) * sizeof(int), s>>>(a, (int)a.G + 1);
+    if (a.R > 0 && a.G > 0) shrink<DT, TRANS>(a, s);
+    if constexpr (DT < 2) {
+        // 16-byte rows for the DMA, 32-bit byte offsets into X and a tile of W
+        const bool dma = a.K % 8 == 0 && a.K > 0 && (TRANS || a.N % 8 == 0) &&
+                         (((uintptr_t)a.X | (uintptr_t)a.W) & 15) == 0 && a.M * a.K * 2 < (1LL << 31) &&
+                         256 * (TRANS ? a.K : a.N) * 2 < (1LL << 31);
+        if (dma) {
+            const int64_t big = (a.M + 255) / 256 * ((a.N + 255) / 256);
+            if (big >= 256) {
+                const int tm = (int)((a.M + 255) / 256), tn = (int)((a.N + 255) / 256);
+                log_choice("lora_matmul: 256x256 tiles over sorted rows");
+                lora_tile_kernel<DT, TRANS != 0, 256><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
+            } else {
+                const int tm = (int)((a.M + 127) / 128), tn = (int)((a.N + 127) / 128);
+                log_choice("lora_matmul: 128x128 tiles over sorted rows");
+                lora_tile_kernel<DT, TRANS != 0, 128><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
+            }
+            return hipGetLastError();
+        }
+    }
+    log_choice("lora_matmul: adapters into Y, then the dense product");
+    expand<DT, TRANS>(a, s);
+    hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : lora_add_dense(a, a.Y, DT, s);
+}
+
+}  // namespace
+
+// whole groups of 8 (columns of a fp32 group: 4), one adapter's matrices within
+// 32-bit offsets, tile counts and rows in 32 bits
+bool lora_rows_ok(int64_t M, int64_t K, int64_t N, int64_t R, int64_t G, int trans) {
+    return K >= 8 && N >= 8 && (trans || R >= 8 || R == 0) && K * R < (1LL << 30) && N * R < (1LL << 30) &&
+           K < (1 << 30) && N < (1 << 30) && G < (1LL << 31) - 1 && M < (1LL << 30) &&
+           (M + 127) / 128 * ((N + 127) / 128) < (1LL << 31) && (M + 63) / 64 < 65536 * 64;
+}
+
+size_t lora_rows_workspace_bytes(int64_t M, int64_t R) {
+    return align256((size_t)M * 4) + align256((size_t)M * 2 * ((R + 127) / 128) * 4) + align256((size_t)M * R * 4);
+}
+
+hipError_t launch_lora_rows(LoraK a, int dt, void* ws, hipStream_t s) {
+    char* w = (char*)ws;
+    a.perm = a.G < 1024 ? (int32_t*)w : nullptr;  // (more adapters than the sort has counters for: rows as they come)
+    w += align256((size_t)a.M * 4);
+    a.tmax = (float*)w;
+    w += align256((size_t)a.M * 2 * ((a.R + 127) / 128) * 4);
+    a.T = (float*)w;
+    if (a.R == 0 || a.G == 0) a.perm = nullptr;
+    switch (dt * 2 + a.trans) {
+        case 0: return rows_run<0, 0>(a, s);
+        case 1: return rows_run<0, 1>(a, s);
+        case 2: return rows_run<1, 0>(a, s);
+        case 3: return rows_run<1, 1>(a, s);
+        case 4: return rows_run<2, 0>(a, s);
+        default: return rows_run<2, 1>(a, s);
+    }
+}
+
+}  // namespace omm

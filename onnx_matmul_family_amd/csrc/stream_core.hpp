@@ -1,7 +1,7 @@
 // Products of a few rows with a streamed weight matrix: the weights pass from
 // memory to the matrix unit once, with no LDS staging.
 //
-// A wave computes 8 fragments of 16 weight columns against groups of 16 rows,
+// A wave computes NF (8, or fewer with TRANS = 1) fragments of 16 weight columns against groups of 16 rows,
 // over a range of the contraction axis.  The weights are the instruction's
 // first operand, the rows its second, so lane l's results are row l % 16,
 // columns 4 (l / 16) + r of a fragment.
@@ -79,23 +79,25 @@ __device__ __forceinline__ f32x4_t mfma16x16x32(u32x4_t a, u32x4_t b, f32x4_t c)
 // the upper 64), and ld, the row stride.  Both include the lane's contraction
 // offset kQ (l / 16).  Bases, ld and kb are uniform over the wave (scalar
 // registers).  tail: only the first n (0 .. kQ) of the lane's contraction.
-template <int DT, int TRANS>
+template <int DT, int TRANS, int NF = 8>
 struct StreamW {
     typedef typename elem_of<DT>::type E;
+    static constexpr int FRAGS = NF;
     const E* base[2];
-    uint32_t off[8];
-    __device__ __forceinline__ void load(u32x4_t (&w)[8], int kb) const {
+    uint32_t off[NF];
+    __device__ __forceinline__ void load(u32x4_t (&w)[NF], int kb) const {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = load16(base[j >> 2] + kb + off[j]);
+        for (int j = 0; j < NF; ++j) w[j] = load16(base[j >> 2] + kb + off[j]);
     }
-    __device__ __forceinline__ void tail(u32x4_t (&w)[8], int kb, int n) const {
+    __device__ __forceinline__ void tail(u32x4_t (&w)[NF], int kb, int n) const {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = load16_first(base[j >> 2] + kb + off[j], n);
+        for (int j = 0; j < NF; ++j) w[j] = load16_first(base[j >> 2] + kb + off[j], n);
     }
 };
 template <int DT>
-struct StreamW<DT, 0> {
+struct StreamW<DT, 0, 8> {
     typedef typename elem_of<DT>::type E;
+    static constexpr int FRAGS = 8;
     const E* p[DT == 2 ? 2 : 1];
     int64_t ld;
     __device__ __forceinline__ const E* at(int kb, int t) const {
@@ -115,8 +117,8 @@ struct StreamW<DT, 0> {
 };
 
 // bf16 / fp16: a lane's operand of fragment j
-template <int TRANS>
-__device__ __forceinline__ u32x4_t stream_frag(const u32x4_t (&w)[8], int j) {
+template <int TRANS, int NF>
+__device__ __forceinline__ u32x4_t stream_frag(const u32x4_t (&w)[NF], int j) {
     if constexpr (TRANS) {
         return w[j];
     } else {
@@ -198,25 +200,29 @@ struct StreamX32 {
     }
 };
 
-template <int DT, int TRANS, int NG, typename X>
-__device__ __forceinline__ void stream_step(const u32x4_t (&w)[8], const u32x4_t (&r)[NG][X::RAW], const X& x,
-                                            f32x4_t (&acc)[8][NG]) {
+template <int DT, int TRANS, int NG, int NF, typename X>
+__device__ __forceinline__ void stream_step(const u32x4_t (&w)[NF], const u32x4_t (&r)[NG][X::RAW], const X& x,
+                                            f32x4_t (&acc)[NF][NG]) {
     u32x4_t o[NG][X::PARTS];
 #pragma unroll
     for (int g = 0; g < NG; ++g) x.operand(r[g], g, o[g]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < NF; ++j) {
         if constexpr (DT == 2) {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    const uint32_t wv = TRANS ? w[j][t] : w[(j >> 2) * 4 + t][j & 3];
+                    uint32_t wv;
+                    if constexpr (TRANS)
+                        wv = w[j][t];
+                    else
+                        wv = w[(j >> 2) * 4 + t][j & 3];
                     acc[j][g] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(wv), __uint_as_float(o[g][0][t]),
                                                                      acc[j][g], 0, 0, 0);
                 }
         } else {
-            const u32x4_t f = stream_frag<TRANS>(w, j);
+            const u32x4_t f = stream_frag<TRANS, NF>(w, j);
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -229,12 +235,12 @@ __device__ __forceinline__ void stream_step(const u32x4_t (&w)[8], const u32x4_t
 // may be partial: the lanes take zeros past kn).  q = kQ (l / 16).
 // Two register sets: the loads of a step are in flight while the one before
 // it multiplies.  `meanwhile` runs while the first loads are on their way.
-template <int DT, int TRANS, int NG, typename X, typename F>
-__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS>& w, const X& x, int s0, int s1, int kn, int q,
-                                           f32x4_t (&acc)[8][NG], F meanwhile) {
+template <int DT, int TRANS, int NG, typename X, int NF, typename F>
+__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS, NF>& w, const X& x, int s0, int s1, int kn, int q,
+                                           f32x4_t (&acc)[NF][NG], F meanwhile) {
     constexpr int ST = kStep<DT>;
     const int full = min(s1, kn / ST);
-    u32x4_t wa[8], wb[8], xa[NG][X::RAW], xb[NG][X::RAW];
+    u32x4_t wa[NF], wb[NF], xa[NG][X::RAW], xb[NG][X::RAW];
     int s = s0;
     if (s < full) {
         w.load(wa, s * ST);
@@ -244,28 +250,28 @@ __device__ __forceinline__ void stream_run(const StreamW<DT, TRANS>& w, const X&
     for (; s + 2 <= full; s += 2) {
         w.load(wb, s * ST + ST);
         x.load(xb, s * ST + ST);
-        stream_step<DT, TRANS, NG>(wa, xa, x, acc);
+        stream_step<DT, TRANS, NG, NF>(wa, xa, x, acc);
         if (s + 2 < full) {
             w.load(wa, s * ST + 2 * ST);
             x.load(xa, s * ST + 2 * ST);
         }
-        stream_step<DT, TRANS, NG>(wb, xb, x, acc);
+        stream_step<DT, TRANS, NG, NF>(wb, xb, x, acc);
     }
     if (s < full) {
-        stream_step<DT, TRANS, NG>(wa, xa, x, acc);
+        stream_step<DT, TRANS, NG, NF>(wa, xa, x, acc);
         ++s;
     }
     if (s < s1 && s * ST < kn) {  // partial last step
         const int n = max(0, min(kQ<DT>, kn - s * ST - q));
         w.tail(wa, s * ST, n);
         x.tail(xa, s * ST, n);
-        stream_step<DT, TRANS, NG>(wa, xa, x, acc);
+        stream_step<DT, TRANS, NG, NF>(wa, xa, x, acc);
     }
 }
 
-template <int DT, int TRANS, int NG, typename X>
-__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS>& w, const X& x, int s0, int s1, int kn, int q,
-                                           f32x4_t (&acc)[8][NG]) {
+template <int DT, int TRANS, int NG, typename X, int NF>
+__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS, NF>& w, const X& x, int s0, int s1, int kn, int q,
+                                           f32x4_t (&acc)[NF][NG]) {
     stream_run<DT, TRANS, NG>(w, x, s0, s1, kn, q, acc, [] {});
 }
 
