@@ -187,14 +187,14 @@ __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
     __shared__ __attribute__((aligned(16))) float red[8 * 8 * kFragPad];
     __shared__ float ex[16 * NG][128];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
-    const int q = (lane >> 4) * kQ<DT>, sp = blockIdx.y;
+    const int q = (lane >> 4) * kQ<DT>, tr = x_row<TRANS>(lane), tq = x_off<DT, TRANS>(lane), sp = blockIdx.y;
     const int M = (int)a.M, K = (int)a.K, N = (int)a.N, c0 = blockIdx.x * 128;
     StreamW<DT, TRANS> w;
     const E* wp = (const E*)a.W;
     if constexpr (TRANS) {
         w.base[0] = w.base[1] = wp;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, N - 1) * K + q;
+        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + tr, N - 1) * K + tq;
     } else {
         w.ld = N;
         if constexpr (DT == 2) {
@@ -204,13 +204,13 @@ __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
             w.p[0] = wp + group_start<DT>(c0, 8 * i, N) + (int64_t)q * N;
         }
     }
-    StreamX<DT, NG> x;  // rows past the last are the last one: their results are not used
+    StreamX<DT, TRANS, NG> x;  // rows past the last are the last one: their results are not used
 #pragma unroll
-    for (int g = 0; g < NG; ++g) x.p[g] = (const E*)a.X + (int64_t)min(16 * g + i, M - 1) * K + q;
+    for (int g = 0; g < NG; ++g) x.p[g] = (const E*)a.X + (int64_t)min(16 * g + tr, M - 1) * K + tq;
     f32x4_t acc[8][NG] = {};
     int s0, s1;
     wave_steps<DT, 8>(K, TRANS, wave, s0, s1, a.splits, sp);
-    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, q, acc, [&] { lora_expand<DT, TRANS>(a, sp, c0, ex, tid); });
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, acc, (u32x4_t*)&red[red_index(wave, 0, 0, 0)], lane, [&] { lora_expand<DT, TRANS>(a, sp, c0, ex, tid); });
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g) __syncthreads();

@@ -91,22 +91,22 @@ __global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int
 }
 
 // T[p, r] = scale[g] sum_k X[m, k] A[g, k, r] of the 16 rows m at positions p0
-// .. p0 + 15 and (up to) 128 r: 8 waves split K, A and the rows go from memory
+// .. p0 + 15 and (up to) 128 r: NW waves split K, A and the rows go from memory
 // to the matrix unit.  One pass for each adapter among the rows.
 // fp16: tmax[p][2 (r / 128) + (r / 64) % 2] = max |T[p, r]| (for the halves' scale).
-template <int DT, int TRANS, int NF>
-__global__ __launch_bounds__(512) void lora_shrink_rows_kernel(LoraK a) {
+template <int DT, int TRANS, int NF, int NW>
+__global__ __launch_bounds__(64 * NW) void lora_shrink_rows_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
-    __shared__ __attribute__((aligned(16))) float red[8 * NF * kFragPad];
+    __shared__ __attribute__((aligned(16))) float red[NW * NF * kFragPad];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
-    const int q = (lane >> 4) * kQ<DT>;
+    const int q = (lane >> 4) * kQ<DT>, tr = x_row<TRANS>(lane), tq = x_off<DT, TRANS>(lane);
     const int M = (int)a.M, K = (int)a.K, R = a.R, p0 = blockIdx.x * 16, c0 = blockIdx.y * 128;
     const int m = row_of(a, min(p0 + i, M - 1));
     const int ad = p0 + i < M ? (int)row_adapter(a, m) : -1;
-    StreamX<DT, 1> x;
-    x.p[0] = (const E*)a.X + (int64_t)m * K + q;
+    StreamX<DT, TRANS, 1> x;
+    x.p[0] = (const E*)a.X + (int64_t)__shfl(m, tr, 64) * K + tq;
     int s0, s1;
-    wave_steps<DT, 8>(K, 1, wave, s0, s1);
+    wave_steps<DT, NW>(K, 1, wave, s0, s1);
     for (uint32_t todo = (uint32_t)__ballot(ad >= 0) & 0xffffu; todo;) {
         const int g = __builtin_amdgcn_readlane(ad, __ffs(todo) - 1);
         const uint32_t in = (uint32_t)__ballot(ad == g) & 0xffffu;
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(512) void lora_shrink_rows_kernel(LoraK a) {
         if constexpr (TRANS) {
             w.base[0] = w.base[1] = A;
 #pragma unroll
-            for (int j = 0; j < NF; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, R - 1) * K + q;
+            for (int j = 0; j < NF; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + tr, R - 1) * K + tq;
         } else {
             w.ld = R;
             if constexpr (DT == 2) {
@@ -127,12 +127,12 @@ __global__ __launch_bounds__(512) void lora_shrink_rows_kernel(LoraK a) {
             }
         }
         f32x4_t acc[NF][1] = {};
-        stream_run<DT, TRANS, 1>(w, x, s0, s1, K, q, acc);
+        stream_run<DT, TRANS, 1>(w, x, s0, s1, K, acc, (u32x4_t*)&red[wave * NF * kFragPad], lane);
 #pragma unroll
         for (int j = 0; j < NF; ++j) *(f32x4_t*)&red[(wave * NF + j) * kFragPad + lane * 4] = acc[j][0];
         __syncthreads();
         const float scale = a.scale ? a.scale[g] : 1.0f;
-        for (int o = tid; o < 16 * 128; o += 512) {
+        for (int o = tid; o < 16 * 128; o += 64 * NW) {
             const int c = o & 127, row = o >> 7;
             if (!((in >> row) & 1)) continue;  // a wave has one row
             float v = 0.0f;
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(512) void lora_shrink_rows_kernel(LoraK a) {
                 int j, l, rr;
                 red_pos<DT, TRANS>(c, c0 + (c & ~(kQ<DT> - 1)) - group_start<DT>(c0, c, R), row, j, l, rr);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v += red[(u * NF + j) * kFragPad + l * 4 + rr];
+                for (int u = 0; u < NW; ++u) v += red[(u * NF + j) * kFragPad + l * 4 + rr];
                 v *= scale;
                 a.T[(int64_t)(p0 + row) * R + c0 + c] = v;
             }
@@ -169,14 +169,16 @@ __device__ __forceinline__ int scale_exp(float mx) {
 template <int DT, int TRANS>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
+    __shared__ u32x4_t scratch[4][8 * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = (lane >> 4) * kQ<DT>;
+    const int tr = x_row<TRANS>(lane), tq = x_off<DT, TRANS>(lane);
     const int M = (int)a.M, N = (int)a.N, R = a.R, c0 = blockIdx.x * 128;
     const int64_t pw = ((int64_t)blockIdx.y * 4 + wave) * 16;
     if (pw >= M) return;
     const int p = (int)min(pw + i, (int64_t)M - 1), m = row_of(a, p);
     const int ad = (int)row_adapter(a, m);
-    typename std::conditional<DT == 2, StreamX<2, 1>, StreamX32<DT, 1>>::type x;
-    x.p[0] = a.T + (int64_t)p * R + q;
+    StreamXf<DT, TRANS, 1> x;
+    x.p[0] = a.T + (int64_t)min(pw + tr, (int64_t)M - 1) * R + x.off(lane);
     float undo = 1.0f;
     if constexpr (DT == 1) {
         const int e = ad >= 0 ? scale_exp(row_max(a, p)) : 0;
@@ -192,7 +194,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
         if constexpr (TRANS) {
             w.base[0] = w.base[1] = B;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, N - 1) * R + q;
+            for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + tr, N - 1) * R + tq;
         } else {
             w.ld = N;
             if constexpr (DT == 2) {
@@ -203,7 +205,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
             }
         }
         f32x4_t acc[8][1] = {};
-        stream_run<DT, TRANS, 1>(w, x, 0, (R + kStep<DT> - 1) / kStep<DT>, R, q, acc);
+        stream_run<DT, TRANS, 1>(w, x, 0, (R + kStep<DT> - 1) / kStep<DT>, R, acc, scratch[wave], lane);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -396,11 +398,11 @@ template <int DT, int TRANS>
 void shrink(const LoraK& a, hipStream_t s) {
     const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)((a.R + 127) / 128));
     if constexpr (TRANS) {
-        if (a.R <= 16) return lora_shrink_rows_kernel<DT, 1, 1><<<grid, 512, 0, s>>>(a);
-        if (a.R <= 32) return lora_shrink_rows_kernel<DT, 1, 2><<<grid, 512, 0, s>>>(a);
-        if (a.R <= 64) return lora_shrink_rows_kernel<DT, 1, 4><<<grid, 512, 0, s>>>(a);
+        if (a.R <= 16) return lora_shrink_rows_kernel<DT, 1, 1, 16><<<grid, 1024, 0, s>>>(a);
+        if (a.R <= 32) return lora_shrink_rows_kernel<DT, 1, 2, 16><<<grid, 1024, 0, s>>>(a);
+        if (a.R <= 64) return lora_shrink_rows_kernel<DT, 1, 4, 8><<<grid, 512, 0, s>>>(a);
     }
-    lora_shrink_rows_kernel<DT, TRANS, 8><<<grid, 512, 0, s>>>(a);
+    lora_shrink_rows_kernel<DT, TRANS, 8, 8><<<grid, 512, 0, s>>>(a);
 }
 
 template <int DT, int TRANS>

@@ -12,8 +12,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "kernels.hpp"
 #include "row_select.hpp"
 #include "stream_core.hpp"
@@ -331,7 +329,7 @@ template <int DT, int TRANS, int NG, int NWS>
 __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r, int t0, float* red, int tid) {
     typedef typename elem_of<DT>::type E;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
-    const int q = (lane >> 4) * kQ<DT>;
+    const int q = (lane >> 4) * kQ<DT>, tr = x_row<TRANS>(lane), tq = x_off<DT, TRANS>(lane);
     const int F = (int)a.F, K = (int)a.K, c0 = blockIdx.x * 64;
     const int64_t eoff = (int64_t)__builtin_amdgcn_readfirstlane(r.e) * a.K * a.F;
     const E* wg = (const E*)a.wg + eoff;
@@ -341,7 +339,7 @@ __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r,
         w.base[0] = wg;
         w.base[1] = wu;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * (j & 3) + i, F - 1) * K + q;
+        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * (j & 3) + tr, F - 1) * K + tq;
     } else {
         w.ld = F;
         if constexpr (DT == 2) {
@@ -351,14 +349,14 @@ __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r,
             w.p[0] = (i < 8 ? wg : wu) + group_start<DT>(c0, 8 * (i & 7), F) + (int64_t)q * F;
         }
     }
-    StreamX<DT, NG> x;  // rows past the last are the last one: their results are not used
+    StreamX<DT, TRANS, NG> x;  // rows past the last are the last one: their results are not used
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-        x.p[g] = (const E*)a.X + (int64_t)r.tok[min(t0 + 16 * g + i, r.n - 1)] * K + q;
+        x.p[g] = (const E*)a.X + (int64_t)r.tok[min(t0 + 16 * g + tr, r.n - 1)] * K + tq;
     f32x4_t acc[8][NG] = {};
     int s0, s1;
     wave_steps<DT, NWS>(K, TRANS, wave, s0, s1);
-    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, q, acc);
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, acc, (u32x4_t*)&red[red_index(wave, 0, 0, 0)], lane);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g) __syncthreads();
@@ -420,14 +418,14 @@ template <int DT, int TRANS, int NG, int NWS>
 __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& r, int t0, float* red, int tid) {
     typedef typename elem_of<DT>::type E;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
-    const int q = (lane >> 4) * kQ<DT>;
+    const int q = (lane >> 4) * kQ<DT>, tr = x_row<TRANS>(lane), tq = x_off<DT, TRANS>(lane);
     const int F = (int)a.F, N = (int)a.K, c0 = blockIdx.x * 128;
     const E* wd = (const E*)a.wd + (int64_t)__builtin_amdgcn_readfirstlane(r.e) * a.K * a.F;
     StreamW<DT, TRANS> w;
     if constexpr (TRANS) {
         w.base[0] = w.base[1] = wd;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + i, N - 1) * F + q;
+        for (int j = 0; j < 8; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + tr, N - 1) * F + tq;
     } else {
         w.ld = N;
         if constexpr (DT == 2) {
@@ -440,15 +438,15 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
     int s0, s1;
     const int sp = blockIdx.z;
     wave_steps<DT, NWS>(F, TRANS, wave, s0, s1, a.splits, sp);
-    typename std::conditional<DT == 2, StreamX<2, NG>, StreamX32<DT, NG>>::type x;
+    StreamXf<DT, TRANS, NG> x;
     float undo[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const int p = r.pair[min(t0 + 16 * g + i, r.n - 1)];
-        x.p[g] = a.h + (int64_t)p * F + q;
+        x.p[g] = a.h + (int64_t)r.pair[min(t0 + 16 * g + tr, r.n - 1)] * F + x.off(lane);
         undo[g] = 1.0f;
         if constexpr (DT == 1) {  // the row's largest value over this wave's range -> [2^13, 2^14)
             const int slabs = (F + 63) / 64;
+            const int p = r.pair[min(t0 + 16 * g + i, r.n - 1)];
             float mx = 0.0f;
             for (int b = s0 >> 1; b < (s1 + 1) >> 1; ++b) mx = fmaxf(mx, a.hmax[(int64_t)p * slabs + b]);
             int ex = 0;
@@ -458,7 +456,7 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
         }
     }
     f32x4_t acc[8][NG] = {};
-    stream_run<DT, TRANS, NG>(w, x, s0, s1, F, q, acc);
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, F, acc, (u32x4_t*)&red[red_index(wave, 0, 0, 0)], lane);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g) __syncthreads();

@@ -9,7 +9,7 @@
 // bf16 / fp16, v_mfma_f32_16x16x32, steps of 32 (lane l: column l % 16,
 // contraction 8 (l / 16) .. + 7):
 //   TRANS = 1: weights (columns, contraction), contraction contiguous.  A
-//     fragment's operand is one 16-byte load a lane.
+//     fragment's operand is one 16-byte load a lane (through row_tile below).
 //   TRANS = 0: weights (contraction, columns), columns contiguous.  A lane
 //     loads 16 bytes (8 columns) of each of 8 contraction rows: an 8 x 8 block
 //     whose j-th columns, paired over the rows with v_perm (half an
@@ -26,9 +26,20 @@
 // 16 bytes wide all the same), sizes no multiples: a TRANS = 0 lane whose
 // columns pass the last one starts at the last whole group instead, and the
 // tail of the contraction is loaded element by element.
+//
+// Loads of rows (the weights of TRANS = 1, and the rows X): in the operand's
+// order 16 neighbouring lanes would read 16 different rows, and the caches look
+// up a line for every lane (measured: 7 bytes a clock and CU, the rate of the
+// memory itself).  So 4 neighbouring lanes read 64 bytes of one row, and the
+// values take their operand places through LDS (1 KiB a fragment, of the wave's
+// own, no barrier).  With TRANS = 0 only the rows X are loaded like that, which
+// are few lines beside the weights': they are read in the operand's order (32
+// tokens over 64 experts: up projection 407 us, through LDS 422).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "row_select.hpp"
@@ -74,22 +85,44 @@ __device__ __forceinline__ f32x4_t mfma16x16x32(u32x4_t a, u32x4_t b, f32x4_t c)
                                                       __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
+// Row and 16-byte piece of its 64 bytes that a lane loads of a tile of 16 rows;
+// the pieces are permuted so that the read back meets every LDS bank once.
+__device__ __forceinline__ int tile_row(int lane) { return lane >> 2; }
+__device__ __forceinline__ int tile_piece(int lane) { return (lane & 3) ^ (lane >> 4); }
+// where the tile's (row, piece) is among the lanes
+__device__ __forceinline__ int tile_slot(int row, int piece) { return 4 * row + (piece ^ (row >> 2)); }
+// contraction offset of the piece
+template <int DT>
+__device__ __forceinline__ int tile_off(int lane) { return tile_piece(lane) * kQ<DT>; }
+
+// v[j] (tile j as loaded) -> lane l's 16 bytes of row l % 16, piece l / 16
+template <int N>
+__device__ __forceinline__ void row_tile(u32x4_t (&v)[N], u32x4_t* scratch, int lane) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) scratch[j * 64 + lane] = v[j];
+    __builtin_amdgcn_wave_barrier();
+    const int slot = tile_slot(lane & 15, lane >> 4);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = scratch[j * 64 + slot];
+    __builtin_amdgcn_wave_barrier();
+}
+
 // One lane's weights.  TRANS = 1: off[j], elements from base[j / 4] to the
-// lane's column of fragment j; TRANS = 0: p, the lane's columns (fp32: p[1] of
-// the upper 64), and ld, the row stride.  Both include the lane's contraction
-// offset kQ (l / 16).  Bases, ld and kb are uniform over the wave (scalar
-// registers).  tail: only the first n (0 .. kQ) of the lane's contraction.
+// tile row's column of fragment j, plus the contraction offset tile_off;
+// TRANS = 0: p, the lane's columns (fp32: p[1] of the upper 64), plus rows
+// kQ (l / 16), and ld, the row stride.  Bases, ld and kb are uniform over the
+// wave (scalar registers).  tail: of a contraction that ends at kn.
 template <int DT, int TRANS, int NF = 8>
 struct StreamW {
     typedef typename elem_of<DT>::type E;
-    static constexpr int FRAGS = NF;
     const E* base[2];
     uint32_t off[NF];
     __device__ __forceinline__ void load(u32x4_t (&w)[NF], int kb) const {
 #pragma unroll
         for (int j = 0; j < NF; ++j) w[j] = load16(base[j >> 2] + kb + off[j]);
     }
-    __device__ __forceinline__ void tail(u32x4_t (&w)[NF], int kb, int n) const {
+    __device__ __forceinline__ void tail(u32x4_t (&w)[NF], int kb, int kn, int lane) const {
+        const int n = max(0, min(kQ<DT>, kn - kb - tile_off<DT>(lane)));
 #pragma unroll
         for (int j = 0; j < NF; ++j) w[j] = load16_first(base[j >> 2] + kb + off[j], n);
     }
@@ -97,7 +130,6 @@ struct StreamW {
 template <int DT>
 struct StreamW<DT, 0, 8> {
     typedef typename elem_of<DT>::type E;
-    static constexpr int FRAGS = 8;
     const E* p[DT == 2 ? 2 : 1];
     int64_t ld;
     __device__ __forceinline__ const E* at(int kb, int t) const {
@@ -110,7 +142,8 @@ struct StreamW<DT, 0, 8> {
 #pragma unroll
         for (int t = 0; t < 8; ++t) w[t] = load16(at(kb, t));
     }
-    __device__ __forceinline__ void tail(u32x4_t (&w)[8], int kb, int n) const {
+    __device__ __forceinline__ void tail(u32x4_t (&w)[8], int kb, int kn, int lane) const {
+        const int n = kn - kb - (lane >> 4) * kQ<DT>;
 #pragma unroll
         for (int t = 0; t < 8; ++t) w[t] = (t & (kQ<DT> - 1)) < n ? load16(at(kb, t)) : u32x4_t{0, 0, 0, 0};
     }
@@ -130,21 +163,38 @@ __device__ __forceinline__ u32x4_t stream_frag(const u32x4_t (&w)[NF], int j) {
     }
 }
 
-// The rows as stored, in the operand layout
-template <int DT, int NG>
+// row of 16 and contraction offset (16-byte pieces of 4 bytes: 4 values; of T:
+// kQ) that a lane loads of the rows X
+template <int TRANS>
+__device__ __forceinline__ int x_row(int lane) { return TRANS ? tile_row(lane) : lane & 15; }
+template <int DT, int TRANS>
+__device__ __forceinline__ int x_off(int lane) { return TRANS ? tile_off<DT>(lane) : (lane >> 4) * kQ<DT>; }
+
+// The rows as stored
+template <int DT, int TRANS, int NG>
 struct StreamX {
     static constexpr int RAW = 1, PARTS = 1;
     typedef typename elem_of<DT>::type E;
-    const E* p[NG];  // the lane's row of each group, offset by kQ (l / 16)
+    const E* p[NG];  // row x_row of each group, plus off
+    __device__ __forceinline__ static int off(int lane) { return x_off<DT, TRANS>(lane); }
     __device__ __forceinline__ void load(u32x4_t (&r)[NG][1], int kb) const {
 #pragma unroll
         for (int g = 0; g < NG; ++g) r[g][0] = load16(p[g] + kb);
     }
-    __device__ __forceinline__ void tail(u32x4_t (&r)[NG][1], int kb, int n) const {
+    __device__ __forceinline__ void tail(u32x4_t (&r)[NG][1], int kb, int kn, int lane) const {
+        const int n = max(0, min(kQ<DT>, kn - kb - off(lane)));
 #pragma unroll
         for (int g = 0; g < NG; ++g) r[g][0] = load16_first(p[g] + kb, n);
     }
-    __device__ __forceinline__ void operand(const u32x4_t (&r)[1], int, u32x4_t (&o)[1]) const { o[0] = r[0]; }
+    __device__ __forceinline__ void operands(const u32x4_t (&r)[NG][1], u32x4_t (&o)[NG][1], u32x4_t* scratch,
+                                             int lane) const {
+        u32x4_t v[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) v[g] = r[g][0];
+        if constexpr (TRANS) row_tile<NG>(v, scratch, lane);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) o[g][0] = v[g];
+    }
 };
 
 // Eight fp32 values as two halves of T whose sum holds them to 16 bits of the
@@ -175,37 +225,64 @@ __device__ __forceinline__ void split_halves(const u32x4_t (&r)[2], float scale,
 // fp32 rows against bf16 / fp16 weights, as the sum of two 16-bit halves: two
 // products instead of one, which the streamed weights leave room for, and the
 // rows are not rounded to T.  fp16 rows are scaled by a power of two per row
-// (scale[g]; the caller divides it out).
-template <int DT, int NG>
+// (scale[g], of row l % 16; the caller divides it out).  Two loads a step:
+// TRANS = 1 two tiles of 16 values of the contraction each, else 8 values.
+template <int DT, int TRANS, int NG>
 struct StreamX32 {
-    static constexpr int RAW = 2, PARTS = 2;
-    const float* p[NG];
+    static constexpr int RAW = 2, PARTS = 2, NEXT = TRANS ? 16 : 4;
+    const float* p[NG];  // row x_row, plus off
     float scale[NG];
+    __device__ __forceinline__ static int off(int lane) { return TRANS ? 4 * tile_piece(lane) : (lane >> 4) * 8; }
     __device__ __forceinline__ void load(u32x4_t (&r)[NG][2], int kb) const {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             r[g][0] = load16(p[g] + kb);
-            r[g][1] = load16(p[g] + kb + 4);
+            r[g][1] = load16(p[g] + kb + NEXT);
         }
     }
-    __device__ __forceinline__ void tail(u32x4_t (&r)[NG][2], int kb, int n) const {
+    __device__ __forceinline__ void tail(u32x4_t (&r)[NG][2], int kb, int kn, int lane) const {
+        const int n = kn - kb - off(lane);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             r[g][0] = load16_first(p[g] + kb, n);
-            r[g][1] = load16_first(p[g] + kb + 4, n - 4);
+            r[g][1] = load16_first(p[g] + kb + NEXT, n - NEXT);
         }
     }
-    __device__ __forceinline__ void operand(const u32x4_t (&r)[2], int g, u32x4_t (&o)[2]) const {
-        split_halves<DT>(r, scale[g], o[0], o[1]);
+    __device__ __forceinline__ void operands(const u32x4_t (&r)[NG][2], u32x4_t (&o)[NG][2], u32x4_t* scratch,
+                                             int lane) const {
+        if constexpr (TRANS) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                scratch[2 * g * 64 + lane] = r[g][0];
+                scratch[(2 * g + 1) * 64 + lane] = r[g][1];
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+        // contraction 8 (l / 16) .. + 7: pieces 2 (l / 16) and the next of the 8
+        const int i = lane & 15, q = lane >> 4, h = (q >> 1) * 64;
+        const int s0 = h + tile_slot(i, 2 * (q & 1)), s1 = h + tile_slot(i, 2 * (q & 1) + 1);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if constexpr (TRANS) {
+                const u32x4_t v[2] = {scratch[2 * g * 64 + s0], scratch[2 * g * 64 + s1]};
+                split_halves<DT>(v, scale[g], o[g][0], o[g][1]);
+            } else {
+                split_halves<DT>(r[g], scale[g], o[g][0], o[g][1]);
+            }
+        }
+        if constexpr (TRANS) __builtin_amdgcn_wave_barrier();
     }
 };
+template <int DT, int TRANS, int NG>
+using StreamXf = typename std::conditional<DT == 2, StreamX<2, TRANS, NG>, StreamX32<DT, TRANS, NG>>::type;
 
+// (w is used up: its tiles are put in place)
 template <int DT, int TRANS, int NG, int NF, typename X>
-__device__ __forceinline__ void stream_step(const u32x4_t (&w)[NF], const u32x4_t (&r)[NG][X::RAW], const X& x,
-                                            f32x4_t (&acc)[NF][NG]) {
+__device__ __forceinline__ void stream_step(u32x4_t (&w)[NF], const u32x4_t (&r)[NG][X::RAW], const X& x,
+                                            f32x4_t (&acc)[NF][NG], u32x4_t* scratch, int lane) {
     u32x4_t o[NG][X::PARTS];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) x.operand(r[g], g, o[g]);
+    x.operands(r, o, scratch, lane);
+    if constexpr (TRANS) row_tile<NF>(w, scratch, lane);
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
         if constexpr (DT == 2) {
@@ -232,47 +309,46 @@ __device__ __forceinline__ void stream_step(const u32x4_t (&w)[NF], const u32x4_
 }
 
 // acc += steps [s0, s1) of kStep of a contraction of length kn (the last step
-// may be partial: the lanes take zeros past kn).  q = kQ (l / 16).
+// may be partial: the lanes take zeros past kn).  scratch: LDS of this wave's
+// own, 1 KiB each for the larger of NF (TRANS = 1) and NG X::RAW tiles.
 // Two register sets: the loads of a step are in flight while the one before
-// it multiplies.  `meanwhile` runs while the first loads are on their way.
+// it multiplies.  `meanwhile` runs while the first weights are on their way (it
+// may still set x).
 template <int DT, int TRANS, int NG, typename X, int NF, typename F>
-__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS, NF>& w, const X& x, int s0, int s1, int kn, int q,
-                                           f32x4_t (&acc)[NF][NG], F meanwhile) {
+__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS, NF>& w, const X& x, int s0, int s1, int kn,
+                                           f32x4_t (&acc)[NF][NG], u32x4_t* scratch, int lane, F meanwhile) {
     constexpr int ST = kStep<DT>;
     const int full = min(s1, kn / ST);
     u32x4_t wa[NF], wb[NF], xa[NG][X::RAW], xb[NG][X::RAW];
     int s = s0;
-    if (s < full) {
-        w.load(wa, s * ST);
-        x.load(xa, s * ST);
-    }
+    if (s < full) w.load(wa, s * ST);
     meanwhile();
+    if (s < full) x.load(xa, s * ST);
     for (; s + 2 <= full; s += 2) {
         w.load(wb, s * ST + ST);
         x.load(xb, s * ST + ST);
-        stream_step<DT, TRANS, NG, NF>(wa, xa, x, acc);
+        stream_step<DT, TRANS, NG, NF>(wa, xa, x, acc, scratch, lane);
         if (s + 2 < full) {
             w.load(wa, s * ST + 2 * ST);
             x.load(xa, s * ST + 2 * ST);
         }
-        stream_step<DT, TRANS, NG, NF>(wb, xb, x, acc);
+        stream_step<DT, TRANS, NG, NF>(wb, xb, x, acc, scratch, lane);
     }
     if (s < full) {
-        stream_step<DT, TRANS, NG, NF>(wa, xa, x, acc);
+        stream_step<DT, TRANS, NG, NF>(wa, xa, x, acc, scratch, lane);
         ++s;
     }
     if (s < s1 && s * ST < kn) {  // partial last step
-        const int n = max(0, min(kQ<DT>, kn - s * ST - q));
-        w.tail(wa, s * ST, n);
-        x.tail(xa, s * ST, n);
-        stream_step<DT, TRANS, NG, NF>(wa, xa, x, acc);
+        w.tail(wa, s * ST, kn, lane);
+        x.tail(xa, s * ST, kn, lane);
+        stream_step<DT, TRANS, NG, NF>(wa, xa, x, acc, scratch, lane);
     }
 }
 
 template <int DT, int TRANS, int NG, typename X, int NF>
-__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS, NF>& w, const X& x, int s0, int s1, int kn, int q,
-                                           f32x4_t (&acc)[NF][NG]) {
-    stream_run<DT, TRANS, NG>(w, x, s0, s1, kn, q, acc, [] {});
+__device__ __forceinline__ void stream_run(const StreamW<DT, TRANS, NF>& w, const X& x, int s0, int s1, int kn,
+                                           f32x4_t (&acc)[NF][NG], u32x4_t* scratch, int lane) {
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, kn, acc, scratch, lane, [] {});
 }
 
 // first column of the lane group that holds column c0 + c (c in 0 .. span) of
