@@ -56,6 +56,11 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x) return 0xffffffffu;
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
+// the same for values that are no NaN (a NaN gets some key)
+__device__ __forceinline__ uint32_t order_key_finite(float x) {
+    const int u = (int)__float_as_uint(x + 0.0f);
+    return (uint32_t)(u ^ ((u >> 31) | (int)0x80000000));
+}
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);  // the NaN key gives a NaN
 }

@@ -6,11 +6,16 @@
 // All three are kept online: a new maximum m' = m + d rescales s by e^-d and
 // turns t into e^-d (t - d s).  (t and d are held in units of log2.)
 //
-// The k largest come from the same pass: a lane's running maximum is the
-// largest of the elements that it has seen, so the k-th largest lane maximum
-// of any one wave is a lower bound T of the row part's k-th largest element.
-// Only lanes whose maximum reaches T read their elements a second time (from
-// L2) and list those >= T; the list is ranked by (value, lower index).
+// The k largest come from the same pass: a lane keeps the three largest of its
+// vectors' maxima and where they were.  The k-th largest of the workgroup's
+// lane maxima is a lower bound T of the row part's k-th largest element (values
+// and indices are ordered together, so equal values need no case of their own).
+// A lane reads its first two vectors again if they reach T, and all of its
+// elements only if the third does (with 20 of 50001 tokens: about one lane a
+// row); what reaches T is listed and ranked by (value, lower index).  Without
+// the positions every lane that reached T read all of its elements again, as
+// many cache lines as the row has: 2048 rows of 50001, 20 alternatives, 73 us,
+// of which the first pass is 38.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -51,18 +56,35 @@ __device__ __forceinline__ Stat merge(Stat a, Stat b) {
     return r;
 }
 
-template <int N>
-__device__ __forceinline__ void update(Stat& st, const float* f, int pos, int& best) {
+// The three largest of a lane's positions (a head element, vectors in order, a
+// tail element) by order key; 0: none.  Positions come in ascending order, so
+// of equal keys the first one is kept first.
+struct Top3 {
+    uint32_t k1, k2, k3;
+    int b1, b2, b3;
+    __device__ __forceinline__ void insert(uint32_t x, int pos) {
+        const bool g1 = x > k1, g2 = x > k2;
+        b3 = g2 ? b2 : x > k3 ? pos : b3;
+        k3 = max(min(x, k2), k3);
+        b2 = g1 ? b1 : g2 ? pos : b2;
+        k2 = max(min(x, k1), k2);
+        b1 = g1 ? pos : b1;
+        k1 = max(x, k1);
+    }
+};
+
+template <int N, bool TOP>
+__device__ __forceinline__ void update(Stat& st, const float* f, int pos, Top3& top) {
     float mv = f[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) mv = fmaxf(mv, f[i]);
+    if constexpr (TOP) top.insert(order_key_finite(mv), pos);
     if (mv > st.m) {
         const float d = d_log2(st.m, mv);  // -inf for the first finite value
         const float e = __builtin_amdgcn_exp2f(d);
         st.t = e * (st.t + st.s * fmaxf(d, -200.0f));
         st.s *= e;
         st.m = mv;
-        best = pos;
     }
     const float ms = safe_max(st.m);
 #pragma unroll
@@ -93,6 +115,29 @@ struct Part {
     }
 };
 
+// first and last index of a lane's position: -1 its head element, 0 .. nv - 1 a
+// vector, nv its tail element
+template <int DT>
+__device__ __forceinline__ int pos_first(const Part<DT>& p, int tid, int pos) {
+    return pos < 0 ? p.v0 + tid : pos < p.nv ? p.v0 + p.head + pos * kVec<DT> : p.tail0() + tid;
+}
+template <int DT>
+__device__ __forceinline__ int pos_last(const Part<DT>& p, int tid, int pos) {
+    return pos_first(p, tid, pos) + (pos >= 0 && pos < p.nv ? kVec<DT> - 1 : 0);
+}
+// Calls f(value, index) for the elements of a position
+template <int DT, typename F>
+__device__ __forceinline__ void for_pos(const Part<DT>& p, int tid, int pos, F f) {
+    const int v = pos_first(p, tid, pos);
+    if (pos >= 0 && pos < p.nv) {
+        float x[kVec<DT>];
+        unpack16<DT>(p.vec(pos), x);
+#pragma unroll
+        for (int i = 0; i < kVec<DT>; ++i) f(x[i], v + i);
+    } else {
+        f(elem_f32<DT>(p.row[v]), v);
+    }
+}
 // Calls f(value, index) for every element that thread `tid` of NT owns
 template <int DT, int NT, typename F>
 __device__ __forceinline__ void for_own(const Part<DT>& p, int tid, F f) {
@@ -149,16 +194,43 @@ __device__ __forceinline__ float top_logprob(uint64_t key, Stat st, float log_s)
     return x == kNegInf ? kNegInf : (x - st.m) - log_s;
 }
 
-template <int DT, int NT>
-__global__ __launch_bounds__(NT) void logprobs_kernel(LpArgs a) {
+// The k-th largest of a wave's lane maxima as one key: value T, and the largest
+// index I up to which elements of value T count (ties go to the lower index).
+// A bit a step from the top.  16 bits of the value will do, a lower T only
+// lists more; the index is looked for where many lanes have T itself.  `idx` is
+// the last index of the maximum's position (so each of the k lanes has an
+// element that counts).
+__device__ __forceinline__ uint64_t kth_lane(uint32_t x, int idx, int k) {
+    uint32_t T = 0;
+    int count = 64;  // lanes >= T
+    for (int b = 31; b >= 16; --b) {
+        const uint32_t c = T | (1u << b);
+        const int n = __popcll(__ballot(x >= c));
+        if (n >= k) {
+            T = c;
+            count = n;
+        }
+    }
+    if (count <= k + 16) return order_key64(T, 0x7fffffffu);
+    for (int b = 15; b >= 0; --b) {
+        const uint32_t c = T | (1u << b);
+        if (__popcll(__ballot(x >= c)) >= k) T = c;
+    }
+    const int more = k - __popcll(__ballot(x > T));
+    const int v = x == T ? idx : 0x7fffffff;
+    int lim = 0;  // the more-th smallest index: the largest lim with fewer below it
+    for (int b = 30; b >= 0; --b) {
+        const int c = lim | (1 << b);
+        if (__popcll(__ballot(v < c)) < more) lim = c;
+    }
+    return order_key64(T, (uint32_t)lim);
+}
+
+template <int DT, int NT, bool TOP>
+__global__ __launch_bounds__(NT, 8) void logprobs_kernel(LpArgs a) {
     typedef typename elem_of<DT>::type E;
     constexpr int NW = NT / 64;
     __shared__ Stat sh_stat[NW];
-    __shared__ uint32_t sh_thr[NW];
-    __shared__ uint64_t sh_cand[kCand];
-    __shared__ uint64_t sh_red[NW];
-    __shared__ uint64_t sh_top[kTopMax];
-    __shared__ int sh_n;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t m = blockIdx.x / a.splits;
     const int sp = (int)(blockIdx.x - m * a.splits);
@@ -166,61 +238,75 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LpArgs a) {
     const Part<DT> p((const E*)a.logits + m * (int64_t)a.V, v0, v1);
 
     Stat st = {kNegInf, 0.0f, 0.0f};
-    int best = 0;
+    Top3 top = {0, 0, 0, 0, 0, 0};
     if (tid < p.head) {
         const float f = elem_f32<DT>(p.row[p.v0 + tid]);
-        update<1>(st, &f, 0, best);
+        update<1, TOP>(st, &f, -1, top);
     }
     for (int j = tid; j < p.nv; j += NT) {
         float x[kVec<DT>];
         unpack16<DT>(p.vec(j), x);
-        update<kVec<DT>>(st, x, j, best);
+        update<kVec<DT>, TOP>(st, x, j, top);
     }
     if (p.tail0() + tid < p.v1) {
         const float f = elem_f32<DT>(p.row[p.tail0() + tid]);
-        update<1>(st, &f, 0, best);
+        update<1, TOP>(st, &f, p.nv, top);
     }
-    const float own_max = st.m;
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) {
         const Stat o = {__shfl_xor(st.m, d, 64), __shfl_xor(st.s, d, 64), __shfl_xor(st.t, d, 64)};
         st = merge(st, o);
     }
     if (lane == 0) sh_stat[wave] = st;
-
-    const uint32_t own_key = order_key(own_max);
-    if (a.k > 0) {
-        // the wave's k-th largest lane maximum, bit by bit: the largest T with
-        // at least k lanes >= T
-        uint32_t T = 0;
-        const int k = min(a.k, 64);
-        for (int b = 31; b >= 0; --b) {
-            const uint32_t c = T | (1u << b);
-            if (__popcll(__ballot(own_key >= c)) >= k) T = c;
-        }
-        if (lane == 0) sh_thr[wave] = T;
+    if constexpr (!TOP) {
+        __syncthreads();
+        st = sh_stat[0];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) st = merge(st, sh_stat[w]);
+    } else {
+        __shared__ uint64_t sh_bound[NW];
+        __shared__ uint64_t sh_cand[kCand];
+        __shared__ uint64_t sh_red[NW];
+        __shared__ uint64_t sh_top[kTopMax];
+        __shared__ int sh_n;
+        // (a wave has 64 maxima; fewer elements than k: all are listed)
+        const uint64_t bound = kth_lane(top.k1, pos_last(p, tid, top.b1), a.k);
+        if (lane == 0) sh_bound[wave] = bound;
         if (tid == 0) sh_n = 0;
-    }
-    __syncthreads();
-    st = sh_stat[0];
+        __syncthreads();
+        st = sh_stat[0];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) st = merge(st, sh_stat[w]);
-
-    if (a.k > 0) {
-        uint32_t T = sh_thr[0];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) T = max(T, sh_thr[w]);
+        for (int w = 1; w < NW; ++w) st = merge(st, sh_stat[w]);
         const bool nan_row = st.s != st.s;  // NaN is above every value, fmaxf has not seen it
         int n = kCand + 1;
         if (!nan_row) {
-            if (own_key >= T)
-                for_own<DT, NT>(p, tid, [&](float x, int v) {
-                    const uint32_t key = order_key(x);
-                    if (key >= T) {
-                        const int i = atomicAdd(&sh_n, 1);
-                        if (i < kCand) sh_cand[i] = order_key64(key, (uint32_t)v);
-                    }
-                });
+            uint64_t best = sh_bound[0];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) best = sh_bound[w] > best ? sh_bound[w] : best;
+            const uint32_t T = (uint32_t)(best >> 32);
+            const int I = (int)key64_index(best);
+            const auto list = [&](float x, int v) {
+                const uint32_t key = order_key(x);
+                if (key > T || (key == T && v <= I)) {
+                    const int i = atomicAdd(&sh_n, 1);
+                    if (i < kCand) sh_cand[i] = order_key64(key, (uint32_t)v);
+                }
+            };
+            // (key 0: no element; T = 0 where fewer than k lanes have one)
+            const auto reaches = [&](uint32_t key, int first) { return key > T || (key == T && key && first <= I); };
+            const bool one = reaches(top.k1, pos_first(p, tid, top.b1));
+            const bool two = reaches(top.k2, pos_first(p, tid, top.b2));
+            // (what comes after the third position in this order cannot reach if it does not)
+            const bool all = reaches(top.k3, pos_first(p, tid, top.b3));
+            if (one && !all) for_pos(p, tid, top.b1, list);
+            if (two && !all) for_pos(p, tid, top.b2, list);
+            // all of a lane's elements: the wave reads them, a vector a lane
+            for (uint64_t todo = __ballot(all); todo; todo &= todo - 1) {
+                const int t = wave * 64 + __ffsll((unsigned long long)todo) - 1;
+                for (int j = t + NT * lane; j < p.nv; j += NT * 64) for_pos(p, t, j, list);
+                if (lane == 0 && t < p.head) for_pos(p, t, -1, list);
+                if (lane == 1 && p.tail0() + t < p.v1) for_pos(p, t, p.nv, list);
+            }
             __syncthreads();
             n = sh_n;
         }
@@ -233,7 +319,7 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LpArgs a) {
                 if (r < kk) sh_top[r] = key;
             }
             __syncthreads();
-        } else {  // many equal values, or NaN: the largest key below the last one, k times
+        } else {  // NaN, or more candidates than fit: the largest key below the last one, k times
             uint64_t last = ~0ull;
             for (int r = 0; r < kk; ++r) {
                 uint64_t mx = 0;
@@ -289,13 +375,18 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LpArgs a) {
     const float log_s = logf(st.s);
     if (lane == 0) write_row<DT>(a, m, st, log_s);
     if (a.k == 0) return;
-    const uint64_t* keys = a.part_key + (m * a.splits + lane) * a.k;
+    __shared__ uint64_t keys[kSplitMax * kTopMax];
+    for (int i = lane; i < a.splits * a.k; i += 64) keys[i] = a.part_key[m * a.splits * a.k + i];
+    __syncthreads();
     int h = 0;
-    uint64_t head = lane < a.splits ? keys[0] : 0, mine = 0;
+    uint64_t head = lane < a.splits ? keys[lane * a.k] : 0, mine = 0;
     for (int r = 0; r < a.k; ++r) {
-        const uint64_t mx = wave_max(head);
+        // (value, then index: two 32-bit maxima by DPP)
+        const uint32_t hi = wave_max_u32((uint32_t)(head >> 32));
+        const uint32_t lo = wave_max_u32((uint32_t)(head >> 32) == hi ? (uint32_t)head : 0);
+        const uint64_t mx = ((uint64_t)hi << 32) | lo;
         if (lane == r) mine = mx;
-        if (head == mx) head = ++h < a.k ? keys[h] : 0;  // keys are distinct: one lane
+        if (head == mx) head = ++h < a.k ? keys[lane * a.k + h] : 0;  // keys are distinct: one lane
     }
     if (lane < a.k) {
         a.top_ids[m * a.k + lane] = (int32_t)key64_index(mine);
@@ -419,9 +510,14 @@ hipError_t launch_token_logprobs(const TokenLogprobsArgs& t, int dt, void* ws, h
     a.part_key = (uint64_t*)((char*)ws + (size_t)t.M * a.splits * 16);
     log_choice("token_logprobs: %d part(s) of %d a row", a.splits, a.chunk);
     const dim3 grid((unsigned)(t.M * a.splits));
-    if (dt == 0) logprobs_kernel<0, 256><<<grid, 256, 0, s>>>(a);
-    else if (dt == 1) logprobs_kernel<1, 256><<<grid, 256, 0, s>>>(a);
-    else logprobs_kernel<2, 256><<<grid, 256, 0, s>>>(a);
+    switch (dt * 2 + (a.k > 0)) {
+        case 0: logprobs_kernel<0, 256, false><<<grid, 256, 0, s>>>(a); break;
+        case 1: logprobs_kernel<0, 256, true><<<grid, 256, 0, s>>>(a); break;
+        case 2: logprobs_kernel<1, 256, false><<<grid, 256, 0, s>>>(a); break;
+        case 3: logprobs_kernel<1, 256, true><<<grid, 256, 0, s>>>(a); break;
+        case 4: logprobs_kernel<2, 256, false><<<grid, 256, 0, s>>>(a); break;
+        default: logprobs_kernel<2, 256, true><<<grid, 256, 0, s>>>(a); break;
+    }
     if (a.splits > 1) {
         const dim3 jg((unsigned)t.M);
         if (dt == 0) logprobs_join_kernel<0><<<jg, 64, 0, s>>>(a);
