@@ -19,5 +19,6 @@ _BINDING = ("matmul", "gemm", "gemm_noalloc", "qlinear_matmul", "grouped_matmul"
 def __getattr__(name):
     if name in _BINDING:
         from . import _omm
-        return getattr(_omm, name)
+        value = globals()[name] = getattr(_omm, name)  # (found without this function from now on)
+        return value
     raise AttributeError(name)

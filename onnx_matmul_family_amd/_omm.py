@@ -9,7 +9,6 @@ GPU tensor, the call raises.
 """
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -64,7 +63,6 @@ def lib():
         L.omm_grouped_matmul_check.argtypes = [vp, vp, i64p]
         L.omm_grouped_matmul_dequant.argtypes = [P, P, P, P, ctypes.c_int64, P, P, P, vp, ctypes.c_size_t, vp]
         i64, sz = ctypes.c_int64, ctypes.c_size_t
-        # (descriptors as packed bytes: _ref)
         L.omm_lora_matmul_workspace_size.restype = sz
         L.omm_lora_matmul_workspace_size.argtypes = [i64] * 4 + [ctypes.c_int32]
         L.omm_lora_matmul.argtypes = [vp] * 7 + [ci, vp, vp, sz, vp]
@@ -235,42 +233,28 @@ def grouped_matmul_check(workspace, stream=None):
 ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 
-# The same descriptor as packed bytes, and the stream as its handle: these
-# operators run for a few microseconds at a time, and the call around them must
-# not take longer (a tensor 0.6 us against 0.8 for a ctypes structure, the
-# stream 0.2 against 2.7 us for a stream object).
-_PACK = struct.Struct("=Qii8q").pack
-_NO_DIMS = tuple((0,) * (MAX_DIMS - n) for n in range(MAX_DIMS + 1))
+# Marshalled by _native.so (csrc/binding.cpp), which costs a call of a few
+# microseconds less than the ctypes calls above do.
+
+_native = None
 
 
-def _ref(x):
-    """x's descriptor (None stays None), with the checks of describe."""
-    if x is None:
-        return None
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("expected a torch.Tensor")
-    if not x.is_cuda:
-        raise ValueError("tensor must be on the GPU")
-    if not x.is_contiguous():
-        raise ValueError("tensor must be contiguous (row-major)")
-    shape = x.shape
-    n = len(shape)
-    if n > MAX_DIMS:
-        raise ValueError("at most %d dims" % MAX_DIMS)
-    return _PACK(x.data_ptr(), _DT[x.dtype], n, *shape, *_NO_DIMS[n])
+def native():
+    """The loaded binding of the decode-side operators; raises if it has not been built."""
+    global _native
+    if _native is None:
+        lib()
+        try:
+            from . import _native as module
+        except ImportError as e:
+            raise RuntimeError("_native.so is not built (run: python -m onnx_matmul_family_amd.build): %s" % e)
+        module.load(LIB_PATH, OmmError)
+        _native = module
+    return _native
 
 
-def _raw_stream(stream, x):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(x.device.index)
-
-
-def _workspace(workspace, need, device):
-    """(workspace, pointer, bytes); `need` is called only where none is given."""
-    if workspace is None:
-        workspace = torch.empty(max(need(), 256), dtype=torch.uint8, device=device)
-    return workspace, workspace.data_ptr(), workspace.nbytes
+def _handle(stream):
+    return stream.cuda_stream if stream is not None else None
 
 
 def lora_matmul_workspace_size(M, K, N, R, dtype):
@@ -283,30 +267,15 @@ def lora_matmul(X, W, A, B, adapter_indices, adapter_scale=None, bias=None, tran
 
     trans=0: W (K, N), A (G, K, R), B (G, R, N); trans=1: W (N, K), A (G, R, K), B (G, N, R).
     A row whose index is outside [0, G) has no adapter.  Returns (Y, workspace)."""
-    L = lib()
-    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3:
-        raise ValueError("X and W must be 2-d, A 3-d")
-    M, K, N, R = X.shape[0], X.shape[1], W.shape[0 if trans else 1], A.shape[1 if trans else 2]
-    if Y is None:
-        Y = torch.empty((M, N), dtype=X.dtype, device=X.device)
-    workspace, ws, nws = _workspace(workspace, lambda: lora_matmul_workspace_size(M, K, N, R, X.dtype), X.device)
-    _check(L.omm_lora_matmul(_ref(X), _ref(W), _ref(A), _ref(B), _ref(adapter_indices), _ref(adapter_scale),
-                             _ref(bias), int(trans), _ref(Y), ws, nws, _raw_stream(stream, X)), "omm_lora_matmul")
-    return Y, workspace
+    return (_native or native()).lora_matmul(X, W, A, B, adapter_indices, adapter_scale, bias, int(trans), Y, workspace,
+                                             _handle(stream))
 
 
 def moe_route(logits, top_k, renormalize=True, indices=None, weights=None, stream=None):
     """The top_k experts of softmax(logits) per token, by descending logit (ties: lower index), and
     their weights (renormalised over the selected ones if renormalize).  Returns (indices, weights):
     indices int32 as grouped_matmul's group_indices, weights fp32."""
-    L = lib()
-    if indices is None:
-        indices = torch.empty((logits.shape[0], top_k), dtype=torch.int32, device=logits.device)
-    if weights is None:
-        weights = torch.empty((logits.shape[0], top_k), dtype=torch.float32, device=logits.device)
-    _check(L.omm_moe_route(_ref(logits), int(top_k), int(renormalize), _ref(indices), _ref(weights),
-                           _raw_stream(stream, logits)), "omm_moe_route")
-    return indices, weights
+    return (_native or native()).moe_route(logits, top_k, int(renormalize), indices, weights, _handle(stream))
 
 
 def moe_layer_workspace_size(M, K, F, E, top_k):
@@ -320,19 +289,10 @@ def moe_layer(X, router_logits, top_k, W_gate, W_up, W_down, renormalize=True, a
 
     trans=0: W_gate, W_up (E, K, F), W_down (E, F, K) as grouped_matmul's weights; trans=1: (E, F, K)
     and (E, K, F).  activation: "silu" or "gelu" (erf).  Returns (Y, workspace)."""
-    L = lib()
-    if X.dim() != 2 or W_gate.dim() != 3:
-        raise ValueError("X must be 2-d, the weights 3-d")
     if activation not in ACTIVATIONS:
         raise ValueError("activation must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
-    M, K, E, F = X.shape[0], X.shape[1], W_gate.shape[0], W_gate.shape[1 if trans else 2]
-    if Y is None:
-        Y = torch.empty_like(X)
-    workspace, ws, nws = _workspace(workspace, lambda: moe_layer_workspace_size(M, K, F, E, top_k), X.device)
-    _check(L.omm_moe_layer(_ref(X), _ref(router_logits), int(top_k), int(renormalize), _ref(W_gate), _ref(W_up),
-                           _ref(W_down), ACTIVATIONS[activation], int(trans), _ref(Y), ws, nws,
-                           _raw_stream(stream, X)), "omm_moe_layer")
-    return Y, workspace
+    return (_native or native()).moe_layer(X, router_logits, top_k, W_gate, W_up, W_down, int(renormalize),
+                                           ACTIVATIONS[activation], int(trans), Y, workspace, _handle(stream))
 
 
 def token_logprobs_workspace_size(M, V, top_k):
@@ -344,31 +304,12 @@ def token_logprobs(logits, targets, top_k=0, workspace=None, stream=None):
 
     Returns (logprobs, entropy, lse, top_ids, top_logprobs): fp32 (M), (M), (M), int32 (M, top_k) and
     fp32 (M, top_k).  A target outside [0, V) gives log probability 0."""
-    L = lib()
-    if logits.dim() != 2:
-        raise ValueError("logits must be 2-d")
-    M, V = logits.shape
-    k = max(int(top_k), 0)
-    dev = logits.device
-    # one allocation for the three vectors, one for each of the tables
-    vec = torch.empty((3, M), dtype=torch.float32, device=dev)
-    ids = torch.empty((M, k), dtype=torch.int32, device=dev)
-    tlp = torch.empty((M, k), dtype=torch.float32, device=dev)
-    lp, ent, lse = vec.unbind()
-    workspace, ws, nws = _workspace(workspace, lambda: token_logprobs_workspace_size(M, V, top_k), dev)
-    _check(L.omm_token_logprobs(_ref(logits), _ref(targets), int(top_k), _ref(lp), _ref(ent), _ref(lse), _ref(ids),
-                                _ref(tlp), ws, nws, _raw_stream(stream, logits)), "omm_token_logprobs")
-    return lp, ent, lse, ids, tlp
+    return (_native or native()).token_logprobs(logits, targets, top_k, workspace, _handle(stream))
 
 
 def token_logprobs_grad(logits, targets, lse, grad_logprobs, entropy=None, grad_entropy=None, grad_logits=None,
                         stream=None):
     """Gradient of token_logprobs' logprobs (and entropy, if grad_entropy is given) with respect to the
     logits; grad_logits may be the logits tensor itself."""
-    L = lib()
-    if grad_logits is None:
-        grad_logits = torch.empty_like(logits)
-    _check(L.omm_token_logprobs_grad(_ref(logits), _ref(targets), _ref(lse), _ref(entropy), _ref(grad_logprobs),
-                                     _ref(grad_entropy), _ref(grad_logits), _raw_stream(stream, logits)),
-           "omm_token_logprobs_grad")
-    return grad_logits
+    return (_native or native()).token_logprobs_grad(logits, targets, lse, entropy, grad_logprobs, grad_entropy,
+                                                     grad_logits, _handle(stream))

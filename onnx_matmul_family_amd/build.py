@@ -1,4 +1,5 @@
-"""Build libomm.so (the C-ABI library with the gfx950 kernels) in the package dir.
+"""Build libomm.so (the C-ABI library with the gfx950 kernels) and _native.so (the
+Python binding of the decode-side operators) in the package dir.
 
     python -m onnx_matmul_family_amd.build          # or build() from Python
 
@@ -11,11 +12,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libomm.so")
+NATIVE = os.path.join(HERE, "_native.so")
 BUILD = os.path.join(HERE, "_build")
 
 SOURCES = ["api.cpp", "dense16.hip", "dense_f32.hip", "dense_f64.hip", "qlinear.hip", "grouped.hip",
@@ -45,11 +48,34 @@ def _compile(src, verbose):
     return obj
 
 
+def _build_native(verbose):
+    """csrc/binding.cpp against the installed torch (host code only)."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    lib = os.path.join(base, "lib")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+           "-DUSE_ROCM", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", os.path.join(HERE, "..", "include"), "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(rocm, "include"),
+           os.path.join(CSRC, "binding.cpp"), "-o", NATIVE + ".tmp", "-L", lib, "-Wl,-rpath," + lib,
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compile failed: binding.cpp\n%s\n%s" % (r.stdout, r.stderr))
+    os.replace(NATIVE + ".tmp", NATIVE)
+
+
 def build(verbose=False, jobs=None):
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(len(SOURCES), max(1, (os.cpu_count() or 4)))
     with ThreadPoolExecutor(jobs) as ex:
+        native = ex.submit(_build_native, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        native.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:
