@@ -74,13 +74,25 @@ __global__ __launch_bounds__(TRANS ? 256 : 1024) void lora_shrink_kernel(LoraK a
         const E* w = (const E*)a.A + (g * a.R + r) * a.K;
         float acc = 0.0f;
         const int kv = K / V;
-#pragma unroll 4
-        for (int c = lane; c < kv; c += 64) {
-            float xv[V], wv[V];
-            unpack16<DT>(load16(x + c * V), xv);
-            unpack16<DT>(load16(w + c * V), wv);
+        // U loads of each on their way at once (past the end: the last one, not used)
+        constexpr int U = 8;
+        for (int c0 = lane; c0 < kv; c0 += 64 * U) {
+            u32x4_t xr[U], wr[U];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc = fmaf(xv[i], wv[i], acc);
+            for (int u = 0; u < U; ++u) {
+                const int c = min(c0 + 64 * u, kv - 1) * V;
+                xr[u] = load16(x + c);
+                wr[u] = load16(w + c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c0 + 64 * u >= kv) continue;
+                float xv[V], wv[V];
+                unpack16<DT>(xr[u], xv);
+                unpack16<DT>(wr[u], wv);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc = fmaf(xv[i], wv[i], acc);
+            }
         }
         const int k = kv * V + lane;
         if (k < K) acc = fmaf(elem_f32<DT>(x[k]), elem_f32<DT>(w[k]), acc);
@@ -94,16 +106,31 @@ __global__ __launch_bounds__(TRANS ? 256 : 1024) void lora_shrink_kernel(LoraK a
         float acc[V] = {};
         if (mine) {
             const E* w = (const E*)a.A + g * a.K * a.R + start;
-#pragma unroll 4
-            for (int k = kk; k < K; k += kn) {
-                const float xv = elem_f32<DT>(x[k]);
-                float wv[V];
-                if constexpr (V == 1)
-                    wv[0] = elem_f32<DT>(w[(int64_t)k * a.R]);
-                else
-                    unpack16<DT>(load16(w + (int64_t)k * a.R), wv);
+            constexpr int U = 8;
+            for (int k0 = kk; k0 < K; k0 += U * kn) {
+                E xr[U];
+                u32x4_t wr[U];
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(xv, wv[i], acc[i]);
+                for (int u = 0; u < U; ++u) {
+                    const int k = min(k0 + u * kn, K - 1);
+                    xr[u] = x[k];
+                    if constexpr (V == 1)
+                        wr[u][0] = __builtin_bit_cast(uint32_t, elem_f32<DT>(w[(int64_t)k * a.R]));
+                    else
+                        wr[u] = load16(w + (int64_t)k * a.R);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (k0 + u * kn >= K) continue;
+                    const float xv = elem_f32<DT>(xr[u]);
+                    float wv[V];
+                    if constexpr (V == 1)
+                        wv[0] = __uint_as_float(wr[u][0]);
+                    else
+                        unpack16<DT>(wr[u], wv);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = fmaf(xv, wv[i], acc[i]);
+                }
             }
         }
         for (int d = tpr; d < 64; d <<= 1)
