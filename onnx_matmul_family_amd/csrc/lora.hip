@@ -49,15 +49,19 @@ __global__ __launch_bounds__(256) void lora_delta_any_kernel(LoraK a, int64_t nb
 }
 
 // ------------------------------------------------------------------ few rows (at most 64)
-// T[m, r] = scale[g] sum_k X[m, k] A[g, k, r], one workgroup a row (or a part of
-// its r): the rows of a decode batch have adapters of their own, so A is read
-// once a row whatever the tiling, on the vector ALU.
+// T[m, r] = scale[g] sum_k X[m, k] A[g, k, r], some workgroups a row: the rows of
+// a decode batch have adapters of their own, so A is read once a row whatever
+// the tiling, on the vector ALU; one CU takes in 32 bytes a clock or so, hence
+// the shares of 32 to 64 KiB.
 //   TRANS = 1: a wave an r, 16 bytes of k a lane.
-//   TRANS = 0: a thread takes V columns of every (1024 / tpr)-th k (tpr threads
-//     a row of R, a power of two); sums over k by shuffles, then LDS.
+//   TRANS = 0: a workgroup a quarter of K (its sum in T's quarter; the reader
+//     adds them up); a thread takes V columns of every (512 / tpr)-th k (tpr
+//     threads a row of R, a power of two); sums over k by shuffles, then LDS.
 // It also zeroes the counters of the kernel that follows it.
+template <int TRANS> constexpr int kParts = TRANS ? 1 : 4;
+
 template <int DT, int TRANS, int V>
-__global__ __launch_bounds__(TRANS ? 256 : 1024) void lora_shrink_kernel(LoraK a, int tpr) {
+__global__ __launch_bounds__(TRANS ? 256 : 512) void lora_shrink_kernel(LoraK a, int tpr) {
     typedef typename elem_of<DT>::type E;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t m = blockIdx.y;
@@ -99,20 +103,21 @@ __global__ __launch_bounds__(TRANS ? 256 : 1024) void lora_shrink_kernel(LoraK a
         acc = wave_sum(acc);
         if (lane == 0) a.T[m * a.R + r] = acc * scale;
     } else {
-        __shared__ float red[16][64][V];
-        const int rb = tid & (tpr - 1), kk = tid / tpr, kn = 1024 / tpr;
+        __shared__ float red[8][64][V];
+        const int rb = tid & (tpr - 1), kk = tid / tpr, kn = 512 / tpr;
+        const int kc = (K + kParts<0> - 1) / kParts<0>, kb = blockIdx.x * kc, ke = min(K, kb + kc);
         const int start = min(rb * V, a.R - V);  // the last group may overlap the one before
         const bool mine = rb * V < a.R;
         float acc[V] = {};
         if (mine) {
             const E* w = (const E*)a.A + g * a.K * a.R + start;
             constexpr int U = 8;
-            for (int k0 = kk; k0 < K; k0 += U * kn) {
+            for (int k0 = kb + kk; k0 < ke; k0 += U * kn) {
                 E xr[U];
                 u32x4_t wr[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int k = min(k0 + u * kn, K - 1);
+                    const int k = min(k0 + u * kn, ke - 1);
                     xr[u] = x[k];
                     if constexpr (V == 1)
                         wr[u][0] = __builtin_bit_cast(uint32_t, elem_f32<DT>(w[(int64_t)k * a.R]));
@@ -121,7 +126,7 @@ __global__ __launch_bounds__(TRANS ? 256 : 1024) void lora_shrink_kernel(LoraK a
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (k0 + u * kn >= K) continue;
+                    if (k0 + u * kn >= ke) continue;
                     const float xv = elem_f32<DT>(xr[u]);
                     float wv[V];
                     if constexpr (V == 1)
@@ -144,8 +149,8 @@ __global__ __launch_bounds__(TRANS ? 256 : 1024) void lora_shrink_kernel(LoraK a
             const int b = tid / V, i = tid - min(b * V, a.R - V);
             float v = 0.0f;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) v += red[u][b][i];
-            a.T[m * a.R + tid] = v * scale;
+            for (int u = 0; u < 8; ++u) v += red[u][b][i];
+            a.T[(blockIdx.x * a.M + m) * a.R + tid] = v * scale;
         }
     }
 }
@@ -179,7 +184,13 @@ __device__ __forceinline__ void lora_expand(const LoraK& a, int split, int c0, f
             ex[j][c] = acc;
         } else {
             float acc[V] = {};
-            auto row = [&](u32x4_t w, float tv) {
+            const auto tsum = [&](const float* p) {
+                float v = p[0];
+#pragma unroll
+                for (int u = 1; u < kParts<TRANS>; ++u) v += p[(int64_t)u * M * R];
+                return v;
+            };
+            const auto row = [&](u32x4_t w, float tv) {
                 float bv[V];
                 unpack16<DT>(w, bv);
 #pragma unroll
@@ -192,12 +203,12 @@ __device__ __forceinline__ void lora_expand(const LoraK& a, int split, int c0, f
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     w[i] = load16(b + (int64_t)(r + i) * a.N);
-                    tv[i] = t[r + i];
+                    tv[i] = tsum(t + r + i);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) row(w[i], tv[i]);
             }
-            for (; r < rn; ++r) row(load16(b + (int64_t)r * a.N), t[r]);
+            for (; r < rn; ++r) row(load16(b + (int64_t)r * a.N), tsum(t + r));
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (n + i >= c0 + c) ex[j][n + i - c0] = acc[i];
@@ -303,9 +314,9 @@ void lora_streamed(const LoraK& a, hipStream_t s) {
         const int v = a.R >= V ? V : 1;
         int tpr = 1;
         while (tpr * v < a.R) tpr *= 2;
-        const dim3 grid(1, (unsigned)a.M);
-        if (v == V) lora_shrink_kernel<DT, 0, V><<<grid, 1024, 0, s>>>(a, tpr);
-        else lora_shrink_kernel<DT, 0, 1><<<grid, 1024, 0, s>>>(a, tpr);
+        const dim3 grid(kParts<0>, (unsigned)a.M);
+        if (v == V) lora_shrink_kernel<DT, 0, V><<<grid, 512, 0, s>>>(a, tpr);
+        else lora_shrink_kernel<DT, 0, 1><<<grid, 512, 0, s>>>(a, tpr);
     }
     const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)a.splits);
     if (a.M <= 16) lora_stream_kernel<DT, TRANS, 1><<<grid, 512, 0, s>>>(a);
@@ -321,7 +332,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt) {
     if (streamable(M, K, N, dt)) {
         const int sp = stream_splits(K, N);
-        return align256((size_t)M * R * 4) + (sp > 1 ? align256((size_t)sp * M * ((N + 127) / 128) * 512) : 0) +
+        return align256((size_t)M * R * 4 * kParts<0>) + (sp > 1 ? align256((size_t)sp * M * ((N + 127) / 128) * 512) : 0) +
                align256((size_t)(N + 127) / 128 * 4);
     }
     return lora_rows_workspace_bytes(M, R);
@@ -369,7 +380,7 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
     a.idx64 = l.idx64;
     if (streamable(l.M, l.K, l.N, dt)) {
         a.splits = stream_splits(l.K, l.N);
-        a.part = (float*)((char*)ws + align256((size_t)l.M * l.R * 4));
+        a.part = (float*)((char*)ws + align256((size_t)l.M * l.R * 4 * kParts<0>));
         a.done = (uint32_t*)((char*)a.part +
                              (a.splits > 1 ? align256((size_t)a.splits * l.M * ((l.N + 127) / 128) * 512) : 0));
         log_choice("lora_matmul: streamed, K in %d part(s)", a.splits);

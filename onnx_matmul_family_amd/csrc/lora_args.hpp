@@ -18,7 +18,7 @@ struct LoraK {
     int64_t M, K, N, G;
     int R, trans, idx64, splits;
     // workspace
-    float* T;        // (M, R), scaled; rows in the order of perm
+    float* T;        // (M, R), scaled; rows in the order of perm (up to 64 rows, trans 0: 4 of them to add up)
     float* part;     // (ceil(N / 128), splits, M, 128)
     uint32_t* done;  // finished workgroups of each 128 columns
     int32_t* perm;   // (M) rows in the order of their adapters, or nullptr: as they come
