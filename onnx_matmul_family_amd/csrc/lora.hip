@@ -66,7 +66,7 @@ __global__ __launch_bounds__(TRANS ? 256 : 512) void lora_shrink_kernel(LoraK a,
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t m = blockIdx.y;
     if (m == 0 && blockIdx.x == 0)
-        for (int64_t i = tid; i < (a.N + 127) / 128; i += blockDim.x) a.done[i] = 0;
+        for (int64_t i = tid; i < (a.N + 15) / 16; i += blockDim.x) a.done[i] = 0;
     const int64_t g = row_adapter(a, m);
     if (g < 0 || a.R == 0) return;
     const E* x = (const E*)a.X + m * a.K;
@@ -158,12 +158,12 @@ __global__ __launch_bounds__(TRANS ? 256 : 512) void lora_shrink_kernel(LoraK a,
 // ex[j][c] = sum_r T[m, r] B[g, r, c0 + c] of the rows m = split + j splits.
 //   TRANS = 1: a thread a column, 16 bytes of r a load.
 //   TRANS = 0: a thread 16 bytes of columns, one r a load.
-template <int DT, int TRANS>
-__device__ __forceinline__ void lora_expand(const LoraK& a, int split, int c0, float (*ex)[128], int tid) {
+template <int DT, int TRANS, int CW>
+__device__ __forceinline__ void lora_expand(const LoraK& a, int split, int c0, float (*ex)[CW], int tid) {
     typedef typename elem_of<DT>::type E;
-    constexpr int V = kQ<DT>, TPR = TRANS ? 128 : 128 / V;  // threads a row
+    constexpr int V = kQ<DT>, TPR = TRANS ? CW : CW / V;  // threads a row
     const int M = (int)a.M, N = (int)a.N, R = a.R;
-    const int c = TRANS ? tid & 127 : (tid & (TPR - 1)) * V;
+    const int c = TRANS ? tid & (CW - 1) : (tid & (TPR - 1)) * V;
     if (c0 + c >= N) return;
     const int n = TRANS ? c0 + c : group_start<DT>(c0, c, N);
     for (int j = tid / TPR, m = split + j * a.splits; m < M; j += 512 / TPR, m = split + j * a.splits) {
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
     f32x4_t acc[8][NG] = {};
     int s0, s1;
     wave_steps<DT, 8>(K, TRANS, wave, s0, s1, a.splits, sp);
-    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, acc, (u32x4_t*)&red[red_index(wave, 0, 0, 0)], lane, [&] { lora_expand<DT, TRANS>(a, sp, c0, ex, tid); });
+    stream_run<DT, TRANS, NG>(w, x, s0, s1, K, acc, (u32x4_t*)&red[red_index(wave, 0, 0, 0)], lane, [&] { lora_expand<DT, TRANS, 128>(a, sp, c0, ex, tid); });
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g) __syncthreads();
@@ -269,14 +269,179 @@ __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
                 if (a.bias) v += elem_f32<DT>(((const E*)a.bias)[n]);
                 ((E*)a.Y)[(int64_t)m * N + n] = f32_elem<DT>(v);
             } else {
-                part_store(a.part, ((int64_t)blockIdx.x * a.splits + sp) * M + m, c, v);
+                part_store<128>(a.part, ((int64_t)blockIdx.x * a.splits + sp) * M + m, c, v);
             }
         }
     }
     // (the kernel before this one zeroed the count)
     if (a.splits == 1 || !part_last(&a.done[blockIdx.x], a.splits, tid)) return;
-    part_sums<512>(
+    part_sums<512, 128>(
         a.part, M, a.splits, tid, [&](int m, int p) { return ((int64_t)blockIdx.x * a.splits + p) * M + m; },
+        [&](int m, int c, float v0, float v1) {
+            const int n = c0 + c;
+            E* y = (E*)a.Y + (int64_t)m * N + n;
+            if (n < N) y[0] = f32_elem<DT>(v0 + (a.bias ? elem_f32<DT>(((const E*)a.bias)[n]) : 0.0f));
+            if (n + 1 < N) y[1] = f32_elem<DT>(v1 + (a.bias ? elem_f32<DT>(((const E*)a.bias)[n + 1]) : 0.0f));
+        });
+}
+
+// Y of 16 NF columns, otherwise as lora_stream_kernel.  With few columns a step
+// is few loads of the weights beside NG of the rows, so U steps are on their way
+// at once in each of two register sets, and the rows take row_tile in either
+// layout.
+//   TRANS = 1: weights by row_tile.
+//   TRANS = 0: a load takes 16-byte pieces of 32 / NF contraction rows (fp32:
+//     16 / NF); in LDS they lie as in memory and are read by columns (16 bits:
+//     the transposing read).  Neighbouring column blocks run on one XCD, whose
+//     L2 puts their pieces of a line together.
+template <int DT, int NF>
+struct ColsW {
+    typedef typename elem_of<DT>::type E;
+    static constexpr int LPR = NF * (DT == 2 ? 4 : 2), ROWS = 64 / LPR;  // lanes a row, rows a load
+    const E* p;  // the lane's row and columns
+    int64_t ld;
+    __device__ __forceinline__ void load(u32x4_t (&w)[NF], int kb) const {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) w[j] = load16(p + (int64_t)(kb + j * ROWS) * ld);
+    }
+    __device__ __forceinline__ void tail(u32x4_t (&w)[NF], int kb, int kn, int lane) const {
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            w[j] = kb + j * ROWS + lane / LPR < kn ? load16(p + (int64_t)(kb + j * ROWS) * ld) : u32x4_t{0, 0, 0, 0};
+    }
+    // tiles as loaded -> operands of the NF fragments
+    __device__ __forceinline__ static void operands(u32x4_t (&w)[NF], u32x4_t* scratch, int lane) {
+        constexpr int RB = LPR * 16;  // bytes a row
+#pragma unroll
+        for (int j = 0; j < NF; ++j) scratch[j * 64 + lane] = w[j];
+        __builtin_amdgcn_wave_barrier();
+        const int i = lane & 15, q = lane >> 4;
+        const char* b = (const char*)scratch;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            if constexpr (DT == 2) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) w[j][t] = *(const uint32_t*)(b + (4 * q + t) * RB + j * 64 + 4 * i);
+            } else {
+                const char* f = b + (8 * q + (i >> 2)) * RB + j * 32 + 8 * (i & 3);
+                const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(OMM_LDS(i16x4_t, f));
+                const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(OMM_LDS(i16x4_t, f + 4 * RB));
+                const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
+                w[j] = u32x4_t{l2.x, l2.y, h2.x, h2.y};
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+};
+
+template <int DT, int TRANS, int NG, int NF, int U>
+__global__ __launch_bounds__(512, 2) void lora_cols_kernel(LoraK a) {
+    typedef typename elem_of<DT>::type E;
+    constexpr int ST = kStep<DT>, CW = 16 * NF, TILES = NF > NG ? NF : NG;
+    constexpr int RED = 8 * NF * NG * kFragPad, SCR = 8 * TILES * 256;
+    __shared__ __attribute__((aligned(16))) float red[RED > SCR ? RED : SCR];
+    __shared__ float ex[16 * NG][CW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int M = (int)a.M, K = (int)a.K, N = (int)a.N;
+    // (blocks split evenly over the XCDs, a run of neighbours each)
+    const int bx = blockIdx.x & 7, block = bx * (int)(gridDim.x >> 3) + min(bx, (int)(gridDim.x & 7)) + (blockIdx.x >> 3);
+    const int c0 = block * CW, sp = blockIdx.y;
+    u32x4_t* scratch = (u32x4_t*)&red[wave * TILES * 256];
+    typename std::conditional<TRANS != 0, StreamW<DT, 1, NF>, ColsW<DT, NF>>::type w;
+    if constexpr (TRANS) {
+        w.base[0] = w.base[1] = (const E*)a.W;
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            w.off[j] = (uint32_t)min(c0 + 16 * j + tile_row(lane), N - 1) * K + tile_off<DT>(lane);
+    } else {
+        constexpr int LPR = ColsW<DT, NF>::LPR;
+        w.ld = N;
+        w.p = (const E*)a.W + (int64_t)(lane / LPR) * N + group_start<DT>(c0, (lane % LPR) * kQ<DT>, N);
+    }
+    StreamX<DT, 1, NG> x;  // rows past the last are the last one: their results are not used
+#pragma unroll
+    for (int g = 0; g < NG; ++g) x.p[g] = (const E*)a.X + (int64_t)min(16 * g + tile_row(lane), M - 1) * K + tile_off<DT>(lane);
+    f32x4_t acc[NF][NG] = {};
+    int s0, s1;
+    wave_steps<DT, 8>(K, 1, wave, s0, s1, a.splits, sp);
+    const int full = min(s1, K / ST);
+    u32x4_t wa[U][NF], wb[U][NF], xa[U][NG][1], xb[U][NG][1];
+    const auto load = [&](u32x4_t (&tw)[U][NF], u32x4_t (&tx)[U][NG][1], int s) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            w.load(tw[u], (s + u) * ST);
+            x.load(tx[u], (s + u) * ST);
+        }
+    };
+    const auto mul1 = [&](u32x4_t (&tw)[NF], const u32x4_t (&tx)[NG][1]) {
+        u32x4_t o[NG][1];
+        x.operands(tx, o, scratch, lane);
+        if constexpr (TRANS)
+            row_tile<NF>(tw, scratch, lane);
+        else
+            w.operands(tw, scratch, lane);
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                if constexpr (DT == 2) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        acc[j][g] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                            __uint_as_float(tw[j][t]), __uint_as_float(o[g][0][t]), acc[j][g], 0, 0, 0);
+                } else {
+                    acc[j][g] = mfma16x16x32<DT>(tw[j], o[g][0], acc[j][g]);
+                }
+            }
+    };
+    const auto mul = [&](u32x4_t (&tw)[U][NF], const u32x4_t (&tx)[U][NG][1]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) mul1(tw[u], tx[u]);
+    };
+    int s = s0;
+    if (s + U <= full) load(wa, xa, s);
+    lora_expand<DT, TRANS, CW>(a, sp, c0, ex, tid);
+    for (; s + 2 * U <= full; s += 2 * U) {
+        load(wb, xb, s + U);
+        mul(wa, xa);
+        if (s + 3 * U <= full) load(wa, xa, s + 2 * U);
+        mul(wb, xb);
+    }
+    if (s + U <= full) {
+        mul(wa, xa);
+        s += U;
+    }
+    for (; s < s1 && s * ST < K; ++s) {  // the rest, the last step with zeros past K
+        w.tail(wa[0], s * ST, K, lane);
+        x.tail(xa[0], s * ST, K, lane);
+        mul1(wa[0], xa[0]);
+    }
+    __syncthreads();  // (the image overlaps other waves' scratch)
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) *(f32x4_t*)&red[((wave * NF + j) * NG + g) * kFragPad + lane * 4] = acc[j][g];
+    __syncthreads();
+    for (int o = tid; o < M * CW; o += 512) {
+        const int c = o % CW, m = o / CW, n = c0 + c;
+        if (n >= N) continue;
+        int pos = c;  // TRANS = 0: the column's place in its group, which may start before its multiple
+        if constexpr (!TRANS)
+            pos = (c & ~(kQ<DT> - 1)) +
+                  min((c & (kQ<DT> - 1)) + c0 + (c & ~(kQ<DT> - 1)) - group_start<DT>(c0, c, N), kQ<DT> - 1);
+        const float* p = &red[((pos >> 4) * NG + (m >> 4)) * kFragPad + (((pos & 15) >> 2) * 16 + (m & 15)) * 4 + (pos & 3)];
+        float v = m % a.splits == sp ? ex[m / a.splits][c] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v += p[u * NF * NG * kFragPad];
+        if (a.splits == 1)
+            ((E*)a.Y)[(int64_t)m * N + n] = f32_elem<DT>(v + (a.bias ? elem_f32<DT>(((const E*)a.bias)[n]) : 0.0f));
+        else
+            part_store<CW>(a.part, ((int64_t)block * a.splits + sp) * M + m, c, v);
+    }
+    // (the kernel before this one zeroed the count)
+    if (a.splits == 1 || !part_last(&a.done[block], a.splits, tid)) return;
+    part_sums<512, CW>(
+        a.part, M, a.splits, tid, [&](int m, int p) { return ((int64_t)block * a.splits + p) * M + m; },
         [&](int m, int c, float v0, float v1) {
             const int n = c0 + c;
             E* y = (E*)a.Y + (int64_t)m * N + n;
@@ -287,22 +452,72 @@ __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
 
 constexpr int64_t kFew = 64;
 
-// Workgroups that share 128 columns by splitting K: as many as run at once (one
-// a CU), each wave with two steps of 32 or more; of the counts that leave a
-// wave the same steps, the smallest.
-int stream_splits(int64_t K, int64_t N) {
-    const int64_t groups = (N + 127) / 128, steps = (K + 31) / 32;
+// How the streamed forms share the work: columns of a workgroup (128:
+// lora_stream_kernel, fewer: lora_cols_kernel) and the parts that K is split
+// into.  Fewer columns make more workgroups without splitting K, whose parts
+// must be joined by the last one (its time grows with rows and parts), but read
+// X more often.  Measured at K = 4096, bf16, W from memory, us with 16 / 32 / 64
+// / 128 columns:
+//   trans 1   N = 1024, 43 rows    8.8   10.7  12.2  18.2
+//             N = 2056,  1 row     8.9   10.4  10.0  10.6;  43 rows  16.5  14.2  15.5  21.0
+//             N = 4104,  1 row    16.7   14.5  16.2  16.8;  43 rows  28.0  22.9  22.2  27.4
+//             N = 8200,  1 row    29.4   30.5  27.8  26.0;  64 rows  52.8  52.2  43.0  62.8
+//   trans 0   N = 1024,  1 row    10.7   10.7   8.9  10.1;  43 rows  12.1  12.2  13.6  18.3
+//             N = 2056,  1 row    14.7   12.7  12.4  10.7;  43 rows  19.4  16.7  17.9  19.5
+//             N = 4104,  1 row    20.2   18.6  16.7  13.5;  43 rows  31.9  26.1  22.4  23.2
+//             N = 8200, 43 rows   50.7   42.3  39.7  35.9
+// So trans 1 (whose columns are rows of memory, any number is as good): as few
+// as leave 136 column blocks, over 16 rows 72.  trans 0: wide ones unless N is
+// small.  K goes into as many parts as fill 256 CUs, each wave two steps of 32 or
+// more; of the counts that leave a wave the same steps, the smallest.
+struct StreamPlan {
+    int cw, splits;
+};
+StreamPlan stream_plan(int64_t M, int64_t K, int64_t N, int trans) {
+    StreamPlan p;
+    const bool few = M <= 16;
+    if (trans) {
+        const int64_t most = few ? 136 : 72;
+        p.cw = N <= 16 * most ? 16 : N <= 32 * most ? 32 : N <= 64 * most || !few ? 64 : 128;
+    } else if (few) {
+        p.cw = N <= 1152 ? 64 : 128;
+    } else {
+        p.cw = N <= 16 * 72 ? 16 : N <= 32 * 72 ? 32 : 128;
+    }
+    const int64_t groups = (N + p.cw - 1) / p.cw, steps = (K + 31) / 32;
     int64_t s = 256 / groups;
     if (s > steps / 16) s = steps / 16;
     if (s > 16) s = 16;
     if (s < 1) s = 1;
     const int64_t per = (steps + 8 * s - 1) / (8 * s);
-    return (int)((steps + 8 * per - 1) / (8 * per));
+    p.splits = (int)((steps + 8 * per - 1) / (8 * per));
+    return p;
+}
+// (the workspace does not depend on the layout: the larger of both)
+size_t part_bytes(int64_t M, int64_t K, int64_t N) {
+    size_t most = 0;
+    for (int trans = 0; trans < 2; ++trans) {
+        const StreamPlan p = stream_plan(M, K, N, trans);
+        const size_t n = p.splits > 1 ? (size_t)p.splits * M * ((N + p.cw - 1) / p.cw) * p.cw * 4 : 0;
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 // few rows, whole groups of 8 columns, W within 32-bit byte offsets
 bool streamable(int64_t M, int64_t K, int64_t N, int dt) {
     return M <= kFew && K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
+}
+
+// (steps on their way a register set: as many as fit)
+template <int DT, int TRANS, int NF>
+void cols_launch(const LoraK& a, int ng, dim3 grid, hipStream_t s) {
+    switch (ng) {
+        case 1: return lora_cols_kernel<DT, TRANS, 1, NF, NF == 4 ? 2 : 4><<<grid, 512, 0, s>>>(a);
+        case 2: return lora_cols_kernel<DT, TRANS, 2, NF, NF == 4 ? 2 : 4><<<grid, 512, 0, s>>>(a);
+        case 3: return lora_cols_kernel<DT, TRANS, 3, NF, NF == 1 ? 4 : 2><<<grid, 512, 0, s>>>(a);
+        default: return lora_cols_kernel<DT, TRANS, 4, NF, 2><<<grid, 512, 0, s>>>(a);
+    }
 }
 
 template <int DT, int TRANS>
@@ -318,11 +533,29 @@ void lora_streamed(const LoraK& a, hipStream_t s) {
         if (v == V) lora_shrink_kernel<DT, 0, V><<<grid, 512, 0, s>>>(a, tpr);
         else lora_shrink_kernel<DT, 0, 1><<<grid, 512, 0, s>>>(a, tpr);
     }
-    const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)a.splits);
-    if (a.M <= 16) lora_stream_kernel<DT, TRANS, 1><<<grid, 512, 0, s>>>(a);
-    else if (a.M <= 32) lora_stream_kernel<DT, TRANS, 2><<<grid, 512, 0, s>>>(a);
-    else if (a.M <= 48) lora_stream_kernel<DT, TRANS, 3><<<grid, 512, 0, s>>>(a);
-    else lora_stream_kernel<DT, TRANS, 4><<<grid, 512, 0, s>>>(a);
+    const dim3 grid((unsigned)((a.N + a.cw - 1) / a.cw), (unsigned)a.splits);
+    const int ng = (int)((a.M + 15) / 16);
+    if constexpr (TRANS) {
+        switch (a.cw) {
+            case 16: return cols_launch<DT, 1, 1>(a, ng, grid, s);
+            case 32: return cols_launch<DT, 1, 2>(a, ng, grid, s);
+            case 64: return cols_launch<DT, 1, 4>(a, ng, grid, s);
+            default: return lora_stream_kernel<DT, 1, 1><<<grid, 512, 0, s>>>(a);  // (up to 16 rows)
+        }
+    } else {
+        switch (a.cw) {
+            case 16: return cols_launch<DT, 0, 1>(a, ng, grid, s);
+            case 32: return cols_launch<DT, 0, 2>(a, ng, grid, s);
+            case 64: return lora_cols_kernel<DT, 0, 1, 4, 2><<<grid, 512, 0, s>>>(a);  // (up to 16 rows)
+            default: break;
+        }
+        switch (ng) {
+            case 1: return lora_stream_kernel<DT, 0, 1><<<grid, 512, 0, s>>>(a);
+            case 2: return lora_stream_kernel<DT, 0, 2><<<grid, 512, 0, s>>>(a);
+            case 3: return lora_stream_kernel<DT, 0, 3><<<grid, 512, 0, s>>>(a);
+            default: return lora_stream_kernel<DT, 0, 4><<<grid, 512, 0, s>>>(a);
+        }
+    }
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -331,9 +564,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt) {
     if (streamable(M, K, N, dt)) {
-        const int sp = stream_splits(K, N);
-        return align256((size_t)M * R * 4 * kParts<0>) + (sp > 1 ? align256((size_t)sp * M * ((N + 127) / 128) * 512) : 0) +
-               align256((size_t)(N + 127) / 128 * 4);
+        return align256((size_t)M * R * 4 * kParts<0>) + align256(part_bytes(M, K, N)) + align256((size_t)(N + 15) / 16 * 4);
     }
     return lora_rows_workspace_bytes(M, R);
 }
@@ -379,11 +610,12 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
     a.trans = l.trans;
     a.idx64 = l.idx64;
     if (streamable(l.M, l.K, l.N, dt)) {
-        a.splits = stream_splits(l.K, l.N);
+        const StreamPlan p = stream_plan(l.M, l.K, l.N, l.trans);
+        a.splits = p.splits;
+        a.cw = p.cw;
         a.part = (float*)((char*)ws + align256((size_t)l.M * l.R * 4 * kParts<0>));
-        a.done = (uint32_t*)((char*)a.part +
-                             (a.splits > 1 ? align256((size_t)a.splits * l.M * ((l.N + 127) / 128) * 512) : 0));
-        log_choice("lora_matmul: streamed, K in %d part(s)", a.splits);
+        a.done = (uint32_t*)((char*)a.part + align256(part_bytes(l.M, l.K, l.N)));
+        log_choice("lora_matmul: streamed, %d columns a workgroup, K in %d part(s)", a.cw, a.splits);
         switch (dt * 2 + a.trans) {
             case 0: lora_streamed<0, 0>(a, s); break;
             case 1: lora_streamed<0, 1>(a, s); break;

@@ -16,11 +16,11 @@ struct LoraK {
     const void* bias;    // (N) or nullptr
     void* Y;
     int64_t M, K, N, G;
-    int R, trans, idx64, splits;
+    int R, trans, idx64, splits, cw;  // cw: columns of a workgroup (streamed form)
     // workspace
     float* T;        // (M, R), scaled; rows in the order of perm (up to 64 rows, trans 0: 4 of them to add up)
-    float* part;     // (ceil(N / 128), splits, M, 128)
-    uint32_t* done;  // finished workgroups of each 128 columns
+    float* part;     // (ceil(N / cw), splits, M, cw)
+    uint32_t* done;  // finished workgroups of each cw columns
     int32_t* perm;   // (M) rows in the order of their adapters, or nullptr: as they come
     float* tmax;     // (M, 2 ceil(R / 128)) largest |T| (fp16)
 };

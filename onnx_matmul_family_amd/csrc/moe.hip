@@ -474,7 +474,7 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
             float v = 0.0f;
 #pragma unroll
             for (int u = 0; u < NWS; ++u) v += red[red_index(u, j, l, rr)];
-            part_store(a.part, ((int64_t)blockIdx.x * a.splits + sp) * (a.M * a.k) + r.pair[t], c, v);
+            part_store<128>(a.part, ((int64_t)blockIdx.x * a.splits + sp) * (a.M * a.k) + r.pair[t], c, v);
         }
     }
 }
@@ -495,7 +495,7 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_down_kernel(La
     // zeroed the count).
     if (!part_last(&a.done[blockIdx.x], r.active * a.splits, tid)) return;
     const int N = (int)a.K, k = a.k;
-    part_sums<64 * NWS>(
+    part_sums<64 * NWS, 128>(
         a.part, a.M, k * a.splits, tid,
         [&](int m, int p) {
             const int sp = p / k;

@@ -397,13 +397,14 @@ __device__ __forceinline__ void red_pos(int c, int shift, int row, int& j, int& 
 }
 
 // ------------------------------------------------------------------ parts of one result in several workgroups
-// A workgroup leaves its part of a row's 128 columns in parts[row][128], past
+// A workgroup leaves its part of a row's CW columns in parts[row][CW], past
 // its own L2 (another one's workgroup may sum it), and counts itself; the last
-// one of a column block to be counted sums the parts.  Whole rows of 512 bytes
+// one of a column block to be counted sums the parts.  Whole lines
 // belong to one column block, and they are read with loads that do not look
 // into this L2 either, so no cache has to be invalidated.
+template <int CW>
 __device__ __forceinline__ void part_store(float* parts, int64_t row, int c, float v) {
-    __hip_atomic_store(parts + row * 128 + c, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(parts + row * CW + c, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // whether this workgroup is the last of `count` (every thread calls it)
 __device__ __forceinline__ bool part_last(uint32_t* done, uint32_t count, int tid) {
@@ -416,22 +417,22 @@ __device__ __forceinline__ bool part_last(uint32_t* done, uint32_t count, int ti
     return last != 0;
 }
 // Calls out(m, c, v0, v1) with the sums over p in [0, np) of parts[first(m) +
-// step(p)][c], [c + 1] for the M rows and 64 column pairs; a thread has NB * SB
+// step(p)][c], [c + 1] for the M rows and CW / 2 column pairs; a thread has NB * SB
 // loads on their way at once (a round trip to memory takes as long as all of
 // them).  The order of the sum is fixed.
-template <int NT, int NB, int SB, typename Row, typename Out>
+template <int NT, int CW, int NB, int SB, typename Row, typename Out>
 __device__ __forceinline__ void part_sums(const float* parts, int M, int np, int tid, Row row, Out out) {
-    for (int o0 = tid; o0 < M * 64; o0 += NT * NB) {
+    for (int o0 = tid; o0 < M * (CW / 2); o0 += NT * NB) {
         float v[NB][2] = {};
         for (int p0 = 0; p0 < np; p0 += SB) {
             uint64_t u[NB][SB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const int o = min(o0 + b * NT, M * 64 - 1);
+                const int o = min(o0 + b * NT, M * (CW / 2) - 1);
 #pragma unroll
                 for (int i = 0; i < SB; ++i)
                     u[b][i] = __hip_atomic_load(
-                        (const uint64_t*)(parts + row(o >> 6, min(p0 + i, np - 1)) * 128 + (o & 63) * 2),
+                        (const uint64_t*)(parts + row(o / (CW / 2), min(p0 + i, np - 1)) * CW + o % (CW / 2) * 2),
                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
 #pragma unroll
@@ -446,16 +447,16 @@ __device__ __forceinline__ void part_sums(const float* parts, int M, int np, int
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int o = o0 + b * NT;
-            if (o < M * 64) out(o >> 6, (o & 63) * 2, v[b][0], v[b][1]);
+            if (o < M * (CW / 2)) out(o / (CW / 2), o % (CW / 2) * 2, v[b][0], v[b][1]);
         }
     }
 }
-template <int NT, typename Row, typename Out>
+template <int NT, int CW, typename Row, typename Out>
 __device__ __forceinline__ void part_sums(const float* parts, int M, int np, int tid, Row row, Out out) {
-    if (M * 64 <= NT)
-        part_sums<NT, 1, 16>(parts, M, np, tid, row, out);
+    if (M * (CW / 2) <= NT)
+        part_sums<NT, CW, 1, 16>(parts, M, np, tid, row, out);
     else
-        part_sums<NT, 4, 8>(parts, M, np, tid, row, out);
+        part_sums<NT, CW, 4, 8>(parts, M, np, tid, row, out);
 }
 
 }  // namespace omm
