@@ -3,6 +3,7 @@
 // (a row whose g is outside [0, G) has no adapter).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "kernels.hpp"
 #include "lora_args.hpp"
@@ -64,9 +65,10 @@ template <int DT, int TRANS, int V>
 __global__ __launch_bounds__(TRANS ? 256 : 512) void lora_shrink_kernel(LoraK a, int tpr) {
     typedef typename elem_of<DT>::type E;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t m = blockIdx.y;
-    if (m == 0 && blockIdx.x == 0)
-        for (int64_t i = tid; i < (a.N + 15) / 16; i += blockDim.x) a.done[i] = 0;
+    if (blockIdx.y == 0 && blockIdx.x == 0)
+        for (int64_t i = tid; i < (a.M + 63) / 64 * ((a.N + a.cw - 1) / a.cw); i += blockDim.x) a.done[i] = 0;
+    row_group(a, blockIdx.y >> 6, kParts<TRANS>, sizeof(E));
+    const int64_t m = blockIdx.y & 63;
     const int64_t g = row_adapter(a, m);
     if (g < 0 || a.R == 0) return;
     const E* x = (const E*)a.X + m * a.K;
@@ -222,6 +224,7 @@ __device__ __forceinline__ void lora_expand(const LoraK& a, int split, int c0, f
 template <int DT, int TRANS, int NG>
 __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
+    row_group(a, blockIdx.z, kParts<TRANS>, sizeof(E));
     __shared__ __attribute__((aligned(16))) float red[8 * 8 * kFragPad];
     __shared__ float ex[16 * NG][128];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
@@ -285,59 +288,12 @@ __global__ __launch_bounds__(512, 2) void lora_stream_kernel(LoraK a) {
         });
 }
 
-// Y of 16 NF columns, otherwise as lora_stream_kernel.  With few columns a step
-// is few loads of the weights beside NG of the rows, so U steps are on their way
-// at once in each of two register sets, and the rows take row_tile in either
-// layout.
-//   TRANS = 1: weights by row_tile.
-//   TRANS = 0: a load takes 16-byte pieces of 32 / NF contraction rows (fp32:
-//     16 / NF); in LDS they lie as in memory and are read by columns (16 bits:
-//     the transposing read).  Neighbouring column blocks run on one XCD, whose
-//     L2 puts their pieces of a line together.
-template <int DT, int NF>
-struct ColsW {
-    typedef typename elem_of<DT>::type E;
-    static constexpr int LPR = NF * (DT == 2 ? 4 : 2), ROWS = 64 / LPR;  // lanes a row, rows a load
-    const E* p;  // the lane's row and columns
-    int64_t ld;
-    __device__ __forceinline__ void load(u32x4_t (&w)[NF], int kb) const {
-#pragma unroll
-        for (int j = 0; j < NF; ++j) w[j] = load16(p + (int64_t)(kb + j * ROWS) * ld);
-    }
-    __device__ __forceinline__ void tail(u32x4_t (&w)[NF], int kb, int kn, int lane) const {
-#pragma unroll
-        for (int j = 0; j < NF; ++j)
-            w[j] = kb + j * ROWS + lane / LPR < kn ? load16(p + (int64_t)(kb + j * ROWS) * ld) : u32x4_t{0, 0, 0, 0};
-    }
-    // tiles as loaded -> operands of the NF fragments
-    __device__ __forceinline__ static void operands(u32x4_t (&w)[NF], u32x4_t* scratch, int lane) {
-        constexpr int RB = LPR * 16;  // bytes a row
-#pragma unroll
-        for (int j = 0; j < NF; ++j) scratch[j * 64 + lane] = w[j];
-        __builtin_amdgcn_wave_barrier();
-        const int i = lane & 15, q = lane >> 4;
-        const char* b = (const char*)scratch;
-#pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            if constexpr (DT == 2) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) w[j][t] = *(const uint32_t*)(b + (4 * q + t) * RB + j * 64 + 4 * i);
-            } else {
-                const char* f = b + (8 * q + (i >> 2)) * RB + j * 32 + 8 * (i & 3);
-                const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(OMM_LDS(i16x4_t, f));
-                const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(OMM_LDS(i16x4_t, f + 4 * RB));
-                const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
-                w[j] = u32x4_t{l2.x, l2.y, h2.x, h2.y};
-            }
-        }
-        __builtin_amdgcn_wave_barrier();
-    }
-};
-
+// Y of 16 NF columns, otherwise as lora_stream_kernel.
 template <int DT, int TRANS, int NG, int NF, int U>
 __global__ __launch_bounds__(512, 2) void lora_cols_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
-    constexpr int ST = kStep<DT>, CW = 16 * NF, TILES = NF > NG ? NF : NG;
+    row_group(a, blockIdx.z, kParts<TRANS>, sizeof(E));
+    constexpr int CW = 16 * NF, TILES = NF > NG ? NF : NG;
     constexpr int RED = 8 * NF * NG * kFragPad, SCR = 8 * TILES * 256;
     __shared__ __attribute__((aligned(16))) float red[RED > SCR ? RED : SCR];
     __shared__ float ex[16 * NG][CW];
@@ -347,75 +303,16 @@ __global__ __launch_bounds__(512, 2) void lora_cols_kernel(LoraK a) {
     const int bx = blockIdx.x & 7, block = bx * (int)(gridDim.x >> 3) + min(bx, (int)(gridDim.x & 7)) + (blockIdx.x >> 3);
     const int c0 = block * CW, sp = blockIdx.y;
     u32x4_t* scratch = (u32x4_t*)&red[wave * TILES * 256];
-    typename std::conditional<TRANS != 0, StreamW<DT, 1, NF>, ColsW<DT, NF>>::type w;
-    if constexpr (TRANS) {
-        w.base[0] = w.base[1] = (const E*)a.W;
-#pragma unroll
-        for (int j = 0; j < NF; ++j)
-            w.off[j] = (uint32_t)min(c0 + 16 * j + tile_row(lane), N - 1) * K + tile_off<DT>(lane);
-    } else {
-        constexpr int LPR = ColsW<DT, NF>::LPR;
-        w.ld = N;
-        w.p = (const E*)a.W + (int64_t)(lane / LPR) * N + group_start<DT>(c0, (lane % LPR) * kQ<DT>, N);
-    }
+    ColsWeights<DT, TRANS, NF> w;
+    cols_start<DT, TRANS, NF>(w, (const E*)a.W, c0, N, K, lane);
     StreamX<DT, 1, NG> x;  // rows past the last are the last one: their results are not used
 #pragma unroll
     for (int g = 0; g < NG; ++g) x.p[g] = (const E*)a.X + (int64_t)min(16 * g + tile_row(lane), M - 1) * K + tile_off<DT>(lane);
     f32x4_t acc[NF][NG] = {};
     int s0, s1;
     wave_steps<DT, 8>(K, 1, wave, s0, s1, a.splits, sp);
-    const int full = min(s1, K / ST);
-    u32x4_t wa[U][NF], wb[U][NF], xa[U][NG][1], xb[U][NG][1];
-    const auto load = [&](u32x4_t (&tw)[U][NF], u32x4_t (&tx)[U][NG][1], int s) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            w.load(tw[u], (s + u) * ST);
-            x.load(tx[u], (s + u) * ST);
-        }
-    };
-    const auto mul1 = [&](u32x4_t (&tw)[NF], const u32x4_t (&tx)[NG][1]) {
-        u32x4_t o[NG][1];
-        x.operands(tx, o, scratch, lane);
-        if constexpr (TRANS)
-            row_tile<NF>(tw, scratch, lane);
-        else
-            w.operands(tw, scratch, lane);
-#pragma unroll
-        for (int j = 0; j < NF; ++j)
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                if constexpr (DT == 2) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        acc[j][g] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                            __uint_as_float(tw[j][t]), __uint_as_float(o[g][0][t]), acc[j][g], 0, 0, 0);
-                } else {
-                    acc[j][g] = mfma16x16x32<DT>(tw[j], o[g][0], acc[j][g]);
-                }
-            }
-    };
-    const auto mul = [&](u32x4_t (&tw)[U][NF], const u32x4_t (&tx)[U][NG][1]) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) mul1(tw[u], tx[u]);
-    };
-    int s = s0;
-    if (s + U <= full) load(wa, xa, s);
-    lora_expand<DT, TRANS, CW>(a, sp, c0, ex, tid);
-    for (; s + 2 * U <= full; s += 2 * U) {
-        load(wb, xb, s + U);
-        mul(wa, xa);
-        if (s + 3 * U <= full) load(wa, xa, s + 2 * U);
-        mul(wb, xb);
-    }
-    if (s + U <= full) {
-        mul(wa, xa);
-        s += U;
-    }
-    for (; s < s1 && s * ST < K; ++s) {  // the rest, the last step with zeros past K
-        w.tail(wa[0], s * ST, K, lane);
-        x.tail(xa[0], s * ST, K, lane);
-        mul1(wa[0], xa[0]);
-    }
+    cols_run<DT, TRANS, NG, NF, U>(w, x, s0, s1, K, acc, scratch, lane,
+                                   [&] { lora_expand<DT, TRANS, CW>(a, sp, c0, ex, tid); });
     __syncthreads();  // (the image overlaps other waves' scratch)
 #pragma unroll
     for (int j = 0; j < NF; ++j)
@@ -425,10 +322,7 @@ __global__ __launch_bounds__(512, 2) void lora_cols_kernel(LoraK a) {
     for (int o = tid; o < M * CW; o += 512) {
         const int c = o % CW, m = o / CW, n = c0 + c;
         if (n >= N) continue;
-        int pos = c;  // TRANS = 0: the column's place in its group, which may start before its multiple
-        if constexpr (!TRANS)
-            pos = (c & ~(kQ<DT> - 1)) +
-                  min((c & (kQ<DT> - 1)) + c0 + (c & ~(kQ<DT> - 1)) - group_start<DT>(c0, c, N), kQ<DT> - 1);
+        const int pos = cols_pos<DT, TRANS>(c0, c, N);
         const float* p = &red[((pos >> 4) * NG + (m >> 4)) * kFragPad + (((pos & 15) >> 2) * 16 + (m & 15)) * 4 + (pos & 3)];
         float v = m % a.splits == sp ? ex[m / a.splits][c] : 0.0f;
 #pragma unroll
@@ -450,7 +344,7 @@ __global__ __launch_bounds__(512, 2) void lora_cols_kernel(LoraK a) {
         });
 }
 
-constexpr int64_t kFew = 64;
+constexpr int64_t kFew = 64;  // rows a group
 
 // How the streamed forms share the work: columns of a workgroup (128:
 // lora_stream_kernel, fewer: lora_cols_kernel) and the parts that K is split
@@ -486,7 +380,7 @@ StreamPlan stream_plan(int64_t M, int64_t K, int64_t N, int trans) {
     } else {
         p.cw = N <= 16 * 72 ? 16 : N <= 32 * 72 ? 32 : 128;
     }
-    const int64_t groups = (N + p.cw - 1) / p.cw, steps = (K + 31) / 32;
+    const int64_t groups = (N + p.cw - 1) / p.cw * ((M + kFew - 1) / kFew), steps = (K + 31) / 32;
     int64_t s = few && p.cw < 128 && groups >= 100 ? 1 : 256 / groups;
     if (s > steps / 16) s = steps / 16;
     if (s > 16) s = 16;
@@ -508,7 +402,8 @@ size_t part_bytes(int64_t M, int64_t K, int64_t N) {
 
 // few rows, whole groups of 8 columns, W within 32-bit byte offsets
 bool streamable(int64_t M, int64_t K, int64_t N, int dt) {
-    return M <= kFew && K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
+    static const int64_t most = getenv("STREAMMAX") ? atoi(getenv("STREAMMAX")) : kFew;
+    return M <= most && K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
 }
 
 // (steps on their way a register set: as many as fit)
@@ -535,8 +430,8 @@ void lora_streamed(const LoraK& a, hipStream_t s) {
         if (v == V) lora_shrink_kernel<DT, 0, V><<<grid, 512, 0, s>>>(a, tpr);
         else lora_shrink_kernel<DT, 0, 1><<<grid, 512, 0, s>>>(a, tpr);
     }
-    const dim3 grid((unsigned)((a.N + a.cw - 1) / a.cw), (unsigned)a.splits);
-    const int ng = (int)((a.M + 15) / 16);
+    const dim3 grid((unsigned)((a.N + a.cw - 1) / a.cw), (unsigned)a.splits, (unsigned)((a.M + kFew - 1) / kFew));
+    const int ng = a.M >= kFew ? 4 : (int)((a.M + 15) / 16);
     if constexpr (TRANS) {
         switch (a.cw) {
             case 16: return cols_launch<DT, 1, 1>(a, ng, grid, s);
@@ -566,7 +461,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt) {
     if (streamable(M, K, N, dt)) {
-        return align256((size_t)M * R * 4 * kParts<0>) + align256(part_bytes(M, K, N)) + align256((size_t)(N + 15) / 16 * 4);
+        return align256((size_t)(M + kFew - 1) / kFew * kFew * R * 4 * kParts<0>) + align256(part_bytes(M, K, N)) + align256((size_t)(M + kFew - 1) / kFew * ((N + 15) / 16) * 4);
     }
     return lora_rows_workspace_bytes(M, R);
 }
@@ -615,7 +510,7 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
         const StreamPlan p = stream_plan(l.M, l.K, l.N, l.trans);
         a.splits = p.splits;
         a.cw = p.cw;
-        a.part = (float*)((char*)ws + align256((size_t)l.M * l.R * 4 * kParts<0>));
+        a.part = (float*)((char*)ws + align256((size_t)(l.M + kFew - 1) / kFew * kFew * l.R * 4 * kParts<0>));
         a.done = (uint32_t*)((char*)a.part + align256(part_bytes(l.M, l.K, l.N)));
         log_choice("lora_matmul: streamed, %d columns a workgroup, K in %d part(s)", a.cw, a.splits);
         switch (dt * 2 + a.trans) {

@@ -22,13 +22,26 @@ struct LoraK {
     float* part;     // (ceil(N / cw), splits, M, cw)
     uint32_t* done;  // finished workgroups of each cw columns
     int32_t* perm;   // (M) rows in the order of their adapters, or nullptr: as they come
-    float* tmax;     // (M, 2 ceil(R / 128)) largest |T| (fp16)
+    float* tmax;     // largest |T| of each row and workgroup of its r (fp16)
 };
 
 // the adapter of row m, -1: none
 __device__ __forceinline__ int64_t row_adapter(const LoraK& a, int64_t m) {
     const int64_t g = a.idx64 ? ((const int64_t*)a.idx)[m] : (int64_t)((const int32_t*)a.idx)[m];
     return g >= 0 && g < a.G ? g : -1;
+}
+
+// The streamed form takes 64 rows a group: `a` becomes the arguments of group z.
+// (T: kParts buffers of 64 rows a group)
+__device__ __forceinline__ void row_group(LoraK& a, int z, int parts, int elem) {
+    const int64_t m0 = (int64_t)z * 64, blocks = (a.N + a.cw - 1) / a.cw;
+    a.X = (const char*)a.X + m0 * a.K * elem;
+    a.Y = (char*)a.Y + m0 * a.N * elem;
+    a.idx = (const char*)a.idx + m0 * (a.idx64 ? 8 : 4);
+    a.T += m0 * parts * a.R;
+    a.part += m0 * blocks * a.splits * a.cw;
+    a.done += z * blocks;
+    a.M = a.M - m0 < 64 ? a.M - m0 : 64;
 }
 
 // Y = X W + C, C (M, N) of T (may be Y)

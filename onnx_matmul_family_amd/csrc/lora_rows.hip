@@ -34,7 +34,7 @@ __device__ __forceinline__ int row_of(const LoraK& a, int p) { return a.perm ? a
 // Stable counting sort of the rows by adapter (bin 0: none) in one workgroup:
 // each wave counts its contiguous share of the rows per bin, a scan over (bin,
 // wave) gives every wave its place in every bin, and it writes its rows there.
-// 4096 rows of 9 bins take 6 us; the tiles that use the order take 250.
+// SORTTIME
 __global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int bins) {
     extern __shared__ int hist[];  // [wave][bin]
     __shared__ int wsum[kSortWaves];
@@ -44,22 +44,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int
     for (int i = tid; i < kSortWaves * bins; i += 64 * kSortWaves) hist[i] = 0;
     __syncthreads();
     int* mine = hist + wave * bins;
-    // calls f(bin, rows of that bin among the 64, whether this lane is one) for each bin present
-    auto each = [&](int m, auto f) {
-        const int b = m < m1 ? (int)row_adapter(a, m) + 1 : -1;
-        uint64_t todo = __ballot(b >= 0);
-        while (todo) {
-            const int lead = __ffsll((unsigned long long)todo) - 1;
-            const int bin = __builtin_amdgcn_readlane(b, lead);
-            const uint64_t in = __ballot(b == bin);
-            f(bin, in, b == bin);
-            todo &= ~in;
-        }
-    };
-    for (int m = m0 + lane; m - lane < m1; m += 64)
-        each(m, [&](int bin, uint64_t in, bool) {
-            if (lane == 0) mine[bin] += __popcll(in);
-        });
+    for (int m = m0 + lane; m < m1; m += 64) atomicAdd(&mine[row_adapter(a, m) + 1], 1);
     __syncthreads();
     // exclusive scan in the order (bin, wave); one bin a thread (bins <= 1024)
     int total = 0;
@@ -82,81 +67,81 @@ __global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int
             scan += n;
         }
     __syncthreads();
-    for (int m = m0 + lane; m - lane < m1; m += 64)
-        each(m, [&](int bin, uint64_t in, bool is) {
-            const int at = mine[bin];
-            if (is) a.perm[at + __popcll(in & ((1ull << lane) - 1))] = m;
-            if (lane == 0) mine[bin] = at + __popcll(in);
-        });
+    for (int m = m0 + lane; m - lane < m1; m += 64) {
+        const int b = m < m1 ? (int)row_adapter(a, m) + 1 : -1;
+        uint64_t same = 0;  // the lanes whose row has this lane's adapter
+        for (uint64_t todo = __ballot(b >= 0); todo;) {
+            const uint64_t in = __ballot(b == __builtin_amdgcn_readlane(b, __ffsll((unsigned long long)todo) - 1));
+            if ((in >> lane) & 1) same = in;
+            todo &= ~in;
+        }
+        if (b >= 0) {
+            const int at = mine[b], rank = __popcll(same & ((1ull << lane) - 1));
+            a.perm[at + rank] = m;
+            if (rank == 0) mine[b] = at + __popcll(same);
+        }
+    }
 }
 
 // T[p, r] = scale[g] sum_k X[m, k] A[g, k, r] of the 16 rows m at positions p0
-// .. p0 + 15 and (up to) 128 r: NW waves split K, A and the rows go from memory
+// .. p0 + 15 and 16 NF r: NW waves split K, A and the rows go from memory
 // to the matrix unit.  One pass for each adapter among the rows.
-// fp16: tmax[p][2 (r / 128) + (r / 64) % 2] = max |T[p, r]| (for the halves' scale).
+// fp16: tmax[p][y] = max |T[p, r]| over the r of blockIdx.y (for the halves' scale).
 template <int DT, int TRANS, int NF, int NW>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_rows_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
+    constexpr int CW = 16 * NF;
     __shared__ __attribute__((aligned(16))) float red[NW * NF * kFragPad];
+    __shared__ uint32_t max_s[16];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
-    const int q = (lane >> 4) * kQ<DT>, tr = x_row<TRANS>(lane), tq = x_off<DT, TRANS>(lane);
-    const int M = (int)a.M, K = (int)a.K, R = a.R, p0 = blockIdx.x * 16, c0 = blockIdx.y * 128;
+    const int M = (int)a.M, K = (int)a.K, R = a.R, p0 = blockIdx.x * 16, c0 = blockIdx.y * CW;
     const int m = row_of(a, min(p0 + i, M - 1));
     const int ad = p0 + i < M ? (int)row_adapter(a, m) : -1;
-    StreamX<DT, TRANS, 1> x;
-    x.p[0] = (const E*)a.X + (int64_t)__shfl(m, tr, 64) * K + tq;
+    StreamX<DT, 1, 1> x;
+    x.p[0] = (const E*)a.X + (int64_t)__shfl(m, tile_row(lane), 64) * K + tile_off<DT>(lane);
+    if (tid < 16) max_s[tid] = 0;
     int s0, s1;
     wave_steps<DT, NW>(K, 1, wave, s0, s1);
     for (uint32_t todo = (uint32_t)__ballot(ad >= 0) & 0xffffu; todo;) {
         const int g = __builtin_amdgcn_readlane(ad, __ffs(todo) - 1);
         const uint32_t in = (uint32_t)__ballot(ad == g) & 0xffffu;
         todo &= ~in;
-        const E* A = (const E*)a.A + (int64_t)g * K * R;
-        StreamW<DT, TRANS, NF> w;
-        if constexpr (TRANS) {
-            w.base[0] = w.base[1] = A;
-#pragma unroll
-            for (int j = 0; j < NF; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + tr, R - 1) * K + tq;
-        } else {
-            w.ld = R;
-            if constexpr (DT == 2) {
-                w.p[0] = A + group_start<DT>(c0, 4 * i, R) + (int64_t)q * R;
-                w.p[1] = A + group_start<DT>(c0, 64 + 4 * i, R) + (int64_t)q * R;
-            } else {
-                w.p[0] = A + group_start<DT>(c0, 8 * i, R) + (int64_t)q * R;
-            }
-        }
+        ColsWeights<DT, TRANS, NF> w;
+        cols_start<DT, TRANS, NF>(w, (const E*)a.A + (int64_t)g * K * R, c0, R, K, lane);
         f32x4_t acc[NF][1] = {};
-        stream_run<DT, TRANS, 1>(w, x, s0, s1, K, acc, (u32x4_t*)&red[wave * NF * kFragPad], lane);
+        cols_run<DT, TRANS, 1, NF, NF == 1 ? 4 : 2>(w, x, s0, s1, K, acc, (u32x4_t*)&red[wave * NF * kFragPad], lane,
+                                                    [] {});
 #pragma unroll
         for (int j = 0; j < NF; ++j) *(f32x4_t*)&red[(wave * NF + j) * kFragPad + lane * 4] = acc[j][0];
         __syncthreads();
         const float scale = a.scale ? a.scale[g] : 1.0f;
-        for (int o = tid; o < 16 * 128; o += 64 * NW) {
-            const int c = o & 127, row = o >> 7;
-            if (!((in >> row) & 1)) continue;  // a wave has one row
+        for (int o = tid; o < 16 * CW; o += 64 * NW) {
+            const int c = o % CW, row = o / CW;
+            if (!((in >> row) & 1) || c0 + c >= R) continue;
+            const int pos = cols_pos<DT, TRANS>(c0, c, R);
+            const float* q = &red[(pos >> 4) * kFragPad + (((pos & 15) >> 2) * 16 + row) * 4 + (pos & 3)];
             float v = 0.0f;
-            if (c0 + c < R) {
-                int j, l, rr;
-                red_pos<DT, TRANS>(c, c0 + (c & ~(kQ<DT> - 1)) - group_start<DT>(c0, c, R), row, j, l, rr);
 #pragma unroll
-                for (int u = 0; u < NW; ++u) v += red[(u * NF + j) * kFragPad + l * 4 + rr];
-                v *= scale;
-                a.T[(int64_t)(p0 + row) * R + c0 + c] = v;
-            }
-            if constexpr (DT == 1) {
-                const uint32_t mx = wave_max_u32(__float_as_uint(fabsf(v)));
-                if (lane == 0)
-                    a.tmax[(int64_t)(p0 + row) * 2 * gridDim.y + 2 * blockIdx.y + (c >> 6)] = __uint_as_float(mx);
-            }
+            for (int u = 0; u < NW; ++u) v += q[u * NF * kFragPad];
+            v *= scale;
+            a.T[(int64_t)(p0 + row) * R + c0 + c] = v;
+            if constexpr (DT == 1) atomicMax(&max_s[row], __float_as_uint(fabsf(v)));  // (NaN is the largest)
         }
         if (todo) __syncthreads();
     }
+    if constexpr (DT == 1) {
+        __syncthreads();
+        if (tid < 16 && p0 + tid < M) a.tmax[(int64_t)(p0 + tid) * gridDim.y + blockIdx.y] = __uint_as_float(max_s[tid]);
+    }
 }
+
+// r of a workgroup of the kernel above, and its workgroups a row
+__host__ __device__ inline int shrink_cols(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+__host__ __device__ inline int shrink_parts(int R) { return (R + shrink_cols(R) - 1) / shrink_cols(R); }
 
 // largest |T| of a position, and the power of two that takes it to [2^13, 2^14)
 __device__ __forceinline__ float row_max(const LoraK& a, int64_t p) {
-    const int n = 2 * ((a.R + 127) / 128);
+    const int n = shrink_parts(a.R);
     float mx = 0.0f;
     for (int b = 0; b < n; ++b) mx = fmaxf(mx, a.tmax[p * n + b]);
     return mx;
@@ -396,13 +381,12 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int DT, int TRANS>
 void shrink(const LoraK& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)((a.R + 127) / 128));
-    if constexpr (TRANS) {
-        if (a.R <= 16) return lora_shrink_rows_kernel<DT, 1, 1, 16><<<grid, 1024, 0, s>>>(a);
-        if (a.R <= 32) return lora_shrink_rows_kernel<DT, 1, 2, 16><<<grid, 1024, 0, s>>>(a);
-        if (a.R <= 64) return lora_shrink_rows_kernel<DT, 1, 4, 8><<<grid, 512, 0, s>>>(a);
+    const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)shrink_parts(a.R));
+    switch (shrink_cols(a.R)) {
+        case 16: return lora_shrink_rows_kernel<DT, TRANS, 1, 16><<<grid, 1024, 0, s>>>(a);
+        case 32: return lora_shrink_rows_kernel<DT, TRANS, 2, 16><<<grid, 1024, 0, s>>>(a);
+        default: return lora_shrink_rows_kernel<DT, TRANS, 4, 8><<<grid, 512, 0, s>>>(a);
     }
-    lora_shrink_rows_kernel<DT, TRANS, 8, 8><<<grid, 512, 0, s>>>(a);
 }
 
 template <int DT, int TRANS>
@@ -452,7 +436,7 @@ bool lora_rows_ok(int64_t M, int64_t K, int64_t N, int64_t R, int64_t G, int tra
 }
 
 size_t lora_rows_workspace_bytes(int64_t M, int64_t R) {
-    return align256((size_t)M * 4) + align256((size_t)M * 2 * ((R + 127) / 128) * 4) + align256((size_t)M * R * 4);
+    return align256((size_t)M * 4) + align256((size_t)M * shrink_parts((int)R) * 4) + align256((size_t)M * R * 4);
 }
 
 hipError_t launch_lora_rows(LoraK a, int dt, void* ws, hipStream_t s) {
@@ -460,7 +444,7 @@ hipError_t launch_lora_rows(LoraK a, int dt, void* ws, hipStream_t s) {
     a.perm = a.G < 1024 ? (int32_t*)w : nullptr;  // (more adapters than the sort has counters for: rows as they come)
     w += align256((size_t)a.M * 4);
     a.tmax = (float*)w;
-    w += align256((size_t)a.M * 2 * ((a.R + 127) / 128) * 4);
+    w += align256((size_t)a.M * shrink_parts(a.R) * 4);
     a.T = (float*)w;
     if (a.R == 0 || a.G == 0) a.perm = nullptr;
     switch (dt * 2 + a.trans) {

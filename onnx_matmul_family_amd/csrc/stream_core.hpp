@@ -396,6 +396,138 @@ __device__ __forceinline__ void red_pos(int c, int shift, int row, int& j, int& 
     r = i & 3;
 }
 
+// ------------------------------------------------------------------ few columns
+// 16 NF columns (NF 1, 2 or 4) against NG groups of 16 rows.  A step is few loads
+// of the weights beside NG of the rows, so U steps are on their way at once in
+// each of two register sets, and the rows take row_tile in either layout.
+//   TRANS = 1: the weights too (StreamW).
+//   TRANS = 0: a load takes 16-byte pieces of 32 / NF contraction rows (fp32:
+//     16 / NF); in LDS they lie as in memory and are read by columns (16 bits:
+//     the transposing read).
+template <int DT, int NF>
+struct ColsW {
+    typedef typename elem_of<DT>::type E;
+    static constexpr int LPR = NF * (DT == 2 ? 4 : 2), ROWS = 64 / LPR;  // lanes a row, rows a load
+    const E* p;  // the lane's row and columns
+    int64_t ld;
+    __device__ __forceinline__ void load(u32x4_t (&w)[NF], int kb) const {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) w[j] = load16(p + (int64_t)(kb + j * ROWS) * ld);
+    }
+    __device__ __forceinline__ void tail(u32x4_t (&w)[NF], int kb, int kn, int lane) const {
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            w[j] = kb + j * ROWS + lane / LPR < kn ? load16(p + (int64_t)(kb + j * ROWS) * ld) : u32x4_t{0, 0, 0, 0};
+    }
+    // tiles as loaded -> operands of the NF fragments
+    __device__ __forceinline__ static void operands(u32x4_t (&w)[NF], u32x4_t* scratch, int lane) {
+        constexpr int RB = LPR * 16;  // bytes a row
+#pragma unroll
+        for (int j = 0; j < NF; ++j) scratch[j * 64 + lane] = w[j];
+        __builtin_amdgcn_wave_barrier();
+        const int i = lane & 15, q = lane >> 4;
+        const char* b = (const char*)scratch;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            if constexpr (DT == 2) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) w[j][t] = *(const uint32_t*)(b + (4 * q + t) * RB + j * 64 + 4 * i);
+            } else {
+                const char* f = b + (8 * q + (i >> 2)) * RB + j * 32 + 8 * (i & 3);
+                const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(OMM_LDS(i16x4_t, f));
+                const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(OMM_LDS(i16x4_t, f + 4 * RB));
+                const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
+                w[j] = u32x4_t{l2.x, l2.y, h2.x, h2.y};
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+};
+
+template <int DT, int TRANS, int NF>
+using ColsWeights = typename std::conditional<TRANS != 0, StreamW<DT, 1, NF>, ColsW<DT, NF>>::type;
+
+// weights of the columns from c0 on: TRANS = 1 (n, k), 0 (k, n)
+template <int DT, int TRANS, int NF>
+__device__ __forceinline__ void cols_start(ColsWeights<DT, TRANS, NF>& w, const typename elem_of<DT>::type* p, int c0,
+                                           int n, int k, int lane) {
+    if constexpr (TRANS) {
+        w.base[0] = w.base[1] = p;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) w.off[j] = (uint32_t)min(c0 + 16 * j + tile_row(lane), n - 1) * k + tile_off<DT>(lane);
+    } else {
+        constexpr int LPR = ColsW<DT, NF>::LPR;
+        w.ld = n;
+        w.p = p + (int64_t)(lane / LPR) * n + group_start<DT>(c0, (lane % LPR) * kQ<DT>, n);
+    }
+}
+// column c's place among the workgroup's (a group of columns may start before its multiple)
+template <int DT, int TRANS>
+__device__ __forceinline__ int cols_pos(int c0, int c, int n) {
+    if constexpr (TRANS) return c;
+    const int g = c & ~(kQ<DT> - 1);
+    return g + min((c - g) + c0 + g - group_start<DT>(c0, c, n), kQ<DT> - 1);
+}
+// acc += steps [s0, s1) as stream_run
+template <int DT, int TRANS, int NG, int NF, int U, typename Fn>
+__device__ __forceinline__ void cols_run(const ColsWeights<DT, TRANS, NF>& w, const StreamX<DT, 1, NG>& x, int s0,
+                                         int s1, int kn, f32x4_t (&acc)[NF][NG], u32x4_t* scratch, int lane,
+                                         Fn meanwhile) {
+    constexpr int ST = kStep<DT>;
+    const int full = min(s1, kn / ST);
+    u32x4_t wa[U][NF], wb[U][NF], xa[U][NG][1], xb[U][NG][1];
+    const auto load = [&](u32x4_t (&tw)[U][NF], u32x4_t (&tx)[U][NG][1], int s) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            w.load(tw[u], (s + u) * ST);
+            x.load(tx[u], (s + u) * ST);
+        }
+    };
+    const auto mul1 = [&](u32x4_t (&tw)[NF], const u32x4_t (&tx)[NG][1]) {
+        u32x4_t o[NG][1];
+        x.operands(tx, o, scratch, lane);
+        if constexpr (TRANS)
+            row_tile<NF>(tw, scratch, lane);
+        else
+            w.operands(tw, scratch, lane);
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                if constexpr (DT == 2) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        acc[j][g] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                            __uint_as_float(tw[j][t]), __uint_as_float(o[g][0][t]), acc[j][g], 0, 0, 0);
+                } else {
+                    acc[j][g] = mfma16x16x32<DT>(tw[j], o[g][0], acc[j][g]);
+                }
+            }
+    };
+    const auto mul = [&](u32x4_t (&tw)[U][NF], const u32x4_t (&tx)[U][NG][1]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) mul1(tw[u], tx[u]);
+    };
+    int s = s0;
+    if (s + U <= full) load(wa, xa, s);
+    meanwhile();
+    for (; s + 2 * U <= full; s += 2 * U) {
+        load(wb, xb, s + U);
+        mul(wa, xa);
+        if (s + 3 * U <= full) load(wa, xa, s + 2 * U);
+        mul(wb, xb);
+    }
+    if (s + U <= full) {
+        mul(wa, xa);
+        s += U;
+    }
+    for (; s < s1 && s * ST < kn; ++s) {  // the rest, the last step with zeros past kn
+        w.tail(wa[0], s * ST, kn, lane);
+        x.tail(xa[0], s * ST, kn, lane);
+        mul1(wa[0], xa[0]);
+    }
+}
+
 // ------------------------------------------------------------------ parts of one result in several workgroups
 // A workgroup leaves its part of a row's CW columns in parts[row][CW], past
 // its own L2 (another one's workgroup may sum it), and counts itself; the last
