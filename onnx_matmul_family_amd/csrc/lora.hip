@@ -3,7 +3,6 @@
 // (a row whose g is outside [0, G) has no adapter).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "kernels.hpp"
 #include "lora_args.hpp"
@@ -400,10 +399,23 @@ size_t part_bytes(int64_t M, int64_t K, int64_t N) {
     return most;
 }
 
-// few rows, whole groups of 8 columns, W within 32-bit byte offsets
+// whole groups of 8 columns, W within 32-bit byte offsets, row groups in a grid
 bool streamable(int64_t M, int64_t K, int64_t N, int dt) {
-    static const int64_t most = getenv("STREAMMAX") ? atoi(getenv("STREAMMAX")) : kFew;
-    return M <= most && K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
+    return (M + kFew - 1) / kFew < 65536 && K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
+}
+
+// Where the streamed form (W once per 64 rows, mostly from the caches) is ahead
+// of the tiles over sorted rows, or of the dense product after the adapters'
+// term where there are no tiles.  us a call, streamed / other (bf16, rank 16):
+//   K, N (trans)         M = 256     M = 512      M = 1024     M = 2048
+//   4096, 1024 (1)     18 /  62     32 /  64     58 /  63    109 /  67
+//   4096, 4096 (1)     32 /  67     58 /  64    108 /  66    208 /  82
+//   4096, 8192 (1)     57 /  68    107 /  65    205 /  79    403 / 129
+//   1175, 3329 (1)     35 / 133     67 / 188    124 / 180    222 / 218   (no tiles)
+//   4000, 8190 (0)     47 / 423     85 / 427    161 / 605    312 / 1174  (no tiles)
+bool stream_ahead(int64_t M, int64_t K, int64_t N, bool tiles) {
+    if (M <= 256) return true;
+    return tiles ? M <= 512 && K * N <= 1 << 24 : true;
 }
 
 // (steps on their way a register set: as many as fit)
@@ -460,10 +472,13 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt) {
-    if (streamable(M, K, N, dt)) {
-        return align256((size_t)(M + kFew - 1) / kFew * kFew * R * 4 * kParts<0>) + align256(part_bytes(M, K, N)) + align256((size_t)(M + kFew - 1) / kFew * ((N + 15) / 16) * 4);
-    }
-    return lora_rows_workspace_bytes(M, R);
+    // (the form depends on layout and alignment too: room for each)
+    const size_t rows = M > kFew || !streamable(M, K, N, dt) ? lora_rows_workspace_bytes(M, R) : 0;
+    if (!streamable(M, K, N, dt)) return rows;
+    const size_t groups = (size_t)(M + kFew - 1) / kFew;
+    const size_t stream = align256(groups * kFew * R * 4 * kParts<0>) + align256(part_bytes(M, K, N)) +
+                          align256(groups * ((N + 15) / 16) * 4);
+    return rows > stream ? rows : stream;
 }
 
 hipError_t lora_add_dense(const LoraK& a, const void* C, int dt, hipStream_t s) {
@@ -506,7 +521,7 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
     a.R = (int)l.R;
     a.trans = l.trans;
     a.idx64 = l.idx64;
-    if (streamable(l.M, l.K, l.N, dt)) {
+    if (streamable(l.M, l.K, l.N, dt) && stream_ahead(l.M, l.K, l.N, lora_tiles_ok(a, dt))) {
         const StreamPlan p = stream_plan(l.M, l.K, l.N, l.trans);
         a.splits = p.splits;
         a.cw = p.cw;

@@ -401,11 +401,7 @@ hipError_t rows_run(const LoraK& a, hipStream_t s) {
         lora_sort_kernel<<<1, 64 * kSortWaves, kSortWaves * (a.G + 1) * sizeof(int), s>>>(a, (int)a.G + 1);
     if (a.R > 0 && a.G > 0) shrink<DT, TRANS>(a, s);
     if constexpr (DT < 2) {
-        // 16-byte rows for the DMA, 32-bit byte offsets into X and a tile of W
-        const bool dma = a.K % 8 == 0 && a.K > 0 && (TRANS || a.N % 8 == 0) &&
-                         (((uintptr_t)a.X | (uintptr_t)a.W) & 15) == 0 && a.M * a.K * 2 < (1LL << 31) &&
-                         256 * (TRANS ? a.K : a.N) * 2 < (1LL << 31);
-        if (dma) {
+        if (lora_tiles_ok(a, DT)) {
             const int64_t big = (a.M + 255) / 256 * ((a.N + 255) / 256);
             if (big >= 256) {
                 const int tm = (int)((a.M + 255) / 256), tn = (int)((a.N + 255) / 256);
@@ -426,6 +422,13 @@ hipError_t rows_run(const LoraK& a, hipStream_t s) {
 }
 
 }  // namespace
+
+// 16-byte rows for the DMA, 32-bit byte offsets into X and a tile of W
+bool lora_tiles_ok(const LoraK& a, int dt) {
+    return dt < 2 && a.K % 8 == 0 && a.K > 0 && (a.trans || a.N % 8 == 0) &&
+           (((uintptr_t)a.X | (uintptr_t)a.W) & 15) == 0 && a.M * a.K * 2 < (1LL << 31) &&
+           256 * (a.trans ? a.K : a.N) * 2 < (1LL << 31);
+}
 
 // whole groups of 8 (columns of a fp32 group: 4), one adapter's matrices within
 // 32-bit offsets, tile counts and rows in 32 bits
