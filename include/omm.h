@@ -270,14 +270,15 @@ int omm_grouped_matmul_check(const void* workspace, void* stream, int64_t* inval
  *   B (G, N, R) (as linear layers store them).
  *   adapter_indices (M) OMM_I32 / OMM_I64: a row whose index is outside [0, G)
  *   (-1 by custom) has no adapter.  adapter_scale (G) OMM_F32 or NULL (1).
- *   R <= 256 (else OMM_ERR_UNSUPPORTED).  One rounding to T of the whole sum
- *   up to OMM_LORA_FEW_ROWS rows; above, and for layouts that take the
- *   element-wise path, the adapter's term (with the bias) is rounded to T once
- *   before the sum.
+ *   R <= 256 (else OMM_ERR_UNSUPPORTED).  The middle product X A is held in fp32
+ *   (or two halves of T); one rounding to T of the whole sum.  Only for a W of
+ *   2 GiB or more, or K or N under 8, may the adapter's term (with the bias) be
+ *   rounded to T once before the sum.
+ *   A row's result does not depend on the other rows' adapters (an infinity or
+ *   NaN in one adapter stays in its rows) and is the same from call to call.
  * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE, OMM_ERR_UNSUPPORTED,
  * OMM_ERR_WORKSPACE.
  */
-#define OMM_LORA_FEW_ROWS 64
 size_t omm_lora_matmul_workspace_size(int64_t M, int64_t K, int64_t N, int64_t R, int32_t dtype);
 int omm_lora_matmul(const omm_tensor* X, const omm_tensor* W, const omm_tensor* A, const omm_tensor* B,
                     const omm_tensor* adapter_indices, const omm_tensor* adapter_scale, const omm_tensor* bias,

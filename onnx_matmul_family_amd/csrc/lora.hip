@@ -399,9 +399,9 @@ size_t part_bytes(int64_t M, int64_t K, int64_t N) {
     return most;
 }
 
-// whole groups of 8 columns, W within 32-bit byte offsets, row groups in a grid
+// whole groups of 8 columns, W within 32-bit byte offsets, a row a grid index
 bool streamable(int64_t M, int64_t K, int64_t N, int dt) {
-    return (M + kFew - 1) / kFew < 65536 && K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
+    return M < 65536 && K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
 }
 
 // Where the streamed form (W once per 64 rows, mostly from the caches) is ahead
@@ -521,7 +521,9 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
     a.R = (int)l.R;
     a.trans = l.trans;
     a.idx64 = l.idx64;
-    if (streamable(l.M, l.K, l.N, dt) && stream_ahead(l.M, l.K, l.N, lora_tiles_ok(a, dt))) {
+    const bool rows_ok = lora_rows_ok(l.M, l.K, l.N, l.R, l.G, l.trans);
+    if (streamable(l.M, l.K, l.N, dt) &&
+        (!rows_ok || stream_ahead(l.M, l.K, l.N, lora_tiles_ok(a, dt)))) {
         const StreamPlan p = stream_plan(l.M, l.K, l.N, l.trans);
         a.splits = p.splits;
         a.cw = p.cw;
@@ -538,7 +540,7 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
         }
         return hipGetLastError();
     }
-    if (lora_rows_ok(l.M, l.K, l.N, l.R, l.G, l.trans)) return launch_lora_rows(a, dt, ws, s);
+    if (rows_ok) return launch_lora_rows(a, dt, ws, s);
     log_choice("lora_matmul: element-wise");
     const int64_t nblk = (l.N + 255) / 256;
     const dim3 gs((unsigned)l.M), gd((unsigned)(l.M * nblk));

@@ -218,8 +218,10 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
 // (mainloop_dma16, rows of X gathered through the order), then T B block by
 // block from registers.
 // BKM: W (N, K), B (G, N, R); else W (K, N), B (G, R, N).
-template <int DT, bool BKM, int BT>
-__global__ __launch_bounds__(NT) void lora_tile_kernel(LoraK a, int tiles_m, int tiles_n) {
+// TH: column fragments of a pass of the epilogue; fewer (4 of 8) leave the
+// registers to keep B's fragments of 64 r from block to block instead of 32.
+template <int DT, bool BKM, int BT, int TH>
+__global__ __launch_bounds__(NT, BT == 128 ? 2 : 1) void lora_tile_kernel(LoraK a, int tiles_m, int tiles_n) {
     constexpr int BM = BT, BN = BT, TM = BM / 32, TN = BN / 32;
     constexpr int STAGE = (BM + BN) * KSTEP * 2;
     __shared__ __attribute__((aligned(1024))) char smem0[STAGE];
@@ -258,35 +260,68 @@ __global__ __launch_bounds__(NT) void lora_tile_kernel(LoraK a, int tiles_m, int
     else
         mainloop_dma16<BM, BN, DT, true, BKM, true>(acc, smem0, smem1, srcA, srcB, nk, lane, wm, wn, wave);
 
-    // d = T B of block i of the wave (rows 16 i .. + 15, in the accumulators'
-    // layout), one adapter of the block after another.  Lane l: row l % 16, r =
-    // r0 + 8 (l / 16) .. + 7.  The accumulators themselves are only read: an
-    // epilogue that multiplied into them made the compiler spill them.
+    // d = T B of block i of the wave (rows 16 i .. + 15) and TH column fragments
+    // from jh on, in the accumulators' layout, one adapter of the block after
+    // another.  Lane l: row l % 16, r = r0 + 8 (l / 16) .. + 7.  The accumulators
+    // themselves are only read: an epilogue that multiplied into them made the
+    // compiler spill them.
     const int i16 = lane & 15, q = (lane >> 4) * 8, row0 = wm * (BM / 2), col0 = wn * (BN / 2);
     const uint16_t* Bp = (const uint16_t*)a.B;
-    u32x4_t bf[TN];  // B's fragments, kept from block to block where one step covers R
+    constexpr int HS = TH == 8 ? 1 : 2;
+    u32x4_t bf[HS][TH];  // B's fragments, kept from block to block where HS steps cover R
     int held = -1;
-    auto load_b = [&](int g, int r0, int n) {
+    // BKM = false: 32 r of 64 columns pass through LDS for the transposing read
+    // (where no tile is staged, in the K loop's)
+    __shared__ u32x4_t bt_s[BKM || BT == 128 ? 1 : 4 * 256];
+    u32x4_t* bt = BT == 128 ? (u32x4_t*)smem0 + wave * 256 : bt_s + (BKM ? 0 : wave * 256);
+    auto load_b = [&](u32x4_t (&f)[TH], int g, int r0, int jh) {
+        const int c = n0 + col0 + 16 * jh;
+        if constexpr (BKM) {
+            const int n = max(0, min(8, R - r0 - q));
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int col = min(n0 + col0 + 16 * j + i16, N - 1);
-            if constexpr (BKM) {
-                bf[j] = load16_first(Bp + ((int64_t)g * N + col) * R + r0 + q, n);
-            } else {
-                bf[j] = u32x4_t{0, 0, 0, 0};
-                const uint16_t* b = Bp + ((int64_t)g * R + r0 + q) * N + col;
+            for (int j = 0; j < TH; ++j)
+                f[j] = load16_first(Bp + ((int64_t)g * N + min(c + 16 * j + i16, N - 1)) * R + r0 + q, n);
+        } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < n) bf[j][e >> 1] |= (uint32_t)b[(int64_t)e * N] << (16 * (e & 1));
-                fence_sched();  // 8 loads at a time: all 64 would spill
+            for (int h = 0; h < TH; h += 4) {
+                const uint16_t* p = Bp + ((int64_t)g * R + r0) * N + min(c + 16 * h + 8 * (lane & 7), N - 8);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int r = 8 * u + (lane >> 3);
+                    f[h + u] = r0 + r < R ? load16(p + (int64_t)r * N) : u32x4_t{0, 0, 0, 0};
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < TH; h += 4) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) bt[u * 64 + lane] = f[h + u];
+                __builtin_amdgcn_wave_barrier();
+                const char* l = (const char*)bt + (q + (i16 >> 2)) * 128 + 8 * (i16 & 3);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(OMM_LDS(i16x4_t, l + 32 * j));
+                    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(OMM_LDS(i16x4_t, l + 32 * j + 4 * 128));
+                    const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
+                    f[h + j] = u32x4_t{l2.x, l2.y, h2.x, h2.y};
+                }
+                __builtin_amdgcn_wave_barrier();
             }
         }
     };
-    auto delta = [&](int i, f32x4_t (&d)[TN]) {
+    auto t_row = [&](int i) { return a.T + (int64_t)min(m0 + row0 + 16 * i + i16, M - 1) * R + q; };
+    auto load_t = [&](u32x4_t (&raw)[2], const float* tp, int r0) {
+        const int n = max(0, min(8, R - r0 - q));
+        raw[0] = load16_first(tp + r0, n);
+        raw[1] = load16_first(tp + r0 + 4, n - 4);
+    };
+    u32x4_t ahead[2];  // the next block's first step of T
+    load_t(ahead, t_row(0), 0);
+    auto delta = [&](int i, int jh, f32x4_t (&d)[TH]) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) d[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < TH; ++j) d[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         const int ad = ad_s[row0 + 16 * i + i16];
-        const float* tp = a.T + (int64_t)min(m0 + row0 + 16 * i + i16, M - 1) * R + q;
+        const u32x4_t first[2] = {ahead[0], ahead[1]};
+        load_t(ahead, t_row(i + 1 < TM ? i + 1 : 0), 0);
         float scale = 1.0f, undo = 1.0f;
         if constexpr (DT == 1) {
             const int e = scale_exp(max_s[row0 + 16 * i + i16]);
@@ -296,22 +331,36 @@ __global__ __launch_bounds__(NT) void lora_tile_kernel(LoraK a, int tiles_m, int
         for (uint32_t todo = (uint32_t)__ballot(ad >= 0) & 0xffffu; todo;) {
             const int g = __builtin_amdgcn_readlane(ad, __ffs(todo) - 1);
             todo &= ~(uint32_t)__ballot(ad == g);
-            f32x4_t v[TN] = {};
-            for (int r0 = 0; r0 < R; r0 += 32) {
-                const int n = max(0, min(8, R - r0 - q));
-                const u32x4_t raw[2] = {load16_first(tp + r0, n), load16_first(tp + r0 + 4, n - 4)};
-                if (held != g) load_b(g, r0, n);
-                if (R <= 32) held = g;
+            f32x4_t v[TH] = {};
+            const auto step = [&](const u32x4_t (&f)[TH], int r0) {
+                u32x4_t raw[2] = {first[0], first[1]};
+                if (r0) load_t(raw, t_row(i), r0);
                 u32x4_t hi, lo;
                 split_halves<DT>(raw, scale, hi, lo);
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    v[j] = mfma16x16x32<DT>(bf[j], hi, v[j]);
-                    v[j] = mfma16x16x32<DT>(bf[j], lo, v[j]);
+                for (int j = 0; j < TH; ++j) {
+                    v[j] = mfma16x16x32<DT>(f[j], hi, v[j]);
+                    v[j] = mfma16x16x32<DT>(f[j], lo, v[j]);
+                }
+            };
+            if (R <= 32 * HS) {
+                if (held != g) {
+#pragma unroll
+                    for (int h = 0; h < HS; ++h)
+                        if (32 * h < R) load_b(bf[h], g, 32 * h, jh);
+                    held = g;
+                }
+#pragma unroll
+                for (int h = 0; h < HS; ++h)
+                    if (32 * h < R) step(bf[h], 32 * h);
+            } else {
+                for (int r0 = 0; r0 < R; r0 += 32) {
+                    load_b(bf[0], g, r0, jh);
+                    step(bf[0], r0);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+            for (int j = 0; j < TH; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) d[j][e] = ad == g ? v[j][e] * undo : d[j][e];
         }
@@ -319,62 +368,59 @@ __global__ __launch_bounds__(NT) void lora_tile_kernel(LoraK a, int tiles_m, int
 
     uint16_t* Y = (uint16_t*)a.Y;
     const uint16_t* bias = (const uint16_t*)a.bias;
-    if constexpr (BT == 256) {
-        // whole tiles leave through LDS as whole row segments (16-byte chunk c
-        // of row r in slot c ^ (r % 16))
-        if (n0 + BN <= N && N % 8 == 0 && ((uintptr_t)Y & 15) == 0) {
-            __syncthreads();  // every wave is done reading the last stage
-            char* stage = (wave < 2 ? smem0 : smem1) + (wave & 1) * (STAGE / 2);
-            const int h = lane >> 4;
-            static_for<0, TM>([&](auto ic) {
-                constexpr int i = decltype(ic)::value;
-                f32x4_t d[TN];
-                delta(i, d);
-                const int r = 16 * i + i16;
+    // whole tiles leave through LDS as whole row segments (16-byte chunk c of
+    // row r in slot c ^ (r % 16)), others by 4 columns
+    const bool staged = BT == 256 && n0 + BN <= N && N % 8 == 0 && ((uintptr_t)Y & 15) == 0;
+    char* stage = (wave < 2 ? smem0 : smem1) + (wave & 1) * (STAGE / 2);
+    __syncthreads();  // every wave is done reading the last stage
+    static_for<0, TN / TH>([&](auto hc) {
+        constexpr int jh = decltype(hc)::value * TH;
+        held = -1;
+        float cb[TH][4];
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const int n = n0 + col0 + 16 * j + 4 * h, c = 2 * j + (h >> 1);
-                    float v[4];
+        for (int j = 0; j < TH; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e] + d[j][e] + (bias ? from_bits<DT>(bias[n + e]) : 0.0f);
-                    *(u32x2_t*)(stage + r * 256 + ((c ^ i16) << 4) + ((h & 1) << 3)) =
-                        u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+            for (int e = 0; e < 4; ++e) {
+                const int n = n0 + col0 + 16 * (jh + j) + 4 * (lane >> 4) + e;
+                cb[j][e] = bias && n < N ? from_bits<DT>(bias[n]) : 0.0f;
+            }
+        static_for<0, TM>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            f32x4_t d[TH];
+            delta(i, jh, d);
+            const int m = row_s[row0 + 16 * i + i16];
+#pragma unroll
+            for (int j = 0; j < TH; ++j) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[i][jh + j][e] + d[j][e] + cb[j][e];
+                const u32x2_t o = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+                const int h = lane >> 4, n = n0 + col0 + 16 * (jh + j) + 4 * h;
+                if (staged) {
+                    const int c = 2 * (jh + j) + (h >> 1);
+                    *(u32x2_t*)(stage + (16 * i + i16) * 256 + ((c ^ i16) << 4) + ((h & 1) << 3)) = o;
+                } else if (m >= 0 && n < N) {
+                    uint16_t* y = Y + (int64_t)m * N + n;
+                    if (n + 4 <= N) {
+                        typedef u32x2_t u32x2_u2 __attribute__((aligned(2)));
+                        *(u32x2_u2*)y = o;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n + e < N) y[e] = to_bits<DT>(v[e]);
+                    }
                 }
-            });
-            uint16_t* yb = Y + n0 + col0 + 8 * (lane & 15);
-#pragma unroll 8
-            for (int k = 0; k < 4 * TM; ++k) {
-                const int r = 4 * k + (lane >> 4), m = row_s[row0 + r];
-                const u32x4_t d = *(const u32x4_t*)(stage + r * 256 + (((lane & 15) ^ (r % 16)) << 4));
-                if (m >= 0) *(u32x4_t*)(yb + (int64_t)m * N) = d;
             }
-            return;
-        }
-    }
-    static_for<0, TM>([&](auto ic) {
-        constexpr int i = decltype(ic)::value;
-        f32x4_t d[TN];
-        delta(i, d);
-        const int m = row_s[row0 + 16 * i + i16];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int n = n0 + col0 + 16 * j + 4 * (lane >> 4);
-            if (m < 0 || n >= N) continue;
-            uint16_t* y = Y + (int64_t)m * N + n;
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = acc[i][j][e] + d[j][e] + (bias && n + e < N ? from_bits<DT>(bias[n + e]) : 0.0f);
-            if (n + 4 <= N) {
-                typedef u32x2_t u32x2_u2 __attribute__((aligned(2)));
-                *(u32x2_u2*)y = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n + e < N) y[e] = to_bits<DT>(v[e]);
-            }
-        }
+        });
     });
+    if (!staged) return;
+    uint16_t* yb = Y + n0 + col0 + 8 * (lane & 15);
+#pragma unroll 8
+    for (int k = 0; k < 4 * TM; ++k) {
+        const int r = 4 * k + (lane >> 4), m = row_s[row0 + r];
+        const u32x4_t d = *(const u32x4_t*)(stage + r * 256 + (((lane & 15) ^ (r % 16)) << 4));
+        if (m >= 0) *(u32x4_t*)(yb + (int64_t)m * N) = d;
+    }
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -406,11 +452,12 @@ hipError_t rows_run(const LoraK& a, hipStream_t s) {
             if (big >= 256) {
                 const int tm = (int)((a.M + 255) / 256), tn = (int)((a.N + 255) / 256);
                 log_choice("lora_matmul: 256x256 tiles over sorted rows");
-                lora_tile_kernel<DT, TRANS != 0, 256><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
+                if (a.R <= 32) lora_tile_kernel<DT, TRANS != 0, 256, 8><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
+                else lora_tile_kernel<DT, TRANS != 0, 256, 4><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
             } else {
                 const int tm = (int)((a.M + 127) / 128), tn = (int)((a.N + 127) / 128);
                 log_choice("lora_matmul: 128x128 tiles over sorted rows");
-                lora_tile_kernel<DT, TRANS != 0, 128><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
+                lora_tile_kernel<DT, TRANS != 0, 128, 4><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
             }
             return hipGetLastError();
         }
