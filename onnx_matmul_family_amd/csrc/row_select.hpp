@@ -111,4 +111,18 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
+// Over 16 neighbouring lanes (row_ror: 8, 4, 2, 1), the result in each of them
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+    v = max(v, dpp_u32<0x128, 0xf>(v, v));
+    v = max(v, dpp_u32<0x124, 0xf>(v, v));
+    v = max(v, dpp_u32<0x122, 0xf>(v, v));
+    return max(v, dpp_u32<0x121, 0xf>(v, v));
+}
+__device__ __forceinline__ float row16_sum(float v) {
+    v = dpp_add<0x128, 0xf>(v);
+    v = dpp_add<0x124, 0xf>(v);
+    v = dpp_add<0x122, 0xf>(v);
+    return dpp_add<0x121, 0xf>(v);
+}
+
 }  // namespace omm
