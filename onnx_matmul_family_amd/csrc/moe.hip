@@ -25,96 +25,30 @@ constexpr int kMaxTop = 16;   // selections a token
 constexpr int kMaxTok = 64;   // tokens of a layer call: one lane each
 
 // ------------------------------------------------------------------ routing
-// One wave, one token.  Lane l holds the logits of experts l, l + 64, ...
-// k rounds of "largest key, lowest index".  Lane s < k returns selection s.
-template <int DT, int NE>
-__device__ __forceinline__ void load_logits(const typename elem_of<DT>::type* logits, int E, int lane,
-                                            float (&x)[NE]) {
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = i * 64 + lane;
-        x[i] = e < E ? elem_f32<DT>(logits[e]) : -__builtin_inff();
-    }
-}
-template <int NE>
-__device__ __forceinline__ void route_token(const float (&x)[NE], int E, int k, int renorm, int lane, int& id,
-                                            float& w) {
-    uint32_t key[NE];
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) key[i] = i * 64 + lane < E ? order_key(x[i]) : 0;
-    uint32_t first = 0;
-    id = 0;
-    for (int s = 0; s < k; ++s) {
-        uint32_t mx = 0;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) mx = max(mx, key[i]);
-        mx = wave_max_u32(mx);
-        if (s == 0) first = mx;
-        int e = 0;
-#pragma unroll
-        for (int i = NE - 1; i >= 0; --i) {
-            const uint64_t b = __ballot(key[i] == mx);
-            if (b) e = i * 64 + __ffsll((unsigned long long)b) - 1;
-        }
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (e == i * 64 + lane) key[i] = 0;
-        if (lane == s) {
-            id = e;
-            top = mx;
-        }
-    }
-    const float mxv = key_value(first);
-    const bool none = mxv == -__builtin_inff();  // every expert masked: all weights 0
-    float p = lane < k ? expf(key_value(top) - mxv) : 0.0f;
-    float sum;
-    if (renorm) {
-        sum = wave_sum(p);
-    } else {
-        float z = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (i * 64 + lane < E) z += expf(x[i] - mxv);
-        sum = wave_sum(z);
-    }
-    w = none ? 0.0f : p / sum;
-}
-
-struct RouteArgs {
-    const void* logits;
-    void* ids;
-    float* weights;
-    int64_t M;
-    int E, k, renorm, ids64;
-};
-
 // 16 lanes a token, four tokens a wave: lane l holds the logits of experts NE l ..
 // + NE - 1, so the lowest expert of a value is the lowest lane's.  A selection is
 // two reductions over 16 lanes (largest key, lowest index) for four tokens at
 // once, where a wave a token took one over 64 lanes each (16384 tokens over 64
 // experts, 8 selections: 9.4 us; the selections' arithmetic was the time).
 template <int DT, int NE>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
-    typedef typename elem_of<DT>::type E;
-    const int l = threadIdx.x & 15;
-    const int64_t m = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const bool here = m < a.M;
-    const E* row = (const E*)a.logits + (here ? m : a.M - 1) * a.E;
-    float x[NE];
-    uint32_t key[NE];
-    if (a.E == 16 * NE) {
+__device__ __forceinline__ void load_logits(const typename elem_of<DT>::type* row, int E, int l, float (&x)[NE]) {
+    if (E == 16 * NE) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) x[i] = elem_f32<DT>(row[l * NE + i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) x[i] = l * NE + i < a.E ? elem_f32<DT>(row[l * NE + i]) : -__builtin_inff();
+        for (int i = 0; i < NE; ++i) x[i] = l * NE + i < E ? elem_f32<DT>(row[l * NE + i]) : -__builtin_inff();
     }
+}
+// Lane l < k returns selection l (all 64 lanes must call)
+template <int NE>
+__device__ __forceinline__ void route_token(const float (&x)[NE], int E, int k, int renorm, int l, int& id, float& w) {
+    uint32_t key[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) key[i] = l * NE + i < a.E ? order_key(x[i]) : 0;
+    for (int i = 0; i < NE; ++i) key[i] = l * NE + i < E ? order_key(x[i]) : 0;
     uint32_t first = 0, top = 0;
-    int id = 0;
-    for (int s = 0; s < a.k; ++s) {
+    id = 0;
+    for (int s = 0; s < k; ++s) {
         uint32_t mx = 0;
 #pragma unroll
         for (int i = 0; i < NE; ++i) mx = max(mx, key[i]);
@@ -135,19 +69,39 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     }
     const float mxv = key_value(first);
     const bool none = mxv == -__builtin_inff();  // every expert masked: all weights 0
-    const float p = l < a.k ? expf(key_value(top) - mxv) : 0.0f;
+    const float p = l < k ? expf(key_value(top) - mxv) : 0.0f;
     float z = p;
-    if (!a.renorm) {
+    if (!renorm) {
         z = 0.0f;
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            if (l * NE + i < a.E) z += expf(x[i] - mxv);
+            if (l * NE + i < E) z += expf(x[i] - mxv);
     }
     z = row16_sum(z);
+    w = none ? 0.0f : p / z;
+}
+
+struct RouteArgs {
+    const void* logits;
+    void* ids;
+    float* weights;
+    int64_t M;
+    int E, k, renorm, ids64;
+};
+
+template <int DT, int NE>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+    const int l = threadIdx.x & 15;
+    const int64_t m = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const bool here = m < a.M;
+    float x[NE], w;
+    int id;
+    load_logits<DT, NE>((const typename elem_of<DT>::type*)a.logits + (here ? m : a.M - 1) * a.E, a.E, l, x);
+    route_token<NE>(x, a.E, a.k, a.renorm, l, id, w);
     if (!here || l >= a.k) return;
     if (a.ids64) ((int64_t*)a.ids)[m * a.k + l] = id;
     else ((int32_t*)a.ids)[m * a.k + l] = id;
-    a.weights[m * a.k + l] = none ? 0.0f : p / z;
+    a.weights[m * a.k + l] = w;
 }
 
 template <int DT>
@@ -199,32 +153,29 @@ struct ExpertRows {
     int e, n, active;
 };
 
-// Routes the call's tokens, NW waves taking one each in turn; a wave's next
-// logits are on their way while it ranks the present ones.
+// Routes the call's tokens, NW waves taking four each in turn
 template <int DT, int NE, int NW>
 __device__ __forceinline__ void route_tokens(const LayerArgs& a, ExpertRows& r, int lane, int wave) {
     const typename elem_of<DT>::type* logits = (const typename elem_of<DT>::type*)a.logits;
-    float x[NE], nx[NE] = {};
-    if (wave < a.M) load_logits<DT, NE>(logits + wave * a.E, a.E, lane, x);
-    for (int m = wave; m < a.M; m += NW) {
-        if (m + NW < a.M) load_logits<DT, NE>(logits + (m + NW) * a.E, a.E, lane, nx);
+    const int l = lane & 15;
+    for (int m0 = wave * 4; m0 < a.M; m0 += NW * 4) {
+        const int m = m0 + (lane >> 4);
+        float x[NE], w;
         int id;
-        float w;
-        route_token<NE>(x, a.E, a.k, a.renorm, lane, id, w);
-        if (lane < a.k) {
-            r.id[m * a.k + lane] = id;
-            r.w[m * a.k + lane] = w;
+        load_logits<DT, NE>(logits + min(m, a.M - 1) * a.E, a.E, l, x);
+        route_token<NE>(x, a.E, a.k, a.renorm, l, id, w);
+        if (m < a.M && l < a.k) {
+            r.id[m * a.k + l] = id;
+            r.w[m * a.k + l] = w;
         }
-#pragma unroll
-        for (int i = 0; i < NE; ++i) x[i] = nx[i];
     }
 }
 template <int DT, int NW>
 __device__ __forceinline__ void route_tokens(const LayerArgs& a, ExpertRows& r, int lane, int wave) {
-    if (a.E <= 64) route_tokens<DT, 1, NW>(a, r, lane, wave);
-    else if (a.E <= 128) route_tokens<DT, 2, NW>(a, r, lane, wave);
-    else if (a.E <= 256) route_tokens<DT, 4, NW>(a, r, lane, wave);
-    else route_tokens<DT, 8, NW>(a, r, lane, wave);
+    if (a.E <= 16) route_tokens<DT, 1, NW>(a, r, lane, wave);
+    else if (a.E <= 64) route_tokens<DT, 4, NW>(a, r, lane, wave);
+    else if (a.E <= 128) route_tokens<DT, 8, NW>(a, r, lane, wave);
+    else route_tokens<DT, 32, NW>(a, r, lane, wave);
 }
 // (the logits may be of another type than the weights)
 template <int NW>
