@@ -314,7 +314,8 @@ int omm_moe_route(const omm_tensor* logits, int top_k, int renormalize, omm_tens
  *   linear layers store them).  1 <= top_k <= E.
  *   act: OMM_ACT_SILU x / (1 + e^-x), OMM_ACT_GELU x (1 + erf(x / sqrt 2)) / 2.
  *   The product of the two branches is held in fp32; one rounding to T at the end.
- *   Only the experts in use are read, each once per 64 tokens.
+ *   Only the experts in use are read, each once for its tokens (an expert of more
+ *   than 16 or 32 of them again, from the caches).
  * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE, OMM_ERR_UNSUPPORTED,
  * OMM_ERR_WORKSPACE.
  */

@@ -34,7 +34,8 @@ __device__ __forceinline__ int row_of(const LoraK& a, int p) { return a.perm ? a
 // Stable counting sort of the rows by adapter (bin 0: none) in one workgroup:
 // each wave counts its contiguous share of the rows per bin, a scan over (bin,
 // wave) gives every wave its place in every bin, and it writes its rows there.
-// SORTTIME
+// 4096 rows: 8 us in runs of 9 bins, 11 us mixed over 17; the tiles
+// that use the order take 225.
 __global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int bins) {
     extern __shared__ int hist[];  // [wave][bin]
     __shared__ int wsum[kSortWaves];

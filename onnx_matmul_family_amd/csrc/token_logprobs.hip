@@ -561,7 +561,10 @@ hipError_t launch_token_logprobs_grad(const TokenLogprobsGradArgs& t, int dt, hi
     a.M = t.M;
     a.V = (int)t.V;
     a.idx64 = t.idx64;
+    // workgroups of 16384 elements, of fewer where that leaves the chip unfilled
+    // (64 rows of 32000 fp32: 7.1 us in 128 workgroups, 4.3 in 1024)
     a.chunk = 16384;
+    while (a.chunk > 2048 && t.M * ((t.V + a.chunk - 1) / a.chunk) < 1024) a.chunk /= 2;
     a.chunks = (int)((t.V + a.chunk - 1) / a.chunk);
     const dim3 grid((unsigned)(t.M * a.chunks));
     if (dt == 0) logprobs_grad_kernel<0, 256><<<grid, 256, 0, s>>>(a);
