@@ -131,12 +131,13 @@ struct LayerArgs {
     void* Y;               // (M, K)
     int32_t* ids;          // workspace: (M, k) selections (element-wise form)
     ExpertList* lists;     // workspace: (min(E, M k)) (streamed form)
-    float* hmax;           // workspace: (M k, ceil(F / 64)) largest |h| (fp16)
+    float* hmax;           // workspace: (M k, ceil(F / hw)) largest |h| (fp16)
     float* h;              // workspace: (M k, F), weighted
     float* part;           // workspace: (ceil(K / 128), splits, M k, 128)
     uint32_t* done;        // workspace: finished workgroups of each 128 output columns
     int64_t K, F;
     int M, E, k, renorm, act, trans, logits_kind, splits;
+    int hw;                // columns of a workgroup of the first kernel (16 or 64)
 };
 
 __device__ __forceinline__ float activate(float g, int act) {
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(256) void moe_down_any_kernel(LayerArgs a) {
 template <int DT>
 void layer_any(const LayerArgs& a, hipStream_t s) {
     const int pairs = a.M * a.k, jmax = pairs < a.E ? pairs : a.E;
-    const dim3 gu((unsigned)((a.F + 63) / 64), (unsigned)jmax);
+    const dim3 gu((unsigned)((a.F + a.hw - 1) / a.hw), (unsigned)jmax);
     moe_up_any_kernel<DT><<<gu, 256, 0, s>>>(a);
     const dim3 gd((unsigned)((a.K + 63) / 64), (unsigned)a.M);
     moe_down_any_kernel<DT><<<gd, 256, 0, s>>>(a);
@@ -383,7 +384,64 @@ __device__ __forceinline__ void up_rows(const LayerArgs& a, const ExpertRows& r,
     }
 }
 
-template <int DT, int TRANS, int NG, int NWS>
+// The same for 16 columns: one gate and one up fragment, U steps on their way at
+// once.  For few experts in use with a small F, where 64 columns would make few
+// workgroups, each with a long contraction.
+template <int DT, int TRANS, int NG>
+__device__ __forceinline__ void up_cols(const LayerArgs& a, const ExpertRows& r, int t0, float* red, int tid) {
+    typedef typename elem_of<DT>::type E;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int F = (int)a.F, K = (int)a.K, c0 = blockIdx.x * 16;
+    const int64_t eoff = (int64_t)__builtin_amdgcn_readfirstlane(r.e) * a.K * a.F;
+    const E* wg = (const E*)a.wg + eoff;
+    const E* wu = (const E*)a.wu + eoff;
+    ColsWeights<DT, TRANS, 2> w;
+    if constexpr (TRANS) {
+        w.base[0] = wg;
+        w.base[1] = wu;
+        w.off[0] = w.off[1] = (uint32_t)min(c0 + tile_row(lane), F - 1) * K + tile_off<DT>(lane);
+    } else {
+        constexpr int LPR = ColsW<DT, 2>::LPR;  // the first half of a row's lanes loads gate
+        const int piece = lane % LPR;
+        w.ld = F;
+        w.p = (piece < LPR / 2 ? wg : wu) + (int64_t)(lane / LPR) * F + group_start<DT>(c0, piece % (LPR / 2) * kQ<DT>, F);
+    }
+    StreamX<DT, 1, NG> x;  // rows past the last are the last one: their results are not used
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        x.p[g] = (const E*)a.X + (int64_t)r.tok[min(t0 + 16 * g + tile_row(lane), r.n - 1)] * K + tile_off<DT>(lane);
+    f32x4_t acc[2][NG] = {};
+    int s0, s1;
+    wave_steps<DT, 8>(K, 1, wave, s0, s1);
+    cols_run<DT, TRANS, NG, 2, NG == 1 ? 4 : 2>(w, x, s0, s1, K, acc, (u32x4_t*)&red[red_index(wave, 0, 0, 0)], lane,
+                                                [] {});
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) *(f32x4_t*)&red[red_index(wave, 2 * j + g, lane, 0)] = acc[j][g];
+    __syncthreads();
+    for (int o = tid; o < 16 * NG * 16; o += 512) {
+        const int c = o & 15, row = o >> 4, t = t0 + row;  // 16 lanes a row
+        const int pos = cols_pos<DT, TRANS>(c0, c, F);
+        float gv = 0.0f, uv = 0.0f;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            const float* q = &red[red_index(v, row >> 4, (pos >> 2) * 16 + (row & 15), pos & 3)];
+            gv += q[0];
+            uv += q[2 * kFragPad];
+        }
+        const bool in = t < r.n && c0 + c < F;
+        const int p = t < r.n ? r.tok[t] * a.k + r.slot[t] : 0;
+        const float h = in ? activate(gv, a.act) * uv * r.w[p] : 0.0f;
+        if (in) a.h[(int64_t)p * F + c0 + c] = h;
+        if constexpr (DT == 1) {
+            const uint32_t mx = row16_max(__float_as_uint(fabsf(h)));
+            if (c == 0 && t < r.n) a.hmax[(int64_t)p * gridDim.x + blockIdx.x] = __uint_as_float(mx);
+        }
+    }
+}
+
+template <int DT, int TRANS, int NG, int NWS, int CW>
 __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_up_kernel(LayerArgs a) {
     __shared__ ExpertRows r;
     __shared__ __attribute__((aligned(16))) float red[NWS * 8 * kFragPad];
@@ -405,7 +463,10 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_up_kernel(Laye
     if (r.e < 0) return;
     for (int t0 = 0; t0 < r.n; t0 += 16 * NG) {
         if (t0) __syncthreads();
-        up_rows<DT, TRANS, NG, NWS>(a, r, t0, red, tid);
+        if constexpr (CW == 16)
+            up_cols<DT, TRANS, NG>(a, r, t0, red, tid);
+        else
+            up_rows<DT, TRANS, NG, NWS>(a, r, t0, red, tid);
     }
 }
 
@@ -441,10 +502,10 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
         x.p[g] = a.h + (int64_t)r.pair[min(t0 + 16 * g + tr, r.n - 1)] * F + x.off(lane);
         undo[g] = 1.0f;
         if constexpr (DT == 1) {  // the row's largest value over this wave's range -> [2^13, 2^14)
-            const int slabs = (F + 63) / 64;
+            const int slabs = (F + a.hw - 1) / a.hw;
             const int p = r.pair[min(t0 + 16 * g + i, r.n - 1)];
             float mx = 0.0f;
-            for (int b = s0 >> 1; b < (s1 + 1) >> 1; ++b) mx = fmaxf(mx, a.hmax[(int64_t)p * slabs + b]);
+            for (int b = s0 * 32 / a.hw; b < min(slabs, (s1 * 32 + a.hw - 1) / a.hw); ++b) mx = fmaxf(mx, a.hmax[(int64_t)p * slabs + b]);
             int ex = 0;
             if (mx > 0.0f && mx < __builtin_inff()) ex = max(-100, min(100, 13 - ilogbf(mx)));
             x.scale[g] = ldexpf(1.0f, ex);
@@ -510,9 +571,14 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_down_kernel(La
 // tokens reads them again (from the caches).
 template <int DT, int TRANS, int NG, int NWS>
 void layer_streamed(const LayerArgs& a, int jmax, hipStream_t s) {
-    const dim3 gu((unsigned)((a.F + 63) / 64), (unsigned)jmax);
+    const dim3 gu((unsigned)((a.F + a.hw - 1) / a.hw), (unsigned)jmax);
     const dim3 gd((unsigned)((a.K + 127) / 128), (unsigned)jmax, (unsigned)a.splits);
-    moe_up_kernel<DT, TRANS, NG, NWS><<<gu, 64 * NWS, 0, s>>>(a);
+    if constexpr (NWS == 8) {
+        if (a.hw == 16) moe_up_kernel<DT, TRANS, NG, 8, 16><<<gu, 512, 0, s>>>(a);
+        else moe_up_kernel<DT, TRANS, NG, 8, 64><<<gu, 512, 0, s>>>(a);
+    } else {
+        moe_up_kernel<DT, TRANS, NG, NWS, 64><<<gu, 64 * NWS, 0, s>>>(a);
+    }
     moe_down_kernel<DT, TRANS, NG, NWS><<<gd, 64 * NWS, 0, s>>>(a);
 }
 
@@ -568,7 +634,7 @@ size_t moe_layer_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int
     const size_t jmax = (size_t)(M * k < E ? M * k : E);
     return align256((size_t)M * k * 4) + align256((size_t)M * k * F * 4) +
            align256((size_t)M * k * ((K + 127) / 128) * 512 * down_splits(M, K, F, E, k)) + align256((size_t)(K + 127) / 128 * 4) + align256(jmax * sizeof(ExpertList)) +
-           align256((size_t)M * k * ((F + 63) / 64) * 4);
+           align256((size_t)M * k * ((F + 15) / 16) * 4);
 }
 
 hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void* ws, hipStream_t s) {
@@ -595,6 +661,13 @@ hipError_t launch_moe_layer(const MoeLayerArgs& l, int dt, int logits_kind, void
     w += align256((size_t)l.M * l.k * l.F * 4);
     a.part = (float*)w;
     a.splits = down_splits(l.M, l.K, l.F, l.E, l.k);
+    // 64 columns of the first kernel, or 16 where that makes few workgroups (trans
+    // 0, whose pieces of 16 columns are 32 bytes: fewer still).  us a call, 64 / 16
+    // columns: trans 1, 2 experts of 2778 x 192 (6 workgroups of 64) fp32 40 / 23,
+    // 13 of 3840 x 192 (39) 39 / 28, 3 of 512 x 1920 (90) 14 / 18; trans 0, 8 of
+    // 2176 x 205 (32) 29 / 26, 16 of 896 x 192 (48) 16 / 20.
+    const int64_t wide = (l.F + 63) / 64 * (l.M * l.k < l.E ? l.M * l.k : l.E);
+    a.hw = wide < (l.trans ? 64 : 40) ? 16 : 64;
     w += align256((size_t)l.M * l.k * ((l.K + 127) / 128) * 512 * a.splits);
     a.done = (uint32_t*)w;
     w += align256((size_t)(l.K + 127) / 128 * 4);

@@ -107,7 +107,7 @@ __device__ __forceinline__ void row_tile(u32x4_t (&v)[N], u32x4_t* scratch, int 
     __builtin_amdgcn_wave_barrier();
 }
 
-// One lane's weights.  TRANS = 1: off[j], elements from base[j / 4] to the
+// One lane's weights.  TRANS = 1: off[j], elements from base[2 j / NF] to the
 // tile row's column of fragment j, plus the contraction offset tile_off;
 // TRANS = 0: p, the lane's columns (fp32: p[1] of the upper 64), plus rows
 // kQ (l / 16), and ld, the row stride.  Bases, ld and kb are uniform over the
@@ -119,12 +119,12 @@ struct StreamW {
     uint32_t off[NF];
     __device__ __forceinline__ void load(u32x4_t (&w)[NF], int kb) const {
 #pragma unroll
-        for (int j = 0; j < NF; ++j) w[j] = load16(base[j >> 2] + kb + off[j]);
+        for (int j = 0; j < NF; ++j) w[j] = load16(base[2 * j / NF] + kb + off[j]);
     }
     __device__ __forceinline__ void tail(u32x4_t (&w)[NF], int kb, int kn, int lane) const {
         const int n = max(0, min(kQ<DT>, kn - kb - tile_off<DT>(lane)));
 #pragma unroll
-        for (int j = 0; j < NF; ++j) w[j] = load16_first(base[j >> 2] + kb + off[j], n);
+        for (int j = 0; j < NF; ++j) w[j] = load16_first(base[2 * j / NF] + kb + off[j], n);
     }
 };
 template <int DT>

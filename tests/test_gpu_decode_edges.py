@@ -234,3 +234,15 @@ def test_binding_refusals_on_gpu_tensors():
         om.lora_matmul(x, W.to(torch.bfloat16), A, B, idx)
     om.lora_matmul(x, W, A, B, idx)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("trans", [0, 1])
+def test_lora_more_rows_than_streamed(dt, trans):
+    """65536 rows and more that the tiles do not take: the adapters' term first, then the dense product."""
+    for M, K, N, R, G in ((66001, 33, 41, 9, 5), (65600, 33, 41, 16, 1100)):
+        c = lora_case(M, K, N, R, G, dt, trans, M)
+        got, _ = run_lora(c, trans)
+        sel = torch.cat([torch.arange(0, M, 997), torch.tensor([M - 2, M - 1])])
+        want, tol = lora(c[0][sel], c[1], c[2], c[3], c[4][sel], c[5], c[6], trans, dt)
+        assert_within(got[sel.cuda()], want, tol)
