@@ -221,6 +221,9 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
 // BKM: W (N, K), B (G, N, R); else W (K, N), B (G, R, N).
 // TH: column fragments of a pass of the epilogue; fewer (4 of 8) leave the
 // registers to keep B's fragments of 64 r from block to block instead of 32.
+// 4096 x 4096 x 8192 with rank 32 (bf16): 225 us, 1.23 PFLOP/s; the K loop alone,
+// as the dense product runs it, takes 222 and up (it is bound by the matrix unit
+// under the chip's clock).
 template <int DT, bool BKM, int BT, int TH>
 __global__ __launch_bounds__(NT, BT == 128 ? 2 : 1) void lora_tile_kernel(LoraK a, int tiles_m, int tiles_n) {
     constexpr int BM = BT, BN = BT, TM = BM / 32, TN = BN / 32;

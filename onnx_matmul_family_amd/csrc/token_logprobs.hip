@@ -14,8 +14,9 @@
 // elements only if the third does (with 20 of 50001 tokens: about one lane a
 // row); what reaches T is listed and ranked by (value, lower index).  Without
 // the positions every lane that reached T read all of its elements again, as
-// many cache lines as the row has: 2048 rows of 50001, 20 alternatives, 73 us,
-// of which the first pass is 38.
+// many cache lines as the row has: 2048 rows of 50001, 20 alternatives, 73 us;
+// now 52, of which the first pass is 38 without positions (5.4 TB/s, the vector
+// ALU about as busy) and 43 with them.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -429,6 +430,7 @@ struct LpGradArgs {
 };
 
 // dx[v] = gl ([v = target] - p) - gH p (ln p + H),  p = e^(x - lse)
+// One read and one write: 4096 rows of 131072 (bf16) in 380 us, 5.6 TB/s.
 struct GradRow {
     float gl, gh, H, lse;
     int t;
