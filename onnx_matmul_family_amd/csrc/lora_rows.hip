@@ -8,8 +8,8 @@
 //   lora_shrink_rows_kernel  T = scale X A in fp32, 16 rows a workgroup
 //   lora_tile_kernel         Y tiles on the LDS-DMA matrix core; as a tile
 //                            leaves, T B is added to its accumulators.  T's
-//                            rows enter as two 16-bit halves, so T is not
-//                            rounded to T's type and neither is T B.
+//                            rows enter as three 16-bit parts, so neither T
+//                            nor T B is rounded.
 // Operands that the DMA cannot take (rows not 16-byte aligned) and fp32:
 //   lora_expand_kernel       bias + T B into Y, to which the framework's dense
 //                            product is then added.
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int
 // T[p, r] = scale[g] sum_k X[m, k] A[g, k, r] of the 16 rows m at positions p0
 // .. p0 + 15 and 16 NF r: NW waves split K, A and the rows go from memory
 // to the matrix unit.  One pass for each adapter among the rows.
-// fp16: tmax[p][y] = max |T[p, r]| over the r of blockIdx.y (for the halves' scale).
+// fp16: tmax[p][y] = max |T[p, r]| over the r of blockIdx.y (for the parts' scale).
 template <int DT, int TRANS, int NF, int NW>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_rows_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
@@ -339,12 +339,13 @@ __global__ __launch_bounds__(NT, BT == 128 ? 2 : 1) void lora_tile_kernel(LoraK 
             const auto step = [&](const u32x4_t (&f)[TH], int r0) {
                 u32x4_t raw[2] = {first[0], first[1]};
                 if (r0) load_t(raw, t_row(i), r0);
-                u32x4_t hi, lo;
-                split_halves<DT>(raw, scale, hi, lo);
+                float left[8];
+                split_start<DT>(raw, scale, left);
 #pragma unroll
-                for (int j = 0; j < TH; ++j) {
-                    v[j] = mfma16x16x32<DT>(f[j], hi, v[j]);
-                    v[j] = mfma16x16x32<DT>(f[j], lo, v[j]);
+                for (int h = 0; h < kParts32; ++h) {
+                    const u32x4_t part = split_next<DT>(left);
+#pragma unroll
+                    for (int j = 0; j < TH; ++j) v[j] = mfma16x16x32<DT>(f[j], part, v[j]);
                 }
             };
             if (R <= 32 * HS) {

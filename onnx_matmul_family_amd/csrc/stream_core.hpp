@@ -197,39 +197,57 @@ struct StreamX {
     }
 };
 
-// Eight fp32 values as two halves of T whose sum holds them to 16 bits of the
-// significand (bf16) or 22 (fp16, whose caller has scaled them into its range).
-// The first bf16 half is cut off, not rounded: a value near the largest float
-// stays finite.  An infinity is its own first half.
+// Eight fp32 values as three parts of T each, which add up to them: 3 x 8 bits of
+// the significand (bf16) or 3 x 11 (fp16, whose caller has scaled the row's
+// largest value into its range; what is lost is 2^-37 of that one).  Two parts
+// are not enough: 16 bits of a bf16 row made 600 of 131072 outputs of an expert
+// layer (32 tokens, 4096 x 2048) miss the nearest bf16.  bf16 parts are
+// cut off, not rounded: a value near the largest float stays finite.  An infinity
+// is its own first part.
+constexpr int kParts32 = 3;
+// the next part of the values, which keep what is left of them
 template <int DT>
-__device__ __forceinline__ void split_halves(const u32x4_t (&r)[2], float scale, u32x4_t& hi, u32x4_t& lo) {
+__device__ __forceinline__ u32x4_t split_next(float (&v)[8]) {
+    u32x4_t p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t ua = r[i >> 1][(i & 1) * 2], ub = r[i >> 1][(i & 1) * 2 + 1];
-        float a = __uint_as_float(ua), b = __uint_as_float(ub), ah, bh;
+        float &a = v[2 * i], &b = v[2 * i + 1], ah, bh;
         if constexpr (DT == 1) {
-            a *= scale;
-            b *= scale;
-            hi[i] = pack2<DT>(a, b);
-            ah = from_bits<DT>((uint16_t)hi[i]);
-            bh = from_bits<DT>((uint16_t)(hi[i] >> 16));
+            p[i] = pack2<DT>(a, b);
+            ah = from_bits<DT>((uint16_t)p[i]);
+            bh = from_bits<DT>((uint16_t)(p[i] >> 16));
         } else {
-            hi[i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+            const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+            p[i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
             ah = __uint_as_float(ua & 0xffff0000u);
             bh = __uint_as_float(ub & 0xffff0000u);
         }
-        lo[i] = pack2<DT>(a == ah ? 0.0f : a - ah, b == bh ? 0.0f : b - bh);
+        a = a == ah ? 0.0f : a - ah;
+        b = b == bh ? 0.0f : b - bh;
     }
+    return p;
+}
+template <int DT>
+__device__ __forceinline__ void split_start(const u32x4_t (&r)[2], float scale, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i >> 2][i & 3]) * (DT == 1 ? scale : 1.0f);
+}
+template <int DT>
+__device__ __forceinline__ void split_parts(const u32x4_t (&r)[2], float scale, u32x4_t (&p)[kParts32]) {
+    float v[8];
+    split_start<DT>(r, scale, v);
+#pragma unroll
+    for (int h = 0; h < kParts32; ++h) p[h] = split_next<DT>(v);
 }
 
-// fp32 rows against bf16 / fp16 weights, as the sum of two 16-bit halves: two
+// fp32 rows against bf16 / fp16 weights, as the sum of three 16-bit parts: three
 // products instead of one, which the streamed weights leave room for, and the
-// rows are not rounded to T.  fp16 rows are scaled by a power of two per row
+// rows are not rounded.  fp16 rows are scaled by a power of two per row
 // (scale[g], of row l % 16; the caller divides it out).  Two loads a step:
 // TRANS = 1 two tiles of 16 values of the contraction each, else 8 values.
 template <int DT, int TRANS, int NG>
 struct StreamX32 {
-    static constexpr int RAW = 2, PARTS = 2, NEXT = TRANS ? 16 : 4;
+    static constexpr int RAW = 2, PARTS = kParts32, NEXT = TRANS ? 16 : 4;
     const float* p[NG];  // row x_row, plus off
     float scale[NG];
     __device__ __forceinline__ static int off(int lane) { return TRANS ? 4 * tile_piece(lane) : (lane >> 4) * 8; }
@@ -248,7 +266,7 @@ struct StreamX32 {
             r[g][1] = load16_first(p[g] + kb + NEXT, n - NEXT);
         }
     }
-    __device__ __forceinline__ void operands(const u32x4_t (&r)[NG][2], u32x4_t (&o)[NG][2], u32x4_t* scratch,
+    __device__ __forceinline__ void operands(const u32x4_t (&r)[NG][2], u32x4_t (&o)[NG][PARTS], u32x4_t* scratch,
                                              int lane) const {
         if constexpr (TRANS) {
 #pragma unroll
@@ -265,9 +283,9 @@ struct StreamX32 {
         for (int g = 0; g < NG; ++g) {
             if constexpr (TRANS) {
                 const u32x4_t v[2] = {scratch[2 * g * 64 + s0], scratch[2 * g * 64 + s1]};
-                split_halves<DT>(v, scale[g], o[g][0], o[g][1]);
+                split_parts<DT>(v, scale[g], o[g]);
             } else {
-                split_halves<DT>(r[g], scale[g], o[g][0], o[g][1]);
+                split_parts<DT>(r[g], scale[g], o[g]);
             }
         }
         if constexpr (TRANS) __builtin_amdgcn_wave_barrier();
