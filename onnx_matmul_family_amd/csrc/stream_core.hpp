@@ -205,6 +205,12 @@ struct StreamX {
 // cut off, not rounded: a value near the largest float stays finite.  An infinity
 // is its own first part.
 constexpr int kParts32 = 3;
+template <int DT> constexpr float kLeastPart = DT == 1 ? 0x1p-24f : 0x1p-133f;
+// |v| or, if that is less or NaN (inf - inf), the least part, unless z is 0; z's sign
+template <int DT>
+__device__ __forceinline__ float at_least(float v, float z) {
+    return copysignf(fmaxf(fabsf(v), fminf(fabsf(z), kLeastPart<DT>)), z);
+}
 // the next part of the values, which keep what is left of them
 template <int DT>
 __device__ __forceinline__ u32x4_t split_next(float (&v)[8]) {
@@ -213,7 +219,7 @@ __device__ __forceinline__ u32x4_t split_next(float (&v)[8]) {
     for (int i = 0; i < 4; ++i) {
         float &a = v[2 * i], &b = v[2 * i + 1], ah, bh;
         if constexpr (DT == 1) {
-            p[i] = pack2<DT>(a, b);
+            p[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
             ah = from_bits<DT>((uint16_t)p[i]);
             bh = from_bits<DT>((uint16_t)(p[i] >> 16));
         } else {
@@ -222,15 +228,21 @@ __device__ __forceinline__ u32x4_t split_next(float (&v)[8]) {
             ah = __uint_as_float(ua & 0xffff0000u);
             bh = __uint_as_float(ub & 0xffff0000u);
         }
-        a = a == ah ? 0.0f : a - ah;
-        b = b == bh ? 0.0f : b - bh;
+        a = at_least<DT>(a - ah, ah);
+        b = at_least<DT>(b - bh, bh);
     }
     return p;
 }
 template <int DT>
 __device__ __forceinline__ void split_start(const u32x4_t (&r)[2], float scale, float (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i >> 2][i & 3]) * (DT == 1 ? scale : 1.0f);
+    for (int i = 0; i < 8; ++i) {
+        v[i] = __uint_as_float(r[i >> 2][i & 3]);
+        if constexpr (DT == 1) {
+            v[i] *= scale;
+            if (fabsf(v[i]) < kLeastPart<DT> && v[i] != 0.0f) v[i] = copysignf(kLeastPart<DT>, v[i]);
+        }
+    }
 }
 template <int DT>
 __device__ __forceinline__ void split_parts(const u32x4_t (&r)[2], float scale, u32x4_t (&p)[kParts32]) {
