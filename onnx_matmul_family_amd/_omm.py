@@ -253,8 +253,19 @@ def native():
     return _native
 
 
-def _handle(stream):
-    return stream.cuda_stream if stream is not None else None
+def _on(stream, f, *args):
+    """f(*args) on another stream than the caller's.
+
+    There every tensor that the call allocates comes from that stream's memory: a
+    workspace that is dropped here, or by the caller, is only used again by what
+    follows on it, and what the block held before is done with.  The tensors handed
+    out are recorded on the caller's stream, where they may be read and freed."""
+    outer = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = f(*args)
+    for t in out if isinstance(out, tuple) else (out,):
+        t.record_stream(outer)
+    return out
 
 
 def lora_matmul_workspace_size(M, K, N, R, dtype):
@@ -267,15 +278,18 @@ def lora_matmul(X, W, A, B, adapter_indices, adapter_scale=None, bias=None, tran
 
     trans=0: W (K, N), A (G, K, R), B (G, R, N); trans=1: W (N, K), A (G, R, K), B (G, N, R).
     A row whose index is outside [0, G) has no adapter.  Returns (Y, workspace)."""
-    return (_native or native()).lora_matmul(X, W, A, B, adapter_indices, adapter_scale, bias, int(trans), Y, workspace,
-                                             _handle(stream))
+    if stream is not None:
+        return _on(stream, lora_matmul, X, W, A, B, adapter_indices, adapter_scale, bias, trans, Y, workspace)
+    return (_native or native()).lora_matmul(X, W, A, B, adapter_indices, adapter_scale, bias, int(trans), Y, workspace)
 
 
 def moe_route(logits, top_k, renormalize=True, indices=None, weights=None, stream=None):
     """The top_k experts of softmax(logits) per token, by descending logit (ties: lower index), and
     their weights (renormalised over the selected ones if renormalize).  Returns (indices, weights):
     indices int32 as grouped_matmul's group_indices, weights fp32."""
-    return (_native or native()).moe_route(logits, top_k, int(renormalize), indices, weights, _handle(stream))
+    if stream is not None:
+        return _on(stream, moe_route, logits, top_k, renormalize, indices, weights)
+    return (_native or native()).moe_route(logits, top_k, int(renormalize), indices, weights)
 
 
 def moe_layer_workspace_size(M, K, F, E, top_k):
@@ -289,10 +303,13 @@ def moe_layer(X, router_logits, top_k, W_gate, W_up, W_down, renormalize=True, a
 
     trans=0: W_gate, W_up (E, K, F), W_down (E, F, K) as grouped_matmul's weights; trans=1: (E, F, K)
     and (E, K, F).  activation: "silu" or "gelu" (erf).  Returns (Y, workspace)."""
+    if stream is not None:
+        return _on(stream, moe_layer, X, router_logits, top_k, W_gate, W_up, W_down, renormalize, activation, trans, Y,
+                   workspace)
     if activation not in ACTIVATIONS:
         raise ValueError("activation must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
     return (_native or native()).moe_layer(X, router_logits, top_k, W_gate, W_up, W_down, int(renormalize),
-                                           ACTIVATIONS[activation], int(trans), Y, workspace, _handle(stream))
+                                           ACTIVATIONS[activation], int(trans), Y, workspace)
 
 
 def token_logprobs_workspace_size(M, V, top_k):
@@ -304,12 +321,16 @@ def token_logprobs(logits, targets, top_k=0, workspace=None, stream=None):
 
     Returns (logprobs, entropy, lse, top_ids, top_logprobs): fp32 (M), (M), (M), int32 (M, top_k) and
     fp32 (M, top_k).  A target outside [0, V) gives log probability 0."""
-    return (_native or native()).token_logprobs(logits, targets, top_k, workspace, _handle(stream))
+    if stream is not None:
+        return _on(stream, token_logprobs, logits, targets, top_k, workspace)
+    return (_native or native()).token_logprobs(logits, targets, top_k, workspace)
 
 
 def token_logprobs_grad(logits, targets, lse, grad_logprobs, entropy=None, grad_entropy=None, grad_logits=None,
                         stream=None):
     """Gradient of token_logprobs' logprobs (and entropy, if grad_entropy is given) with respect to the
     logits; grad_logits may be the logits tensor itself."""
+    if stream is not None:
+        return _on(stream, token_logprobs_grad, logits, targets, lse, grad_logprobs, entropy, grad_entropy, grad_logits)
     return (_native or native()).token_logprobs_grad(logits, targets, lse, entropy, grad_logprobs, grad_entropy,
-                                                     grad_logits, _handle(stream))
+                                                     grad_logits)

@@ -111,11 +111,10 @@ int64_t integer(PyObject* o) {
     return v;
 }
 
-// a stream handle, or (None) the current stream of x's device
-void* stream(PyObject* o, const at::Tensor& x) {
-    if (o == Py_None) return (void*)c10::hip::getCurrentHIPStream(x.device().index()).stream();
-    return (void*)(uintptr_t)integer(o);
-}
+// The current stream of x's device, to which what is allocated here belongs too.
+// (A call for another stream makes that one current: memory of this stream's could
+// be handed out again while the other one still uses it.)
+void* stream(const at::Tensor& x) { return (void*)c10::hip::getCurrentHIPStream(x.device().index()).stream(); }
 
 template <typename F>
 void call(const char* what, F f) {
@@ -161,9 +160,9 @@ PyObject* pack(std::initializer_list<at::Tensor> xs) {
     return t;
 }
 
-// X, W, A, B, adapter_indices, adapter_scale, bias, trans, Y, workspace, stream
+// X, W, A, B, adapter_indices, adapter_scale, bias, trans, Y, workspace
 PyObject* lora_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 11, [&] {
+    return guarded(n, 10, [&] {
         const at::Tensor &X = tensor(a[0]), &W = tensor(a[1]), &A = tensor(a[2]);
         const int trans = (int)integer(a[7]);
         if (X.dim() != 2 || W.dim() != 2 || A.dim() != 3) fail(PyExc_ValueError, "X and W must be 2-d, A 3-d");
@@ -171,7 +170,7 @@ PyObject* lora_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t M = X.size(0), K = X.size(1), N = W.size(trans ? 0 : 1), R = A.size(trans ? 1 : 2);
         Out y(a[8], {M, N}, X, X.scalar_type());
         const Workspace ws = workspace(a[9], X, [&] { return L.lora_matmul_ws(M, K, N, R, x.t.dtype); });
-        void* s = stream(a[10], X);
+        void* s = stream(X);
         call("omm_lora_matmul", [&] {
             return L.lora_matmul(x.p, w.p, la.p, lb.p, idx.p, scale.p, bias.p, trans, &y.t, ws.ptr(), ws.bytes(), s);
         });
@@ -179,24 +178,24 @@ PyObject* lora_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// logits, top_k, renormalize, indices, weights, stream
+// logits, top_k, renormalize, indices, weights
 PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 6, [&] {
+    return guarded(n, 5, [&] {
         const at::Tensor& logits = tensor(a[0]);
         const int64_t k = integer(a[1]), renorm = integer(a[2]);
         if (logits.dim() != 2) fail(PyExc_ValueError, "logits must be 2-d");
         Arg x(a[0]);
         const int64_t M = logits.size(0), kk = std::max<int64_t>(k, 0);
         Out ids(a[3], {M, kk}, logits, at::kInt), w(a[4], {M, kk}, logits, at::kFloat);
-        void* s = stream(a[5], logits);
+        void* s = stream(logits);
         call("omm_moe_route", [&] { return L.moe_route(x.p, (int)k, renorm != 0, &ids.t, &w.t, s); });
         return pack({ids.x, w.x});
     });
 }
 
-// X, router_logits, top_k, W_gate, W_up, W_down, renormalize, activation, trans, Y, workspace, stream
+// X, router_logits, top_k, W_gate, W_up, W_down, renormalize, activation, trans, Y, workspace
 PyObject* moe_layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 12, [&] {
+    return guarded(n, 11, [&] {
         const at::Tensor &X = tensor(a[0]), &W = tensor(a[3]);
         const int64_t k = integer(a[2]), renorm = integer(a[6]), act = integer(a[7]), trans = integer(a[8]);
         if (X.dim() != 2 || W.dim() != 3) fail(PyExc_ValueError, "X must be 2-d, the weights 3-d");
@@ -204,7 +203,7 @@ PyObject* moe_layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t M = X.size(0), K = X.size(1), E = W.size(0), F = W.size(trans ? 1 : 2);
         Out y(a[9], {M, K}, X, X.scalar_type());
         const Workspace ws = workspace(a[10], X, [&] { return L.moe_layer_ws(M, K, F, E, k); });
-        void* s = stream(a[11], X);
+        void* s = stream(X);
         call("omm_moe_layer", [&] {
             return L.moe_layer(x.p, logits.p, (int)k, renorm != 0, wg.p, wu.p, wd.p, (int)act, trans != 0, &y.t,
                                ws.ptr(), ws.bytes(), s);
@@ -213,9 +212,9 @@ PyObject* moe_layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// logits, targets, top_k, workspace, stream
+// logits, targets, top_k, workspace
 PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 5, [&] {
+    return guarded(n, 4, [&] {
         const at::Tensor& logits = tensor(a[0]);
         const int64_t k = integer(a[2]), kk = std::max<int64_t>(k, 0);
         if (logits.dim() != 2) fail(PyExc_ValueError, "logits must be 2-d");
@@ -225,7 +224,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
             lse(nullptr, {M}, logits, at::kFloat), ids(nullptr, {M, kk}, logits, at::kInt),
             tlp(nullptr, {M, kk}, logits, at::kFloat);
         const Workspace ws = workspace(a[3], logits, [&] { return L.token_logprobs_ws(M, V, k); });
-        void* s = stream(a[4], logits);
+        void* s = stream(logits);
         call("omm_token_logprobs", [&] {
             return L.token_logprobs(x.p, t.p, (int)k, &lp.t, &ent.t, &lse.t, &ids.t, &tlp.t, ws.ptr(), ws.bytes(), s);
         });
@@ -233,13 +232,13 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// logits, targets, lse, entropy, grad_logprobs, grad_entropy, grad_logits, stream
+// logits, targets, lse, entropy, grad_logprobs, grad_entropy, grad_logits
 PyObject* token_logprobs_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 8, [&]() -> PyObject* {
+    return guarded(n, 7, [&]() -> PyObject* {
         const at::Tensor& logits = tensor(a[0]);
         Arg x(a[0]), t(a[1]), lse(a[2]), ent(a[3]), gl(a[4]), gh(a[5]);
         Out g(a[6], logits.sizes(), logits, logits.scalar_type());
-        void* s = stream(a[7], logits);
+        void* s = stream(logits);
         call("omm_token_logprobs_grad",
              [&] { return L.token_logprobs_grad(x.p, t.p, lse.p, ent.p, gl.p, gh.p, &g.t, s); });
         return THPVariable_Wrap(g.x);
