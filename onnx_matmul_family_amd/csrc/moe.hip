@@ -302,7 +302,7 @@ __global__ __launch_bounds__(256) void moe_down_any_kernel(LayerArgs a) {
     const int64_t sf = a.trans ? 1 : a.K, sn = a.trans ? a.F : 1;
     const int64_t fc = (a.F + 3) / 4, f0 = wave * fc, f1 = f0 + fc < a.F ? f0 + fc : a.F;
     float acc = 0.0f;
-    for (int s = 0; s < a.k; ++s) {
+    for (int s = 0; s < (a.F ? a.k : 0); ++s) {  // (no hidden columns: no first kernel, no selections)
         const int64_t p = m * a.k + s;
         const E* wd = (const E*)a.wd + (int64_t)a.ids[p] * a.K * a.F + (n < a.K ? n : 0) * sn;
         const float* h = a.h + p * a.F;
@@ -318,7 +318,7 @@ template <int DT>
 void layer_any(const LayerArgs& a, hipStream_t s) {
     const int pairs = a.M * a.k, jmax = pairs < a.E ? pairs : a.E;
     const dim3 gu((unsigned)((a.F + a.hw - 1) / a.hw), (unsigned)jmax);
-    moe_up_any_kernel<DT><<<gu, 256, 0, s>>>(a);
+    if (a.F) moe_up_any_kernel<DT><<<gu, 256, 0, s>>>(a);
     const dim3 gd((unsigned)((a.K + 63) / 64), (unsigned)a.M);
     moe_down_any_kernel<DT><<<gd, 256, 0, s>>>(a);
 }
