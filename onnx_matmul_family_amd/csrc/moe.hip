@@ -143,7 +143,7 @@ struct LayerArgs {
     uint32_t* done;        // workspace: finished workgroups of each 128 output columns
     int64_t K, F;
     int M, E, k, renorm, act, trans, logits_kind, splits;
-    int hw;                // columns of a workgroup of the first kernel (16 or 64)
+    int hw;                // columns of a workgroup of the first kernel (16 or 64; streamed form)
 };
 
 __device__ __forceinline__ float activate(float g, int act) {
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(256) void moe_down_any_kernel(LayerArgs a) {
 template <int DT>
 void layer_any(const LayerArgs& a, hipStream_t s) {
     const int pairs = a.M * a.k, jmax = pairs < a.E ? pairs : a.E;
-    const dim3 gu((unsigned)((a.F + a.hw - 1) / a.hw), (unsigned)jmax);
+    const dim3 gu((unsigned)((a.F + 63) / 64), (unsigned)jmax);
     if (a.F) moe_up_any_kernel<DT><<<gu, 256, 0, s>>>(a);
     const dim3 gd((unsigned)((a.K + 63) / 64), (unsigned)a.M);
     moe_down_any_kernel<DT><<<gd, 256, 0, s>>>(a);
