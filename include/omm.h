@@ -312,6 +312,8 @@ int omm_moe_route(const omm_tensor* logits, int top_k, int renormalize, omm_tens
  *   trans = 0: W_gate, W_up (E, K, F), W_down (E, F, K) (the layout of
  *   omm_grouped_matmul's weights); trans != 0: (E, F, K) and (E, K, F) (as
  *   linear layers store them).  1 <= top_k <= E.  F = 0: Y = 0.
+ *   A selection of weight 0 (an expert whose logit is -inf, or too far below the
+ *   largest) adds nothing, whatever the expert's weights hold.
  *   act: OMM_ACT_SILU x / (1 + e^-x), OMM_ACT_GELU x (1 + erf(x / sqrt 2)) / 2.
  *   The product of the two branches is held in fp32; one rounding to T at the end.
  *   Only the experts in use are read, each once for its tokens (an expert of more

@@ -122,11 +122,14 @@ void route_launch(const RouteArgs& a, hipStream_t s) {
 
 // ------------------------------------------------------------------ layer
 // The (token, selection) pairs of one expert in use, as the first kernel
-// leaves them to the second
+// leaves them to the second; ~pair where the weight is 0.  Such a pair adds
+// nothing, whatever the expert's weights hold: 0 NaN would not be 0, and an
+// excluded expert is selected where fewer than k others are left.
 struct ExpertList {
     int32_t e, n, active, unused;
     int32_t pair[kMaxTok];
 };
+__device__ __forceinline__ int pair_of(int p) { return p ^ (p >> 31); }
 
 struct LayerArgs {
     const void* X;         // (M, K)
@@ -135,7 +138,7 @@ struct LayerArgs {
     const void* wu;
     const void* wd;        // trans 0: (E, F, K), 1: (E, K, F)
     void* Y;               // (M, K)
-    int32_t* ids;          // workspace: (M, k) selections (element-wise form)
+    int32_t* ids;          // workspace: (M, k) selections, -1 for those of weight 0 (element-wise form)
     ExpertList* lists;     // workspace: (min(E, M k)) (streamed form)
     float* hmax;           // workspace: (M k, ceil(F / hw)) largest |h| (fp16)
     float* h;              // workspace: (M k, F), weighted
@@ -249,7 +252,7 @@ __global__ __launch_bounds__(256) void moe_up_any_kernel(LayerArgs a) {
     route_all<4>(a, r, lane, wave);
     __syncthreads();
     if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int i = tid; i < a.M * a.k; i += 256) a.ids[i] = r.id[i];
+        for (int i = tid; i < a.M * a.k; i += 256) a.ids[i] = r.w[i] == 0.0f ? -1 : r.id[i];
     expert_rows<256>(r, a.M, a.k, (int)blockIdx.y, tid);
     if (r.e < 0) return;
     const int64_t f = (int64_t)blockIdx.x * 64 + lane;
@@ -304,6 +307,7 @@ __global__ __launch_bounds__(256) void moe_down_any_kernel(LayerArgs a) {
     float acc = 0.0f;
     for (int s = 0; s < (a.F ? a.k : 0); ++s) {  // (no hidden columns: no first kernel, no selections)
         const int64_t p = m * a.k + s;
+        if (a.ids[p] < 0) continue;
         const E* wd = (const E*)a.wd + (int64_t)a.ids[p] * a.K * a.F + (n < a.K ? n : 0) * sn;
         const float* h = a.h + p * a.F;
         for (int64_t f = f0; f < f1; ++f) acc = fmaf(h[f], elem_f32<DT>(wd[f * sf]), acc);
@@ -459,7 +463,10 @@ __global__ __launch_bounds__(64 * NWS, NWS == 4 ? 3 : 2) void moe_up_kernel(Laye
     expert_rows<64 * NWS>(r, a.M, a.k, (int)blockIdx.y, tid);
     if (blockIdx.x == 0 && tid < 64) {
         ExpertList& l = a.lists[blockIdx.y];
-        if (tid < r.n) l.pair[tid] = r.tok[tid] * a.k + r.slot[tid];
+        if (tid < r.n) {
+            const int p = r.tok[tid] * a.k + r.slot[tid];
+            l.pair[tid] = r.w[p] == 0.0f ? ~p : p;
+        }
         if (tid == 0) {
             l.e = r.e;
             l.n = r.n;
@@ -505,11 +512,11 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
     float undo[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        x.p[g] = a.h + (int64_t)r.pair[min(t0 + 16 * g + tr, r.n - 1)] * F + x.off(lane);
+        x.p[g] = a.h + (int64_t)pair_of(r.pair[min(t0 + 16 * g + tr, r.n - 1)]) * F + x.off(lane);
         undo[g] = 1.0f;
         if constexpr (DT == 1) {  // the row's largest value over this wave's range -> [2^13, 2^14)
             const int slabs = (F + a.hw - 1) / a.hw;
-            const int p = r.pair[min(t0 + 16 * g + i, r.n - 1)];
+            const int p = pair_of(r.pair[min(t0 + 16 * g + i, r.n - 1)]);
             float mx = 0.0f;
             for (int b = s0 * 32 / a.hw; b < min(slabs, (s1 * 32 + a.hw - 1) / a.hw); ++b) mx = fmaxf(mx, a.hmax[(int64_t)p * slabs + b]);
             int ex = 0;
@@ -537,7 +544,8 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
             float v = 0.0f;
 #pragma unroll
             for (int u = 0; u < NWS; ++u) v += red[red_index(u, j, l, rr)];
-            part_store<128>(a.part, ((int64_t)blockIdx.x * a.splits + sp) * (a.M * a.k) + r.pair[t], c, v);
+            const int p = r.pair[t];
+            part_store<128>(a.part, ((int64_t)blockIdx.x * a.splits + sp) * (a.M * a.k) + pair_of(p), c, p < 0 ? 0.0f : v);
         }
     }
 }
