@@ -271,9 +271,9 @@ int omm_grouped_matmul_check(const void* workspace, void* stream, int64_t* inval
  *   adapter_indices (M) OMM_I32 / OMM_I64: a row whose index is outside [0, G)
  *   (-1 by custom) has no adapter.  adapter_scale (G) OMM_F32 or NULL (1).
  *   R <= 256 (else OMM_ERR_UNSUPPORTED).  The middle product X A is held in fp32;
- *   one rounding to T of the whole sum.  Only for a W of
- *   2 GiB or more, or K or N under 8, may the adapter's term (with the bias) be
- *   rounded to T once before the sum.
+ *   one rounding to T of the whole sum.  Only for a W of 2 GiB or more, or K or N
+ *   under 8, or more than 65472 rows of fp32, may the adapter's term (with the
+ *   bias) be rounded to T once before the sum.
  *   A row's result does not depend on the other rows' adapters (an infinity or
  *   NaN in one adapter stays in its rows) and is the same from call to call.
  * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE, OMM_ERR_UNSUPPORTED,

@@ -769,7 +769,7 @@ int omm_lora_matmul(const omm_tensor* X, const omm_tensor* W, const omm_tensor* 
     if (bias && !has_shape(bias, 1, N)) return OMM_ERR_SHAPE;
     if (!has_shape(Y, 2, M, N)) return OMM_ERR_SHAPE;
     if (M == 0 || N == 0) return OMM_OK;
-    if (R > 256 || M * ((N + 255) / 256) > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
+    if (R > 256 || N > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
     if ((rc = check_workspace(workspace, workspace_bytes, omm::lora_workspace_bytes(M, K, N, R, kind)))) return rc;
     omm::LoraArgs a;
     a.X = X->data;

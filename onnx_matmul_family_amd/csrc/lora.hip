@@ -11,6 +11,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kernels.hpp"
 #include "lora_args.hpp"
 #include "row_select.hpp"
@@ -20,13 +22,15 @@ namespace omm {
 
 namespace {
 
-// T[m, r] = scale[g] sum_k X[m, k] A[g, k, r]: a workgroup a row, a wave an r
+// T[p, r] = scale[g] sum_k X[m, k] A[g, k, r], m the row at position p: a
+// workgroup a row, a wave an r.  fp16, for the tiles: the largest |T| of the row.
 template <int DT>
 __global__ __launch_bounds__(256) void lora_shrink_any_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t m = blockIdx.x, g = row_adapter(a, m);
+    const int64_t p = blockIdx.x, m = a.perm ? a.perm[p] : p, g = row_adapter(a, m);
     if (g < 0) return;
+    float most = 0.0f;
     const E* x = (const E*)a.X + m * a.K;
     const int64_t sk = a.trans ? 1 : a.R, sr = a.trans ? a.K : 1;
     for (int r = wave; r < a.R; r += 4) {
@@ -34,7 +38,15 @@ __global__ __launch_bounds__(256) void lora_shrink_any_kernel(LoraK a) {
         float acc = 0.0f;
         for (int64_t k = lane; k < a.K; k += 64) acc = fmaf(elem_f32<DT>(x[k]), elem_f32<DT>(w[k * sk]), acc);
         acc = wave_sum(acc);
-        if (lane == 0) a.T[m * a.R + r] = a.scale ? acc * a.scale[g] : acc;
+        if (a.scale) acc *= a.scale[g];
+        most = fmaxf(most, fabsf(acc));
+        if (lane == 0) a.T[p * a.R + r] = acc;
+    }
+    if (DT == 1 && a.tmax) {
+        __shared__ float red[4];
+        if (lane == 0) red[wave] = most;
+        __syncthreads();
+        if (threadIdx.x == 0) a.tmax[p] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     }
 }
 
@@ -406,9 +418,32 @@ size_t part_bytes(int64_t M, int64_t K, int64_t N) {
     return most;
 }
 
-// whole groups of 8 columns, W within 32-bit byte offsets, a row a grid index
-bool streamable(int64_t M, int64_t K, int64_t N, int dt) {
-    return M < 65536 && K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
+// whole groups of 8 columns, W within 32-bit byte offsets
+bool streamable(int64_t K, int64_t N, int dt) {
+    return K >= 8 && N >= 8 && K * N < (dt == 2 ? 1LL << 29 : 1LL << 30);
+}
+
+// Rows of one launch of each form; a call of more is taken in pieces, one after
+// the other in the same workspace (bf16 and fp16: the forms that add the adapter's
+// term to a dense product round it to T before the sum).
+//   streamed: a row a grid index in y.
+//   tiles: 32-bit byte offsets into X (any other form of lora_rows.hip: as many);
+//     all of them within 2^32 threads.
+//   element-wise: 2^32 threads of 256 columns.
+constexpr int64_t kStreamRows = 1023 * kFew;
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;
+int64_t tile_rows(int64_t K, int64_t N, int dt) {
+    int64_t n = 1 << 20;
+    const int64_t offsets = dt < 2 && K > 0 ? ((1LL << 31) - 1) / (2 * K) : n;
+    if (offsets >= 256) n = std::min(n, offsets);  // (else no tiles)
+    n = std::min(n, kMaxBlocks / ((N + 127) / 128) * 128);
+    return std::max<int64_t>(n / 256 * 256, 128);
+}
+int64_t any_rows(int64_t N) { return std::max<int64_t>(1, kMaxBlocks / ((N + 255) / 256)); }
+// M rows in pieces of at most `most`: rows of a piece (the last one may have fewer)
+int64_t piece_rows(int64_t M, int64_t most) {
+    const int64_t n = (M + most - 1) / most, even = (M + n - 1) / n;
+    return std::min(most, (even + 255) / 256 * 256);
 }
 
 // Where the streamed form (W once per 64 rows, mostly from the caches) is ahead
@@ -478,14 +513,23 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt) {
-    // (the form depends on layout and alignment too: room for each)
-    const size_t rows = M > kFew || !streamable(M, K, N, dt) ? lora_rows_workspace_bytes(M, R) : 0;
-    if (!streamable(M, K, N, dt)) return rows;
+// of one piece (the form depends on layout and alignment too: room for each)
+static size_t piece_bytes(int64_t M, int64_t K, int64_t N, int64_t R, bool stream) {
+    const size_t rows = M > kFew || !stream ? lora_rows_workspace_bytes(M, R) : 0;
+    if (!stream || M > kStreamRows) return rows;
     const size_t groups = (size_t)(M + kFew - 1) / kFew;
-    const size_t stream = align256(groups * kFew * R * 4 * kParts<0>) + align256(part_bytes(M, K, N)) +
-                          align256(groups * ((N + 15) / 16) * 4);
-    return rows > stream ? rows : stream;
+    const size_t bytes = align256(groups * kFew * R * 4 * kParts<0>) + align256(part_bytes(M, K, N)) +
+                         align256(groups * ((N + 15) / 16) * 4);
+    return rows > bytes ? rows : bytes;
+}
+size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt) {
+    const bool stream = streamable(K, N, dt) && !(dt == 2 && M > kStreamRows);
+    size_t most = 0;
+    for (const int64_t limit : {kStreamRows, tile_rows(K, N, dt), any_rows(N)}) {
+        const int64_t piece = piece_rows(M, limit), last = M - (M - 1) / piece * piece;
+        for (const int64_t m : {piece, last}) most = std::max(most, piece_bytes(std::min(m, M), K, N, R, stream));
+    }
+    return most;
 }
 
 hipError_t lora_add_dense(const LoraK& a, const void* C, int dt, hipStream_t s) {
@@ -510,32 +554,21 @@ hipError_t lora_add_dense(const LoraK& a, const void* C, int dt, hipStream_t s) 
     return dt == 2 ? launch_dense_f32(d, s) : launch_dense16(d, dt, s);
 }
 
-hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
-    LoraK a = {};
-    a.X = l.X;
-    a.W = l.W;
-    a.A = l.A;
-    a.B = l.B;
-    a.idx = l.idx;
-    a.scale = l.scale;
-    a.bias = l.bias;
-    a.Y = l.Y;
-    a.T = (float*)ws;
-    a.M = l.M;
-    a.K = l.K;
-    a.N = l.N;
-    a.G = l.G;
-    a.R = (int)l.R;
-    a.trans = l.trans;
-    a.idx64 = l.idx64;
-    const bool rows_ok = lora_rows_ok(l.M, l.K, l.N, l.R, l.G, l.trans);
-    if (streamable(l.M, l.K, l.N, dt) &&
-        (!rows_ok || stream_ahead(l.M, l.K, l.N, lora_tiles_ok(a, dt)))) {
-        const StreamPlan p = stream_plan(l.M, l.K, l.N, l.trans);
+void lora_shrink_any(const LoraK& a, int dt, hipStream_t s) {
+    const dim3 grid((unsigned)a.M);
+    if (dt == 0) lora_shrink_any_kernel<0><<<grid, 256, 0, s>>>(a);
+    else if (dt == 1) lora_shrink_any_kernel<1><<<grid, 256, 0, s>>>(a);
+    else lora_shrink_any_kernel<2><<<grid, 256, 0, s>>>(a);
+}
+
+// one piece
+static hipError_t launch_piece(LoraK a, int dt, bool stream, bool rows, void* ws, hipStream_t s) {
+    if (stream && (!rows || stream_ahead(a.M, a.K, a.N, lora_tiles_ok(a, dt)))) {
+        const StreamPlan p = stream_plan(a.M, a.K, a.N, a.trans);
         a.splits = p.splits;
         a.cw = p.cw;
-        a.part = (float*)((char*)ws + align256((size_t)(l.M + kFew - 1) / kFew * kFew * l.R * 4 * kParts<0>));
-        a.done = (uint32_t*)((char*)a.part + align256(part_bytes(l.M, l.K, l.N)));
+        a.part = (float*)((char*)ws + align256((size_t)(a.M + kFew - 1) / kFew * kFew * a.R * 4 * kParts<0>));
+        a.done = (uint32_t*)((char*)a.part + align256(part_bytes(a.M, a.K, a.N)));
         log_choice("lora_matmul: streamed, %d columns a workgroup, K in %d part(s)", a.cw, a.splits);
         switch (dt * 2 + a.trans) {
             case 0: lora_streamed<0, 0>(a, s); break;
@@ -547,22 +580,56 @@ hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
         }
         return hipGetLastError();
     }
-    if (rows_ok) return launch_lora_rows(a, dt, ws, s);
+    if (rows) return launch_lora_rows(a, dt, ws, s);
     log_choice("lora_matmul: element-wise");
-    const int64_t nblk = (l.N + 255) / 256;
-    const dim3 gs((unsigned)l.M), gd((unsigned)(l.M * nblk));
-    if (dt == 0) {
-        lora_shrink_any_kernel<0><<<gs, 256, 0, s>>>(a);
-        lora_delta_any_kernel<0><<<gd, 256, 0, s>>>(a, nblk);
-    } else if (dt == 1) {
-        lora_shrink_any_kernel<1><<<gs, 256, 0, s>>>(a);
-        lora_delta_any_kernel<1><<<gd, 256, 0, s>>>(a, nblk);
-    } else {
-        lora_shrink_any_kernel<2><<<gs, 256, 0, s>>>(a);
-        lora_delta_any_kernel<2><<<gd, 256, 0, s>>>(a, nblk);
-    }
+    const int64_t nblk = (a.N + 255) / 256;
+    const dim3 grid((unsigned)(a.M * nblk));
+    lora_shrink_any(a, dt, s);
+    if (dt == 0) lora_delta_any_kernel<0><<<grid, 256, 0, s>>>(a, nblk);
+    else if (dt == 1) lora_delta_any_kernel<1><<<grid, 256, 0, s>>>(a, nblk);
+    else lora_delta_any_kernel<2><<<grid, 256, 0, s>>>(a, nblk);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : lora_add_dense(a, a.Y, dt, s);
+}
+
+hipError_t launch_lora(const LoraArgs& l, int dt, void* ws, hipStream_t s) {
+    LoraK a = {};
+    a.X = l.X;
+    a.W = l.W;
+    a.A = l.A;
+    a.B = l.B;
+    a.idx = l.idx;
+    a.scale = l.scale;
+    a.bias = l.bias;
+    a.Y = l.Y;
+    a.T = (float*)ws;
+    a.K = l.K;
+    a.N = l.N;
+    a.G = l.G;
+    a.R = (int)l.R;
+    a.trans = l.trans;
+    a.idx64 = l.idx64;
+    // Over 65472 rows, us a call, streamed / other (rank 16, trans 1):
+    //   fp32, 65600 rows of 1024 x 1024            2974 / 1920 (adapters into Y, the dense product)
+    //                       2001 x 1003            5221 / 3055
+    //   bf16, 65600 rows of 1024 x 1024, rank 4,
+    //         trans 0                              1856 / 481 (tiles, T by elements)
+    const bool many = l.M > kStreamRows;
+    const bool stream = streamable(l.K, l.N, dt) && !(dt == 2 && many);
+    a.M = piece_rows(l.M, tile_rows(l.K, l.N, dt));
+    const bool narrow = !l.trans && l.R > 0 && l.R < 8, tiles = lora_tiles_ok(a, dt);
+    const bool rows = lora_rows_ok(l.K, l.N, l.R, l.G) && (!narrow || (many && tiles));
+    const int64_t piece = rows && (tiles || !stream) ? a.M : piece_rows(l.M, stream ? kStreamRows : any_rows(l.N));
+    const int64_t elem = dt == 2 ? 4 : 2;
+    for (int64_t m = 0; m < l.M; m += piece) {
+        a.M = std::min(piece, l.M - m);
+        a.X = (const char*)l.X + m * l.K * elem;
+        a.Y = (char*)l.Y + m * l.N * elem;
+        a.idx = (const char*)l.idx + m * (l.idx64 ? 8 : 4);
+        const hipError_t e = launch_piece(a, dt, stream, rows, ws, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace omm

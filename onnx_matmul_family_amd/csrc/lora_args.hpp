@@ -47,9 +47,13 @@ __device__ __forceinline__ void row_group(LoraK& a, int z, int parts, int elem) 
 // Y = X W + C, C (M, N) of T (may be Y)
 hipError_t lora_add_dense(const LoraK& a, const void* C, int dt, hipStream_t s);
 
+// T (and fp16: tmax, if not nullptr) by elements, of any sizes
+void lora_shrink_any(const LoraK& a, int dt, hipStream_t s);
+
 // whether lora_tile_kernel takes these operands
 bool lora_tiles_ok(const LoraK& a, int dt);
-bool lora_rows_ok(int64_t M, int64_t K, int64_t N, int64_t R, int64_t G, int trans);
+// whether the forms of lora_rows.hip take these sizes (of up to 2^20 rows)
+bool lora_rows_ok(int64_t K, int64_t N, int64_t R, int64_t G);
 size_t lora_rows_workspace_bytes(int64_t M, int64_t R);
 hipError_t launch_lora_rows(LoraK a, int dt, void* ws, hipStream_t s);
 

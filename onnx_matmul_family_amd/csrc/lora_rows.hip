@@ -10,7 +10,8 @@
 //                            leaves, T B is added to its accumulators.  T's
 //                            rows enter as three 16-bit parts, so neither T
 //                            nor T B is rounded.
-// Operands that the DMA cannot take (rows not 16-byte aligned) and fp32:
+// Operands that the DMA cannot take (rows not 16-byte aligned) and fp32, with a
+// W too large for the streamed form (2 GiB and more):
 //   lora_expand_kernel       bias + T B into Y, to which the framework's dense
 //                            product is then added.
 // A block of rows that mixes adapters multiplies each one's B on its own and
@@ -450,7 +451,10 @@ template <int DT, int TRANS>
 hipError_t rows_run(const LoraK& a, hipStream_t s) {
     if (a.perm && a.R > 0 && a.G > 0)
         lora_sort_kernel<<<1, 64 * kSortWaves, kSortWaves * (a.G + 1) * sizeof(int), s>>>(a, (int)a.G + 1);
-    if (a.R > 0 && a.G > 0) shrink<DT, TRANS>(a, s);
+    if (a.R > 0 && a.G > 0) {
+        if (!TRANS && a.R < 8) lora_shrink_any(a, DT, s);  // (no group of 8 columns of A)
+        else shrink<DT, TRANS>(a, s);
+    }
     if constexpr (DT < 2) {
         if (lora_tiles_ok(a, DT)) {
             const int64_t big = (a.M + 255) / 256 * ((a.N + 255) / 256);
@@ -483,11 +487,10 @@ bool lora_tiles_ok(const LoraK& a, int dt) {
 }
 
 // whole groups of 8 (columns of a fp32 group: 4), one adapter's matrices within
-// 32-bit offsets, tile counts and rows in 32 bits
-bool lora_rows_ok(int64_t M, int64_t K, int64_t N, int64_t R, int64_t G, int trans) {
-    return K >= 8 && N >= 8 && (trans || R >= 8 || R == 0) && K * R < (1LL << 30) && N * R < (1LL << 30) &&
-           K < (1 << 30) && N < (1 << 30) && G < (1LL << 31) - 1 && M < (1LL << 30) &&
-           (M + 127) / 128 * ((N + 127) / 128) < (1LL << 31) && (M + 63) / 64 < 65536 * 64;
+// 32-bit offsets
+bool lora_rows_ok(int64_t K, int64_t N, int64_t R, int64_t G) {
+    return K >= 8 && N >= 8 && K * R < (1LL << 30) && N * R < (1LL << 30) &&
+           K < (1 << 30) && N < (1 << 30) && G < (1LL << 31) - 1;
 }
 
 size_t lora_rows_workspace_bytes(int64_t M, int64_t R) {
