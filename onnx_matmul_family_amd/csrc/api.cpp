@@ -735,7 +735,11 @@ int check_workspace(const void* ws, size_t bytes, size_t need) {
     return !ws || bytes < need || ((uintptr_t)ws & 255) ? OMM_ERR_WORKSPACE : OMM_OK;
 }
 
-constexpr int64_t kMaxBlocks = 0x7fffffffLL;
+// workgroups of 256 threads in one launch: a grid has at most 2^32 - 1 threads a dim
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;
+constexpr int64_t kMaxIndex = 0x7fffffffLL;  // of a logit, a column
+
+int64_t blocks(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
 }  // namespace
 
@@ -769,7 +773,7 @@ int omm_lora_matmul(const omm_tensor* X, const omm_tensor* W, const omm_tensor* 
     if (bias && !has_shape(bias, 1, N)) return OMM_ERR_SHAPE;
     if (!has_shape(Y, 2, M, N)) return OMM_ERR_SHAPE;
     if (M == 0 || N == 0) return OMM_OK;
-    if (R > 256 || N > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
+    if (R > 256 || blocks(N, 256) > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
     if ((rc = check_workspace(workspace, workspace_bytes, omm::lora_workspace_bytes(M, K, N, R, kind)))) return rc;
     omm::LoraArgs a;
     a.X = X->data;
@@ -802,7 +806,7 @@ int omm_moe_route(const omm_tensor* logits, int top_k, int renormalize, omm_tens
     if (top_k < 0 || top_k > E) return OMM_ERR_SHAPE;
     if (!has_shape(indices, 2, M, top_k) || !has_shape(weights, 2, M, top_k)) return OMM_ERR_SHAPE;
     if (M == 0 || top_k == 0) return OMM_OK;
-    if (E > OMM_MOE_MAX_EXPERTS || top_k > OMM_MOE_MAX_TOP_K || M > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
+    if (E > OMM_MOE_MAX_EXPERTS || top_k > OMM_MOE_MAX_TOP_K || blocks(M, 16) > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
     omm::MoeRouteArgs a;
     a.logits = logits->data;
     a.ids = indices->data;
@@ -839,7 +843,7 @@ int omm_moe_layer(const omm_tensor* X, const omm_tensor* router_logits, int top_
     if (activation != OMM_ACT_SILU && activation != OMM_ACT_GELU) return OMM_ERR_UNSUPPORTED;
     if (M == 0 || K == 0) return OMM_OK;
     if (M > OMM_MOE_LAYER_MAX_TOKENS || E > OMM_MOE_MAX_EXPERTS || top_k > OMM_MOE_MAX_TOP_K ||
-        K > kMaxBlocks || F > kMaxBlocks)
+        blocks(K, 64) > kMaxBlocks || blocks(F, 64) > kMaxBlocks)
         return OMM_ERR_UNSUPPORTED;
     if ((rc = check_workspace(workspace, workspace_bytes, omm::moe_layer_workspace_bytes(M, K, F, E, top_k))))
         return rc;
@@ -862,7 +866,7 @@ int omm_moe_layer(const omm_tensor* X, const omm_tensor* router_logits, int top_
 }
 
 size_t omm_token_logprobs_workspace_size(int64_t M, int64_t V, int64_t top_k) {
-    if (M <= 0 || V <= 0 || V > kMaxBlocks || top_k < 0) return 0;
+    if (M <= 0 || V <= 0 || V > kMaxIndex || top_k < 0) return 0;
     return omm::token_logprobs_workspace_bytes(M, V, top_k);
 }
 
@@ -886,7 +890,7 @@ int omm_token_logprobs(const omm_tensor* logits, const omm_tensor* targets, int 
     }
     if (M == 0) return OMM_OK;
     // (at least 512 rows are not split, fewer into at most 64 parts each)
-    if (top_k > OMM_TOKEN_LOGPROBS_MAX_TOP_K || V > kMaxBlocks - 65536 || M > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
+    if (top_k > OMM_TOKEN_LOGPROBS_MAX_TOP_K || V > kMaxIndex - 65536 || M > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
     if ((rc = check_workspace(workspace, workspace_bytes, omm::token_logprobs_workspace_bytes(M, V, top_k))))
         return rc;
     omm::TokenLogprobsArgs a;
@@ -919,7 +923,8 @@ int omm_token_logprobs_grad(const omm_tensor* logits, const omm_tensor* targets,
     for (const omm_tensor* t : {lse, entropy, grad_logprobs, grad_entropy})
         if ((rc = check_f32_vec(t, M))) return rc;
     if (M == 0 || V == 0) return OMM_OK;
-    if (V > kMaxBlocks - 65536 || M * ((V + 1023) / 1024) > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
+    // (workgroups of fewer than 16384 elements: fewer than 2048 of them)
+    if (V > kMaxIndex - 65536 || M * blocks(V, 16384) > kMaxBlocks) return OMM_ERR_UNSUPPORTED;
     omm::TokenLogprobsGradArgs a;
     a.logits = logits->data;
     a.targets = targets->data;
