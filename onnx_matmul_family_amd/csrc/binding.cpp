@@ -105,10 +105,11 @@ Workspace workspace(PyObject* o, const at::Tensor& like, const F& need) {
     return Workspace(o, like, [](const void* f) { return (*(const F*)f)(); }, &need);
 }
 
-int64_t integer(PyObject* o) {
+int integer(PyObject* o) {  // OverflowError for what the library's int does not hold
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw Failed{};
-    return v;
+    if (v != (int)v) fail(PyExc_OverflowError, "integer argument out of range");
+    return (int)v;
 }
 
 // The current stream of x's device, to which what is allocated here belongs too.
@@ -164,7 +165,7 @@ PyObject* pack(std::initializer_list<at::Tensor> xs) {
 PyObject* lora_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 10, [&] {
         const at::Tensor &X = tensor(a[0]), &W = tensor(a[1]), &A = tensor(a[2]);
-        const int trans = (int)integer(a[7]);
+        const int trans = integer(a[7]);
         if (X.dim() != 2 || W.dim() != 2 || A.dim() != 3) fail(PyExc_ValueError, "X and W must be 2-d, A 3-d");
         Arg x(a[0]), w(a[1]), la(a[2]), lb(a[3]), idx(a[4]), scale(a[5]), bias(a[6]);
         const int64_t M = X.size(0), K = X.size(1), N = W.size(trans ? 0 : 1), R = A.size(trans ? 1 : 2);
@@ -182,13 +183,13 @@ PyObject* lora_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 5, [&] {
         const at::Tensor& logits = tensor(a[0]);
-        const int64_t k = integer(a[1]), renorm = integer(a[2]);
+        const int k = integer(a[1]), renorm = integer(a[2]);
         if (logits.dim() != 2) fail(PyExc_ValueError, "logits must be 2-d");
         Arg x(a[0]);
-        const int64_t M = logits.size(0), kk = std::max<int64_t>(k, 0);
+        const int64_t M = logits.size(0), kk = std::max(k, 0);
         Out ids(a[3], {M, kk}, logits, at::kInt), w(a[4], {M, kk}, logits, at::kFloat);
         void* s = stream(logits);
-        call("omm_moe_route", [&] { return L.moe_route(x.p, (int)k, renorm != 0, &ids.t, &w.t, s); });
+        call("omm_moe_route", [&] { return L.moe_route(x.p, k, renorm, &ids.t, &w.t, s); });
         return pack({ids.x, w.x});
     });
 }
@@ -197,7 +198,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* moe_layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 11, [&] {
         const at::Tensor &X = tensor(a[0]), &W = tensor(a[3]);
-        const int64_t k = integer(a[2]), renorm = integer(a[6]), act = integer(a[7]), trans = integer(a[8]);
+        const int k = integer(a[2]), renorm = integer(a[6]), act = integer(a[7]), trans = integer(a[8]);
         if (X.dim() != 2 || W.dim() != 3) fail(PyExc_ValueError, "X must be 2-d, the weights 3-d");
         Arg x(a[0]), logits(a[1]), wg(a[3]), wu(a[4]), wd(a[5]);
         const int64_t M = X.size(0), K = X.size(1), E = W.size(0), F = W.size(trans ? 1 : 2);
@@ -205,8 +206,7 @@ PyObject* moe_layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Workspace ws = workspace(a[10], X, [&] { return L.moe_layer_ws(M, K, F, E, k); });
         void* s = stream(X);
         call("omm_moe_layer", [&] {
-            return L.moe_layer(x.p, logits.p, (int)k, renorm != 0, wg.p, wu.p, wd.p, (int)act, trans != 0, &y.t,
-                               ws.ptr(), ws.bytes(), s);
+            return L.moe_layer(x.p, logits.p, k, renorm, wg.p, wu.p, wd.p, act, trans, &y.t, ws.ptr(), ws.bytes(), s);
         });
         return pack({y.x, ws.x});
     });
@@ -216,7 +216,8 @@ PyObject* moe_layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 4, [&] {
         const at::Tensor& logits = tensor(a[0]);
-        const int64_t k = integer(a[2]), kk = std::max<int64_t>(k, 0);
+        const int k = integer(a[2]);
+        const int64_t kk = std::max(k, 0);
         if (logits.dim() != 2) fail(PyExc_ValueError, "logits must be 2-d");
         Arg x(a[0]), t(a[1]);
         const int64_t M = logits.size(0), V = logits.size(1);
@@ -226,7 +227,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Workspace ws = workspace(a[3], logits, [&] { return L.token_logprobs_ws(M, V, k); });
         void* s = stream(logits);
         call("omm_token_logprobs", [&] {
-            return L.token_logprobs(x.p, t.p, (int)k, &lp.t, &ent.t, &lse.t, &ids.t, &tlp.t, ws.ptr(), ws.bytes(), s);
+            return L.token_logprobs(x.p, t.p, k, &lp.t, &ent.t, &lse.t, &ids.t, &tlp.t, ws.ptr(), ws.bytes(), s);
         });
         return pack({lp.x, ent.x, lse.x, ids.x, tlp.x});
     });
