@@ -87,7 +87,6 @@ struct Out {
     // the caller's tensor, or a new one of this shape
     Out(PyObject* o, at::IntArrayRef shape, const at::Tensor& like, at::ScalarType dt)
         : x(o && o != Py_None ? tensor(o) : at::empty(shape, like.options().dtype(dt))), t(describe(x)) {}
-    explicit Out(const at::Tensor& y) : x(y), t(describe(x)) {}
 };
 
 struct Workspace {
