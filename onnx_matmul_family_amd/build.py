@@ -8,6 +8,7 @@ are disabled (-packed-fp32-ops) and the QLinearMatMul requantisation file is
 built without floating-point contraction, so its fp32 steps stay separately
 rounded.
 """
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -54,12 +55,12 @@ def _build_native(verbose):
     base = os.path.dirname(torch.__file__)
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
     lib = os.path.join(base, "lib")
-    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+    cmd = [hipcc(), "-no-hip-rt", "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
            "-DUSE_ROCM", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
            "-I", os.path.join(HERE, "..", "include"), "-isystem", os.path.join(base, "include"),
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(rocm, "include"),
-           os.path.join(CSRC, "binding.cpp"), "-o", NATIVE + ".tmp", "-L", lib, "-Wl,-rpath," + lib,
+           os.path.join(CSRC, "binding.cpp"), "-x", "none", "-o", NATIVE + ".tmp", "-L", lib, "-Wl,-rpath," + lib,
            "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -70,18 +71,22 @@ def _build_native(verbose):
 
 
 def build(verbose=False, jobs=None):
+    """libomm.so, then _native.so, which only a Python with torch needs: without torch the
+    library is all there is to build."""
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(len(SOURCES), max(1, (os.cpu_count() or 4)))
     with ThreadPoolExecutor(jobs) as ex:
-        native = ex.submit(_build_native, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        native.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+    if importlib.util.find_spec("torch") is None:
+        print("torch is not installed: _native.so is not built", file=sys.stderr)
+    else:
+        _build_native(verbose)
     return LIB
 
 
