@@ -379,7 +379,8 @@ constexpr int64_t kFew = 64;  // rows a group
 //             N = 4104,  1 row    20.2   18.6  16.7  13.5;  43 rows  31.9  26.1  22.4  23.2
 //             N = 8200, 43 rows   50.7   42.3  39.7  35.9
 // So trans 1 (whose columns are rows of memory, any number is as good): as few
-// as leave 260 column blocks, over 16 rows 72.  trans 0: wide ones unless N is
+// as leave 256 column blocks, one a CU (N = 4104, 16 / 32 columns: 1 row 14.9 / 13.7, 16
+// rows 18.0 / 16.1), over 16 rows 72.  trans 0: wide ones unless N is
 // small.  K goes into as many parts as fill 256 CUs, each wave two steps of 32 or
 // more (of the counts that leave a wave the same steps, the smallest), but in
 // one where up to 16 rows already make 100 workgroups (1 row, trans 1, N = 2048:
@@ -391,7 +392,7 @@ StreamPlan stream_plan(int64_t M, int64_t K, int64_t N, int trans) {
     StreamPlan p;
     const bool few = M <= 16;
     if (trans) {
-        const int64_t most = few ? 260 : 72;
+        const int64_t most = few ? 256 : 72;
         p.cw = N <= 16 * most ? 16 : N <= 32 * most ? 32 : N <= 64 * most || !few ? 64 : 128;
     } else if (few) {
         p.cw = N <= 1152 ? 64 : 128;
