@@ -90,6 +90,9 @@ __device__ __forceinline__ void update(Stat& st, const float* f, int pos, Top3& 
     const float ms = safe_max(st.m);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+        // (d is rounded once, which puts a term off by |d| 2^-24 of itself: in the sums
+        // that averages out.  Corrected as in the gradient, 2048 rows of 50001 take 59
+        // us instead of 52, and the error of 64 rows of 131072 stays at 4e-7.)
         const float d = (f[i] - ms) * kLog2e;
         const float e = __builtin_amdgcn_exp2f(d);  // NaN and +inf - +inf reach s
         st.s += e;
@@ -435,10 +438,12 @@ struct GradRow {
     float gl, gh, H, lse;
     int t;
     __device__ __forceinline__ float operator()(float x, int v) const {
-        const float l = x - lse;
-        const float p = __builtin_amdgcn_exp2f(l * kLog2e);
         // p = 0 below -200: the clamp keeps 0 * -inf (a masked logit) out
-        float d = -p * fmaf(gh, fmaxf(l, -200.0f) + H, gl);
+        const float l = x - lse, lc = fmaxf(l, -200.0f), b = l * kLog2e;
+        float p = __builtin_amdgcn_exp2f(b);
+        // (what the rounding of b leaves of l: without it p would be off by |l| 2^-24)
+        p = fmaf(p, fmaf(fmaxf(b, -200.0f * kLog2e), -kLn2, lc), p);
+        float d = -p * fmaf(gh, lc + H, gl);
         return v == t ? d + gl : d;
     }
 };
