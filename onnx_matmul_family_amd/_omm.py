@@ -234,7 +234,8 @@ ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 
 # Marshalled by _native.so (csrc/binding.cpp), which costs a call of a few
-# microseconds less than the ctypes calls above do.
+# microseconds less than the ctypes calls above do.  None of them records an
+# autograd graph: inputs that require a gradient give outputs that do not.
 
 _native = None
 
@@ -320,7 +321,8 @@ def token_logprobs(logits, targets, top_k=0, workspace=None, stream=None):
     """Log probabilities of `targets` under softmax(logits), entropy, log-sum-exp and the top_k tokens.
 
     Returns (logprobs, entropy, lse, top_ids, top_logprobs): fp32 (M), (M), (M), int32 (M, top_k) and
-    fp32 (M, top_k).  A target outside [0, V) gives log probability 0."""
+    fp32 (M, top_k).  A target outside [0, V) gives log probability 0.  No autograd graph is recorded:
+    for the gradient with respect to the logits call token_logprobs_grad with lse (and entropy)."""
     if stream is not None:
         return _on(stream, token_logprobs, logits, targets, top_k, workspace)
     return (_native or native()).token_logprobs(logits, targets, top_k, workspace)
