@@ -820,7 +820,7 @@ int omm_moe_route(const omm_tensor* logits, int top_k, int renormalize, omm_tens
 }
 
 size_t omm_moe_layer_workspace_size(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k) {
-    if (M <= 0 || K <= 0 || F < 0 || E <= 0 || top_k < 0) return 0;
+    if (M <= 0 || K <= 0 || F < 0 || E <= 0 || top_k <= 0) return 0;
     return omm::moe_layer_workspace_bytes(M, K, F, E, top_k);
 }
 

@@ -1,4 +1,8 @@
 """Sizes past what a launch can take are refused on the host, as unsupported."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 om = pytest.importorskip("onnx_matmul_family_amd._omm")
@@ -6,6 +10,7 @@ om = pytest.importorskip("onnx_matmul_family_amd._omm")
 from tests.test_abi_cpu import BF16, F32, I32, I64, T  # noqa: E402
 from tests.test_decode_abi_cpu import layer_args, layer_call, lora_args, lora_call, lp_args, lp_call, opt, route_call  # noqa: E402
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BLOCKS = 1 << 24  # workgroups of 256 threads: 2^32 threads, one more than a grid has
 
 
@@ -39,3 +44,10 @@ def test_columns_of_the_projection(trans):
     a = lora_args(M=1, K=1, N=256 * BLOCKS, r=1, trans=trans)
     a.update(n=1 << 62)
     assert lora_call(a) == -5
+
+
+@pytest.mark.parametrize("sizes", [(2, 8, 6, 4, 0), (2, 8, 0, 4, 0), (64, 4096, 2048, 512, 0)])
+def test_workspace_of_a_layer_that_selects_nothing(sizes):
+    """Asked for before the call's own checks: no division by the number of pairs."""
+    code = "from onnx_matmul_family_amd import _omm as om; assert om.lib().omm_moe_layer_workspace_size%r == 0" % (sizes,)
+    assert subprocess.run([sys.executable, "-c", code], cwd=ROOT).returncode == 0

@@ -59,3 +59,14 @@ def test_status_of_each_refusal():
     assert code(om.lora_matmul, x, W, A, B.transpose(1, 2).contiguous(), idx) == -3
     assert code(om.moe_layer, x, x, 2, *[torch.randn((16, 16, 16), device="cuda") for _ in range(3)],
                 workspace=small) == -6
+
+
+def test_no_selections():
+    """top_k = 0: the router has nothing to write, the layer refuses."""
+    x, w = torch.randn((4, 16), device="cuda"), torch.randn((16, 16, 16), device="cuda")
+    ids, p = om.moe_route(x, 0)
+    assert ids.shape == (4, 0) and p.shape == (4, 0)
+    for k in (0, -1):
+        with pytest.raises(om.OmmError) as e:
+            om.moe_layer(x, x, k, w, w, w)
+        assert e.value.code == -3
