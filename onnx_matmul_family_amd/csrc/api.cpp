@@ -821,6 +821,9 @@ int omm_moe_route(const omm_tensor* logits, int top_k, int renormalize, omm_tens
 
 size_t omm_moe_layer_workspace_size(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k) {
     if (M <= 0 || K <= 0 || F < 0 || E <= 0 || top_k <= 0) return 0;
+    if (M > OMM_MOE_LAYER_MAX_TOKENS || top_k > OMM_MOE_MAX_TOP_K || blocks(K, 64) > kMaxBlocks ||
+        blocks(F, 64) > kMaxBlocks)
+        return 0;  // (what the call refuses; products of such sizes need not fit 64 bits)
     return omm::moe_layer_workspace_bytes(M, K, F, E, top_k);
 }
 

@@ -46,8 +46,9 @@ def test_columns_of_the_projection(trans):
     assert lora_call(a) == -5
 
 
-@pytest.mark.parametrize("sizes", [(2, 8, 6, 4, 0), (2, 8, 0, 4, 0), (64, 4096, 2048, 512, 0)])
-def test_workspace_of_a_layer_that_selects_nothing(sizes):
-    """Asked for before the call's own checks: no division by the number of pairs."""
+@pytest.mark.parametrize("sizes", [(2, 8, 6, 4, 0), (2, 8, 0, 4, 0), (64, 4096, 2048, 512, 0),
+                                   (1 << 31, 1 << 20, 256, 9, 1 << 32), (1, 1 << 62, 1 << 62, 4, 2)])
+def test_workspace_of_a_layer_that_is_refused(sizes):
+    """Asked for before the call's own checks: no division by the number of pairs, be it 0 or past 64 bits."""
     code = "from onnx_matmul_family_amd import _omm as om; assert om.lib().omm_moe_layer_workspace_size%r == 0" % (sizes,)
     assert subprocess.run([sys.executable, "-c", code], cwd=ROOT).returncode == 0
