@@ -4,9 +4,9 @@
 //
 // Here: the streamed form by groups of 64 rows (T = scale X A on the vector ALU,
 // then X W streamed once a group with T B added), and an element-wise form for
-// what it does not take.  One row, 4096 x 4096, rank 16 (bf16, trans 1): 3.1 + 6.2
-// us, W at 5.4 TB/s from the last-level cache; 43 rows of 32 adapters, 4096 x
-// 4104, rank 24 (fp16, trans 0): 4.4 + 21 us, where W takes 7 and the join of the
+// what it does not take.  One row, 4096 x 4096, rank 16 (bf16, trans 1): 3.2 + 6.5
+// us, W at 5.2 TB/s from the last-level cache; 43 rows of 32 adapters, 4096 x
+// 4104, rank 24 (fp16, trans 0): 4.4 + 22 us, where W takes 7 and the join of the
 // K parts with its round trips as long.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -36,7 +36,7 @@ __device__ __forceinline__ int row_of(const LoraK& a, int p) { return a.perm ? a
 // each wave counts its contiguous share of the rows per bin, a scan over (bin,
 // wave) gives every wave its place in every bin, and it writes its rows there.
 // 4096 rows: 8 us in runs of 9 bins, 11 us mixed over 17; the tiles
-// that use the order take 225.
+// that use the order take 232.
 __global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int bins) {
     extern __shared__ int hist[];  // [wave][bin]
     __shared__ int wsum[kSortWaves];
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
 // BKM: W (N, K), B (G, N, R); else W (K, N), B (G, R, N).
 // TH: column fragments of a pass of the epilogue; fewer (4 of 8) leave the
 // registers to keep B's fragments of 64 r from block to block instead of 32.
-// 4096 x 4096 x 8192 with rank 32 (bf16): 225 us, 1.23 PFLOP/s; the K loop alone,
+// 4096 x 4096 x 8192 with rank 32 (bf16): 232 us, 1.19 PFLOP/s; the K loop alone,
 // as the dense product runs it, takes 222 and up (it is bound by the matrix unit
 // under the chip's clock).
 template <int DT, bool BKM, int BT, int TH>

@@ -11,7 +11,7 @@
 // workspace.  The second multiplies h by the down weights.
 //
 // Both are one read of the weights in use.  One token, 8 of 64 experts, 4096 x
-// 2048 (bf16): 54 + 28 us for 268 + 134 MB; 32 tokens: 402 + 201 us for 2.1 +
+// 2048 (bf16): 54 + 28 us for 268 + 134 MB; 32 tokens: 404 + 201 us for 2.1 +
 // 1.1 GB, 5.4 TB/s, which is what the memory gives.  Small layers are bound by
 // the steps around the stream: 23 tokens, 16 experts of 1024 x 1000 (fp16): 17 +
 // 16 us, of which the weights take 11 + 8, routing 2, the join of the experts 4.
