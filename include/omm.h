@@ -257,7 +257,8 @@ int omm_grouped_matmul_check(const void* workspace, void* stream, int64_t* inval
  * OMM_ERR_UNSUPPORTED); sums, softmax statistics and intermediate results are
  * fp32.  Workspaces are device memory of the caller, 256-byte aligned, of at
  * least the stated size, used only during the call's kernels; they need no
- * preparation.
+ * preparation.  Fewer rows can need more (they are split further): a workspace
+ * for several row counts has the largest of their sizes.
  */
 
 /* ------------------------------------------------------------------------
