@@ -434,6 +434,7 @@ struct LpGradArgs {
 
 // dx[v] = gl ([v = target] - p) - gH p (ln p + H),  p = e^(x - lse)
 // One read and one write: 4096 rows of 131072 (bf16) in 380 us, 5.6 TB/s.
+template <int DT>
 struct GradRow {
     float gl, gh, H, lse;
     int t;
@@ -441,8 +442,9 @@ struct GradRow {
         // p = 0 below -200: the clamp keeps 0 * -inf (a masked logit) out
         const float l = x - lse, lc = fmaxf(l, -200.0f), b = l * kLog2e;
         float p = __builtin_amdgcn_exp2f(b);
-        // (what the rounding of b leaves of l: without it p would be off by |l| 2^-24)
-        p = fmaf(p, fmaf(fmaxf(b, -200.0f * kLog2e), -kLn2, lc), p);
+        // What the rounding of b leaves of l: without it p would be off by |l| 2^-24.
+        // Only a fp32 gradient shows it (131 rows of 55296 in bf16: 7.3 us with it, 6.8 without).
+        if constexpr (DT == 2) p = fmaf(p, fmaf(fmaxf(b, -200.0f * kLog2e), -kLn2, lc), p);
         float d = -p * fmaf(gh, lc + H, gl);
         return v == t ? d + gl : d;
     }
@@ -457,7 +459,7 @@ __global__ __launch_bounds__(NT) void logprobs_grad_kernel(LpGradArgs a) {
     const int v0 = min(a.V, c * a.chunk), v1 = min(a.V, v0 + a.chunk);
     const E* row = (const E*)a.logits + m * (int64_t)a.V;
     E* out = (E*)a.dlogits + m * (int64_t)a.V;
-    GradRow g;
+    GradRow<DT> g;
     const int64_t t = a.idx64 ? ((const int64_t*)a.targets)[m] : (int64_t)((const int32_t*)a.targets)[m];
     g.t = t >= 0 && t < a.V ? (int)t : -1;
     g.gl = g.t >= 0 ? a.g_logprobs[m] : 0.0f;
