@@ -23,14 +23,13 @@ namespace omm {
 namespace {
 
 // T[p, r] = scale[g] sum_k X[m, k] A[g, k, r], m the row at position p: a
-// workgroup a row, a wave an r.  fp16, for the tiles: the largest |T| of the row.
+// workgroup a row, a wave an r.
 template <int DT>
 __global__ __launch_bounds__(256) void lora_shrink_any_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t p = blockIdx.x, m = a.perm ? a.perm[p] : p, g = row_adapter(a, m);
     if (g < 0) return;
-    float most = 0.0f;
     const E* x = (const E*)a.X + m * a.K;
     const int64_t sk = a.trans ? 1 : a.R, sr = a.trans ? a.K : 1;
     for (int r = wave; r < a.R; r += 4) {
@@ -38,15 +37,7 @@ __global__ __launch_bounds__(256) void lora_shrink_any_kernel(LoraK a) {
         float acc = 0.0f;
         for (int64_t k = lane; k < a.K; k += 64) acc = fmaf(elem_f32<DT>(x[k]), elem_f32<DT>(w[k * sk]), acc);
         acc = wave_sum(acc);
-        if (a.scale) acc *= a.scale[g];
-        most = fmaxf(most, fabsf(acc));
-        if (lane == 0) a.T[p * a.R + r] = acc;
-    }
-    if (DT == 1 && a.tmax) {
-        __shared__ float red[4];
-        if (lane == 0) red[wave] = most;
-        __syncthreads();
-        if (threadIdx.x == 0) a.tmax[p] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        if (lane == 0) a.T[p * a.R + r] = a.scale ? acc * a.scale[g] : acc;
     }
 }
 

@@ -22,7 +22,10 @@ struct LoraK {
     float* part;     // (ceil(N / cw), splits, M, cw)
     uint32_t* done;  // finished workgroups of each cw columns
     int32_t* perm;   // (M) rows in the order of their adapters, or nullptr: as they come
-    float* tmax;     // largest |T| of each row and workgroup of its r (fp16)
+    // bf16, fp16 over sorted rows, instead of T: its parts (3, M, R up to a multiple of 8,
+    // zeros there), and (fp16) what a row's parts are multiplied by, for each 64 r
+    uint16_t* Tp;
+    float* undo;
 };
 
 // the adapter of row m, -1: none
@@ -47,7 +50,7 @@ __device__ __forceinline__ void row_group(LoraK& a, int z, int parts, int elem) 
 // Y = X W + C, C (M, N) of T (may be Y)
 hipError_t lora_add_dense(const LoraK& a, const void* C, int dt, hipStream_t s);
 
-// T (and fp16: tmax, if not nullptr) by elements, of any sizes
+// T by elements, of any sizes
 void lora_shrink_any(const LoraK& a, int dt, hipStream_t s);
 
 // whether lora_tile_kernel takes these operands

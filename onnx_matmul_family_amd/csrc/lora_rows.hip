@@ -5,11 +5,13 @@
 // that results do not depend on scheduling), which makes almost every block of
 // 16 rows one of a single adapter:
 //   lora_sort_kernel         the order
-//   lora_shrink_rows_kernel  T = scale X A in fp32, 16 rows a workgroup
+//   lora_shrink_rows_kernel  T = scale X A, 16 rows a workgroup, left as three
+//                            16-bit parts that add up to its fp32 values
 //   lora_tile_kernel         Y tiles on the LDS-DMA matrix core; as a tile
-//                            leaves, T B is added to its accumulators.  T's
-//                            rows enter as three 16-bit parts, so neither T
-//                            nor T B is rounded.
+//                            leaves, T B is added to its accumulators, part by
+//                            part, so neither T nor T B is rounded.
+// (T is split where it is computed.  Split again in every column tile, 3844 rows of
+// 512 x 4480, rank 8, trans 1, took 98 us in bf16 and 107 in fp16; now 73 and 76.)
 // Operands that the DMA cannot take (rows not 16-byte aligned) and fp32, with a
 // W too large for the streamed form (2 GiB and more):
 //   lora_expand_kernel       bias + T B into Y, to which the framework's dense
@@ -17,6 +19,8 @@
 // A block of rows that mixes adapters multiplies each one's B on its own and
 // adds it under a mask: a zero row times another adapter's infinity would be
 // NaN.
+#include <algorithm>
+
 #include "gemm16_core.hpp"
 #include "kernels.hpp"
 #include "lora_args.hpp"
@@ -36,7 +40,7 @@ __device__ __forceinline__ int row_of(const LoraK& a, int p) { return a.perm ? a
 // each wave counts its contiguous share of the rows per bin, a scan over (bin,
 // wave) gives every wave its place in every bin, and it writes its rows there.
 // 4096 rows: 8 us in runs of 9 bins, 11 us mixed over 17; the tiles
-// that use the order take 232.
+// that use the order take 208 and up.
 __global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int bins) {
     extern __shared__ int hist[];  // [wave][bin]
     __shared__ int wsum[kSortWaves];
@@ -87,8 +91,8 @@ __global__ __launch_bounds__(64 * kSortWaves) void lora_sort_kernel(LoraK a, int
 
 // T[p, r] = scale[g] sum_k X[m, k] A[g, k, r] of the 16 rows m at positions p0
 // .. p0 + 15 and 16 NF r: NW waves split K, A and the rows go from memory
-// to the matrix unit.  One pass for each adapter among the rows.
-// fp16: tmax[p][y] = max |T[p, r]| over the r of blockIdx.y (for the parts' scale).
+// to the matrix unit.  One pass for each adapter among the rows.  bf16 and fp16: the
+// parts of T, fp16 scaled by a power of two for the 16 NF r of the row.
 template <int DT, int TRANS, int NF, int NW>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_rows_kernel(LoraK a) {
     typedef typename elem_of<DT>::type E;
@@ -117,23 +121,40 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_rows_kernel(LoraK a) {
         for (int j = 0; j < NF; ++j) *(f32x4_t*)&red[(wave * NF + j) * kFragPad + lane * 4] = acc[j][0];
         __syncthreads();
         const float scale = a.scale ? a.scale[g] : 1.0f;
-        for (int o = tid; o < 16 * CW; o += 64 * NW) {
-            const int c = o % CW, row = o / CW;
-            if (!((in >> row) & 1) || c0 + c >= R) continue;
+        constexpr int NV = (16 * CW + 64 * NW - 1) / (64 * NW);  // values a thread
+        float v[NV];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int o = tid + n * 64 * NW, c = o % CW, row = o / CW;
+            v[n] = 0.0f;
+            if (row >= 16 || !((in >> row) & 1) || c0 + c >= R) continue;
             const int pos = cols_pos<DT, TRANS>(c0, c, R);
             const float* q = &red[(pos >> 4) * kFragPad + (((pos & 15) >> 2) * 16 + row) * 4 + (pos & 3)];
-            float v = 0.0f;
 #pragma unroll
-            for (int u = 0; u < NW; ++u) v += q[u * NF * kFragPad];
-            v *= scale;
-            a.T[(int64_t)(p0 + row) * R + c0 + c] = v;
-            if constexpr (DT == 1) atomicMax(&max_s[row], __float_as_uint(fabsf(v)));  // (NaN is the largest)
+            for (int u = 0; u < NW; ++u) v[n] += q[u * NF * kFragPad];
+            v[n] *= scale;
+            if constexpr (DT == 2) a.T[(int64_t)(p0 + row) * R + c0 + c] = v[n];
+            if constexpr (DT == 1) atomicMax(&max_s[row], __float_as_uint(fabsf(v[n])));  // (NaN is the largest)
+        }
+        if constexpr (DT == 1) __syncthreads();
+        if constexpr (DT < 2) {
+            const int rp = (R + 7) & ~7;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const int o = tid + n * 64 * NW, c = o % CW, row = o / CW;
+                if (row >= 16 || !((in >> row) & 1) || c0 + c >= rp) continue;
+                float w = v[n], none = 0.0f;
+                if constexpr (DT == 1) {
+                    const int e = split_exp(__uint_as_float(max_s[row]));
+                    w = split_raise<DT>(w * ldexpf(1.0f, e));
+                    if (c == 0) a.undo[(int64_t)(p0 + row) * gridDim.y + blockIdx.y] = ldexpf(1.0f, -e);
+                }
+                uint16_t* t = a.Tp + (int64_t)(p0 + row) * rp + c0 + c;
+#pragma unroll
+                for (int h = 0; h < kParts32; ++h) t[h * (a.M * rp)] = (uint16_t)split_pair<DT>(w, none);
+            }
         }
         if (todo) __syncthreads();
-    }
-    if constexpr (DT == 1) {
-        __syncthreads();
-        if (tid < 16 && p0 + tid < M) a.tmax[(int64_t)(p0 + tid) * gridDim.y + blockIdx.y] = __uint_as_float(max_s[tid]);
     }
 }
 
@@ -141,15 +162,34 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_rows_kernel(LoraK a) {
 __host__ __device__ inline int shrink_cols(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 __host__ __device__ inline int shrink_parts(int R) { return (R + shrink_cols(R) - 1) / shrink_cols(R); }
 
-// largest |T| of a position, and the power of two that takes it to [2^13, 2^14)
-__device__ __forceinline__ float row_max(const LoraK& a, int64_t p) {
-    const int n = shrink_parts(a.R);
-    float mx = 0.0f;
-    for (int b = 0; b < n; ++b) mx = fmaxf(mx, a.tmax[p * n + b]);
-    return mx;
-}
-__device__ __forceinline__ int scale_exp(float mx) {
-    return mx > 0.0f && mx < __builtin_inff() ? max(-100, min(100, 13 - ilogbf(mx))) : 0;
+// fp16: what the parts of position p's r from 64 b on are multiplied by
+__device__ __forceinline__ float row_undo(const LoraK& a, int64_t p, int b) { return a.undo[p * shrink_parts(a.R) + b]; }
+
+// T of up to 8 r -> its parts, a thread a position
+template <int DT>
+__global__ __launch_bounds__(256) void lora_split_kernel(LoraK a) {
+    const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (p >= a.M) return;
+    if (row_adapter(a, row_of(a, (int)p)) < 0) return;
+    float v[8], mx = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        v[r] = r < a.R ? a.T[p * a.R + r] : 0.0f;
+        mx = fmaxf(mx, fabsf(v[r]));
+    }
+    if constexpr (DT == 1) {
+        const int e = split_exp(mx);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = split_raise<DT>(v[r] * ldexpf(1.0f, e));
+        a.undo[p] = ldexpf(1.0f, -e);
+    }
+#pragma unroll
+    for (int h = 0; h < kParts32; ++h) {
+        u32x4_t t;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = split_pair<DT>(v[2 * i], v[2 * i + 1]);
+        *(u32x4_t*)(a.Tp + (h * a.M + p) * 8) = t;
+    }
 }
 
 // Y[m, n] = bias[n] + sum_r T[p, r] B[g, r, n], a wave 16 positions and 128 columns
@@ -164,13 +204,14 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
     if (pw >= M) return;
     const int p = (int)min(pw + i, (int64_t)M - 1), m = row_of(a, p);
     const int ad = (int)row_adapter(a, m);
-    StreamXf<DT, TRANS, 1> x;
-    x.p[0] = a.T + (int64_t)min(pw + tr, (int64_t)M - 1) * R + x.off(lane);
-    float undo = 1.0f;
-    if constexpr (DT == 1) {
-        const int e = ad >= 0 ? scale_exp(row_max(a, p)) : 0;
-        x.scale[0] = ldexpf(1.0f, e);
-        undo = ldexpf(1.0f, -e);
+    typename std::conditional<DT == 2, StreamX<2, TRANS, 1>, StreamXParts<DT, TRANS, 1>>::type x;
+    const int64_t xrow = min(pw + tr, (int64_t)M - 1);
+    if constexpr (DT == 2) {
+        x.p[0] = a.T + xrow * R + x.off(lane);
+    } else {
+        const int rp = (R + 7) & ~7;
+        x.p[0] = a.Tp + xrow * rp + x.off(lane);
+        x.plane = a.M * rp;
     }
     f32x4_t res[8] = {};
     for (uint32_t todo = (uint32_t)__ballot(ad >= 0) & 0xffffu; todo;) {
@@ -191,12 +232,17 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
                 w.p[0] = B + group_start<DT>(c0, 8 * i, N) + (int64_t)q * N;
             }
         }
-        f32x4_t acc[8][1] = {};
-        stream_run<DT, TRANS, 1>(w, x, 0, (R + kStep<DT> - 1) / kStep<DT>, R, acc, scratch[wave], lane);
+        // (fp16: 64 r at a time, which have a scale of their own)
+        const int steps = (R + kStep<DT> - 1) / kStep<DT>, span = DT == 1 ? 2 : steps;
+        for (int s0 = 0; s0 < steps; s0 += span) {
+            f32x4_t acc[8][1] = {};
+            stream_run<DT, TRANS, 1>(w, x, s0, min(steps, s0 + span), R, acc, scratch[wave], lane);
+            const float undo = DT == 1 && ad == g ? row_undo(a, p, s0 / 2) : 1.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) res[j][e] = ad == g ? acc[j][0][e] * undo : res[j][e];
+                for (int e = 0; e < 4; ++e) res[j][e] = ad == g ? fmaf(acc[j][0][e], undo, res[j][e]) : res[j][e];
+        }
     }
     if (pw + i >= M) return;
     E* y = (E*)a.Y + (int64_t)m * N;
@@ -222,17 +268,18 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraK a) {
 // BKM: W (N, K), B (G, N, R); else W (K, N), B (G, R, N).
 // TH: column fragments of a pass of the epilogue; fewer (4 of 8) leave the
 // registers to keep B's fragments of 64 r from block to block instead of 32.
-// 4096 x 4096 x 8192 with rank 32 (bf16): 232 us, 1.19 PFLOP/s; the K loop alone,
-// as the dense product runs it, takes 222 and up (it is bound by the matrix unit
-// under the chip's clock).
-template <int DT, bool BKM, int BT, int TH>
+// LONG: R over what is kept, B's fragments are loaded again for every block.
+// 4096 x 4096 x 8192 with rank 32 (bf16), called in turn with the dense product of
+// the same sizes: 208 to 218 us, 1.26 PFLOP/s and up; that one, which is the K loop,
+// 189 to 194 (both are bound by the matrix unit under the chip's clock).
+template <int DT, bool BKM, int BT, int TH, bool LONG>
 __global__ __launch_bounds__(NT, BT == 128 ? 2 : 1) void lora_tile_kernel(LoraK a, int tiles_m, int tiles_n) {
     constexpr int BM = BT, BN = BT, TM = BM / 32, TN = BN / 32;
     constexpr int STAGE = (BM + BN) * KSTEP * 2;
     __shared__ __attribute__((aligned(1024))) char smem0[STAGE];
     __shared__ __attribute__((aligned(1024))) char smem1[STAGE];
     __shared__ int row_s[BM], ad_s[BM];
-    __shared__ float max_s[DT == 1 ? BM : 1];
+    __shared__ float undo_s[DT == 1 ? BM : 1];  // (of the first 64 r)
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int w = xcd_remap((int)blockIdx.x, (int)gridDim.x);
@@ -244,7 +291,7 @@ __global__ __launch_bounds__(NT, BT == 128 ? 2 : 1) void lora_tile_kernel(LoraK 
         const int p = m0 + r, m = p < M ? row_of(a, p) : -1, ad = m < 0 ? -1 : (int)row_adapter(a, m);
         row_s[r] = m;
         ad_s[r] = ad;
-        if constexpr (DT == 1) max_s[r] = ad < 0 ? 0.0f : row_max(a, p);
+        if constexpr (DT == 1) undo_s[r] = ad < 0 || R == 0 ? 1.0f : row_undo(a, p, 0);
     }
     __syncthreads();
     GatherDma<BM> srcA;
@@ -273,7 +320,7 @@ __global__ __launch_bounds__(NT, BT == 128 ? 2 : 1) void lora_tile_kernel(LoraK 
     const int i16 = lane & 15, q = (lane >> 4) * 8, row0 = wm * (BM / 2), col0 = wn * (BN / 2);
     const uint16_t* Bp = (const uint16_t*)a.B;
     constexpr int HS = TH == 8 ? 1 : 2;
-    u32x4_t bf[HS][TH];  // B's fragments, kept from block to block where HS steps cover R
+    u32x4_t bf[LONG ? 1 : HS][TH];  // B's fragments
     int held = -1;
     // BKM = false: 32 r of 64 columns pass through LDS for the transposing read
     // (where no tile is staged, in the K loop's)
@@ -313,43 +360,43 @@ __global__ __launch_bounds__(NT, BT == 128 ? 2 : 1) void lora_tile_kernel(LoraK 
             }
         }
     };
-    auto t_row = [&](int i) { return a.T + (int64_t)min(m0 + row0 + 16 * i + i16, M - 1) * R + q; };
-    auto load_t = [&](u32x4_t (&raw)[2], const float* tp, int r0) {
-        const int n = max(0, min(8, R - r0 - q));
-        raw[0] = load16_first(tp + r0, n);
-        raw[1] = load16_first(tp + r0 + 4, n - 4);
+    const int rp = (R + 7) & ~7;
+    const int64_t plane = a.M * rp;
+    auto t_row = [&](int i) { return a.Tp + (int64_t)min(m0 + row0 + 16 * i + i16, M - 1) * rp + q; };
+    auto load_t = [&](u32x4_t (&part)[kParts32], const uint16_t* tp, int r0) {
+#pragma unroll
+        for (int h = 0; h < kParts32; ++h)
+            part[h] = r0 + q < rp ? *(const u32x4_t*)(tp + h * plane + r0) : u32x4_t{0, 0, 0, 0};
     };
-    u32x4_t ahead[2];  // the next block's first step of T
+    u32x4_t ahead[kParts32];  // the next block's first step of T
     load_t(ahead, t_row(0), 0);
     auto delta = [&](int i, int jh, f32x4_t (&d)[TH]) {
 #pragma unroll
         for (int j = 0; j < TH; ++j) d[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         const int ad = ad_s[row0 + 16 * i + i16];
-        const u32x4_t first[2] = {ahead[0], ahead[1]};
+        const u32x4_t first[kParts32] = {ahead[0], ahead[1], ahead[2]};
         load_t(ahead, t_row(i + 1 < TM ? i + 1 : 0), 0);
-        float scale = 1.0f, undo = 1.0f;
-        if constexpr (DT == 1) {
-            const int e = scale_exp(max_s[row0 + 16 * i + i16]);
-            scale = ldexpf(1.0f, e);
-            undo = ldexpf(1.0f, -e);
-        }
         for (uint32_t todo = (uint32_t)__ballot(ad >= 0) & 0xffffu; todo;) {
             const int g = __builtin_amdgcn_readlane(ad, __ffs(todo) - 1);
             todo &= ~(uint32_t)__ballot(ad == g);
             f32x4_t v[TH] = {};
             const auto step = [&](const u32x4_t (&f)[TH], int r0) {
-                u32x4_t raw[2] = {first[0], first[1]};
-                if (r0) load_t(raw, t_row(i), r0);
-                float left[8];
-                split_start<DT>(raw, scale, left);
+                u32x4_t part[kParts32] = {first[0], first[1], first[2]};
+                if (r0) load_t(part, t_row(i), r0);
 #pragma unroll
-                for (int h = 0; h < kParts32; ++h) {
-                    const u32x4_t part = split_next<DT>(left);
+                for (int h = 0; h < kParts32; ++h)
 #pragma unroll
-                    for (int j = 0; j < TH; ++j) v[j] = mfma16x16x32<DT>(f[j], part, v[j]);
-                }
+                    for (int j = 0; j < TH; ++j) v[j] = mfma16x16x32<DT>(f[j], part[h], v[j]);
             };
-            if (R <= 32 * HS) {
+            // adds the rows of this adapter; fp16: of 64 r, which have a scale of their own
+            const auto add = [&](float undo) {
+#pragma unroll
+                for (int j = 0; j < TH; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[j][e] = ad == g ? fmaf(v[j][e], undo, d[j][e]) : d[j][e];
+            };
+            const float undo = DT == 1 ? undo_s[row0 + 16 * i + i16] : 1.0f;
+            if constexpr (!LONG) {
                 if (held != g) {
 #pragma unroll
                     for (int h = 0; h < HS; ++h)
@@ -359,16 +406,22 @@ __global__ __launch_bounds__(NT, BT == 128 ? 2 : 1) void lora_tile_kernel(LoraK 
 #pragma unroll
                 for (int h = 0; h < HS; ++h)
                     if (32 * h < R) step(bf[h], 32 * h);
+#pragma unroll
+                for (int j = 0; j < TH; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[j][e] = ad == g ? (DT == 1 ? v[j][e] * undo : v[j][e]) : d[j][e];
             } else {
                 for (int r0 = 0; r0 < R; r0 += 32) {
                     load_b(bf[0], g, r0, jh);
                     step(bf[0], r0);
+                    if (DT == 1 && (r0 & 32) && r0 + 32 < R) {
+                        add(r0 < 64 ? undo : row_undo(a, min(m0 + row0 + 16 * i + i16, M - 1), r0 / 64));
+#pragma unroll
+                        for (int j = 0; j < TH; ++j) v[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
                 }
+                add(DT == 1 && R > 64 ? row_undo(a, min(m0 + row0 + 16 * i + i16, M - 1), (R - 1) / 64) : undo);
             }
-#pragma unroll
-            for (int j = 0; j < TH; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d[j][e] = ad == g ? v[j][e] * undo : d[j][e];
         }
     };
 
@@ -452,8 +505,12 @@ hipError_t rows_run(const LoraK& a, hipStream_t s) {
     if (a.perm && a.R > 0 && a.G > 0)
         lora_sort_kernel<<<1, 64 * kSortWaves, kSortWaves * (a.G + 1) * sizeof(int), s>>>(a, (int)a.G + 1);
     if (a.R > 0 && a.G > 0) {
-        if (!TRANS && a.R < 8) lora_shrink_any(a, DT, s);  // (no group of 8 columns of A)
-        else shrink<DT, TRANS>(a, s);
+        if (DT < 2 && !TRANS && a.R < 8) {  // (no group of 8 columns of A)
+            lora_shrink_any(a, DT, s);
+            if constexpr (DT < 2) lora_split_kernel<DT><<<dim3((unsigned)((a.M + 255) / 256)), 256, 0, s>>>(a);
+        } else {
+            shrink<DT, TRANS>(a, s);
+        }
     }
     if constexpr (DT < 2) {
         if (lora_tiles_ok(a, DT)) {
@@ -461,12 +518,16 @@ hipError_t rows_run(const LoraK& a, hipStream_t s) {
             if (big >= 256) {
                 const int tm = (int)((a.M + 255) / 256), tn = (int)((a.N + 255) / 256);
                 log_choice("lora_matmul: 256x256 tiles over sorted rows");
-                if (a.R <= 32) lora_tile_kernel<DT, TRANS != 0, 256, 8><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
-                else lora_tile_kernel<DT, TRANS != 0, 256, 4><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
+                const dim3 grid((unsigned)(tm * tn));
+                if (a.R <= 32) lora_tile_kernel<DT, TRANS != 0, 256, 8, false><<<grid, NT, 0, s>>>(a, tm, tn);
+                else if (a.R <= 64) lora_tile_kernel<DT, TRANS != 0, 256, 4, false><<<grid, NT, 0, s>>>(a, tm, tn);
+                else lora_tile_kernel<DT, TRANS != 0, 256, 4, true><<<grid, NT, 0, s>>>(a, tm, tn);
             } else {
                 const int tm = (int)((a.M + 127) / 128), tn = (int)((a.N + 127) / 128);
                 log_choice("lora_matmul: 128x128 tiles over sorted rows");
-                lora_tile_kernel<DT, TRANS != 0, 128, 4><<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, tm, tn);
+                const dim3 grid((unsigned)(tm * tn));
+                if (a.R <= 64) lora_tile_kernel<DT, TRANS != 0, 128, 4, false><<<grid, NT, 0, s>>>(a, tm, tn);
+                else lora_tile_kernel<DT, TRANS != 0, 128, 4, true><<<grid, NT, 0, s>>>(a, tm, tn);
             }
             return hipGetLastError();
         }
@@ -493,17 +554,21 @@ bool lora_rows_ok(int64_t K, int64_t N, int64_t R, int64_t G) {
            K < (1 << 30) && N < (1 << 30) && G < (1LL << 31) - 1;
 }
 
+// the order of the rows, the parts' factors, T or its parts, and T where it is split by a kernel of its own
 size_t lora_rows_workspace_bytes(int64_t M, int64_t R) {
-    return align256((size_t)M * 4) + align256((size_t)M * shrink_parts((int)R) * 4) + align256((size_t)M * R * 4);
+    const size_t whole = align256((size_t)M * R * 4), parts = align256((size_t)kParts32 * M * ((R + 7) / 8 * 8) * 2);
+    return align256((size_t)M * 4) + align256((size_t)M * shrink_parts((int)R) * 4) +
+           std::max(whole, parts + (R < 8 ? whole : 0));
 }
 
 hipError_t launch_lora_rows(LoraK a, int dt, void* ws, hipStream_t s) {
     char* w = (char*)ws;
     a.perm = a.G < 1024 ? (int32_t*)w : nullptr;  // (more adapters than the sort has counters for: rows as they come)
     w += align256((size_t)a.M * 4);
-    a.tmax = (float*)w;
+    a.undo = (float*)w;
     w += align256((size_t)a.M * shrink_parts(a.R) * 4);
-    a.T = (float*)w;
+    a.Tp = (uint16_t*)w;
+    a.T = dt == 2 ? (float*)w : (float*)(w + align256((size_t)kParts32 * a.M * ((a.R + 7) / 8 * 8) * 2));
     if (a.R == 0 || a.G == 0) a.perm = nullptr;
     switch (dt * 2 + a.trans) {
         case 0: return rows_run<0, 0>(a, s);

@@ -519,8 +519,7 @@ __device__ __forceinline__ void down_rows(const LayerArgs& a, const ExpertList& 
             const int p = pair_of(r.pair[min(t0 + 16 * g + i, r.n - 1)]);
             float mx = 0.0f;
             for (int b = s0 * 32 / a.hw; b < min(slabs, (s1 * 32 + a.hw - 1) / a.hw); ++b) mx = fmaxf(mx, a.hmax[(int64_t)p * slabs + b]);
-            int ex = 0;
-            if (mx > 0.0f && mx < __builtin_inff()) ex = max(-100, min(100, 13 - ilogbf(mx)));
+            const int ex = split_exp(mx);
             x.scale[g] = ldexpf(1.0f, ex);
             undo[g] = ldexpf(1.0f, -ex);
         }

@@ -211,45 +211,47 @@ template <int DT>
 __device__ __forceinline__ float at_least(float v, float z) {
     return copysignf(fmaxf(fabsf(v), fminf(fabsf(z), kLeastPart<DT>)), z);
 }
-// the next part of the values, which keep what is left of them
+// what is less than the least part is raised to it (fp16, whose rows are scaled)
 template <int DT>
-__device__ __forceinline__ u32x4_t split_next(float (&v)[8]) {
-    u32x4_t p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float &a = v[2 * i], &b = v[2 * i + 1], ah, bh;
-        if constexpr (DT == 1) {
-            p[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
-            ah = from_bits<DT>((uint16_t)p[i]);
-            bh = from_bits<DT>((uint16_t)(p[i] >> 16));
-        } else {
-            const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-            p[i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
-            ah = __uint_as_float(ua & 0xffff0000u);
-            bh = __uint_as_float(ub & 0xffff0000u);
-        }
-        a = at_least<DT>(a - ah, ah);
-        b = at_least<DT>(b - bh, bh);
+__device__ __forceinline__ float split_raise(float v) {
+    if (DT == 1 && fabsf(v) < kLeastPart<DT> && v != 0.0f) return copysignf(kLeastPart<DT>, v);
+    return v;
+}
+// the next part of two values (a in the low half), which keep what is left of them
+template <int DT>
+__device__ __forceinline__ uint32_t split_pair(float& a, float& b) {
+    uint32_t p;
+    float ah, bh;
+    if constexpr (DT == 1) {
+        p = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+        ah = from_bits<DT>((uint16_t)p);
+        bh = from_bits<DT>((uint16_t)(p >> 16));
+    } else {
+        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+        p = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+        ah = __uint_as_float(ua & 0xffff0000u);
+        bh = __uint_as_float(ub & 0xffff0000u);
     }
+    a = at_least<DT>(a - ah, ah);
+    b = at_least<DT>(b - bh, bh);
     return p;
 }
 template <int DT>
-__device__ __forceinline__ void split_start(const u32x4_t (&r)[2], float scale, float (&v)[8]) {
+__device__ __forceinline__ void split_parts(const u32x4_t (&r)[2], float scale, u32x4_t (&p)[kParts32]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = __uint_as_float(r[i >> 2][i & 3]);
+    for (int i = 0; i < 4; ++i) {
+        float a = __uint_as_float(r[i >> 1][(i & 1) * 2]), b = __uint_as_float(r[i >> 1][(i & 1) * 2 + 1]);
         if constexpr (DT == 1) {
-            v[i] *= scale;
-            if (fabsf(v[i]) < kLeastPart<DT> && v[i] != 0.0f) v[i] = copysignf(kLeastPart<DT>, v[i]);
+            a = split_raise<DT>(a * scale);
+            b = split_raise<DT>(b * scale);
         }
+#pragma unroll
+        for (int h = 0; h < kParts32; ++h) p[h][i] = split_pair<DT>(a, b);
     }
 }
-template <int DT>
-__device__ __forceinline__ void split_parts(const u32x4_t (&r)[2], float scale, u32x4_t (&p)[kParts32]) {
-    float v[8];
-    split_start<DT>(r, scale, v);
-#pragma unroll
-    for (int h = 0; h < kParts32; ++h) p[h] = split_next<DT>(v);
+// the power of two that takes a row's largest value to [2^13, 2^14) (fp16)
+__device__ __forceinline__ int split_exp(float mx) {
+    return mx > 0.0f && mx < __builtin_inff() ? max(-100, min(100, 13 - ilogbf(mx))) : 0;
 }
 
 // fp32 rows against bf16 / fp16 weights, as the sum of three 16-bit parts: three
@@ -301,6 +303,41 @@ struct StreamX32 {
             }
         }
         if constexpr (TRANS) __builtin_amdgcn_wave_barrier();
+    }
+};
+// The same from rows that are split already: p in the first part's rows, the next
+// parts `plane` elements further on each.
+template <int DT, int TRANS, int NG>
+struct StreamXParts {
+    static constexpr int RAW = kParts32, PARTS = kParts32;
+    typedef typename elem_of<DT>::type E;
+    const E* p[NG];  // row x_row, plus off
+    int64_t plane;
+    __device__ __forceinline__ static int off(int lane) { return x_off<DT, TRANS>(lane); }
+    __device__ __forceinline__ void load(u32x4_t (&r)[NG][RAW], int kb) const {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int h = 0; h < RAW; ++h) r[g][h] = load16(p[g] + h * plane + kb);
+    }
+    __device__ __forceinline__ void tail(u32x4_t (&r)[NG][RAW], int kb, int kn, int lane) const {
+        const int n = max(0, min(kQ<DT>, kn - kb - off(lane)));
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int h = 0; h < RAW; ++h) r[g][h] = load16_first(p[g] + h * plane + kb, n);
+    }
+    __device__ __forceinline__ void operands(const u32x4_t (&r)[NG][RAW], u32x4_t (&o)[NG][PARTS], u32x4_t* scratch,
+                                             int lane) const {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            u32x4_t v[PARTS];
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) v[h] = r[g][h];
+            if constexpr (TRANS) row_tile<PARTS>(v, scratch, lane);
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) o[g][h] = v[h];
+        }
     }
 };
 template <int DT, int TRANS, int NG>
