@@ -294,7 +294,7 @@ int omm_lora_matmul(const omm_tensor* X, const omm_tensor* W, const omm_tensor* 
  *   renormalize != 0.
  *   A logit of -inf excludes its expert: it is selected after every other one
  *   (lower index first) with weight 0; a token whose logits are all -inf gets
- *   weights 0.  A NaN logit ranks first and makes the token's weights NaN.
+ *   weights 0.  A NaN logit ranks first; it or a +inf makes the token's weights NaN.
  *   E <= OMM_MOE_MAX_EXPERTS, top_k <= min(E, OMM_MOE_MAX_TOP_K).
  * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE (also top_k outside
  * [0, E]), OMM_ERR_UNSUPPORTED (beyond the limits).
