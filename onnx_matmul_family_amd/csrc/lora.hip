@@ -442,9 +442,9 @@ int64_t piece_rows(int64_t M, int64_t most) {
 // of the tiles over sorted rows, or of the dense product after the adapters'
 // term where there are no tiles.  us a call, streamed / other (bf16, rank 16):
 //   K, N (trans)         M = 256     M = 512      M = 1024     M = 2048
-//   4096, 1024 (1)     18 /  62     32 /  64     58 /  63    109 /  67
-//   4096, 4096 (1)     32 /  67     58 /  64    108 /  66    208 /  82
-//   4096, 8192 (1)     57 /  68    107 /  65    205 /  79    403 / 129
+//   4096, 1024 (1)     17 /  48     32 /  58     58 /  59    107 /  61
+//   4096, 4096 (1)     31 /  58     58 /  59    110 /  62    208 /  78
+//   4096, 8192 (1)     55 /  60    112 /  61    205 /  76    403 / 120
 //   1175, 3329 (1)     35 / 133     67 / 188    124 / 180    222 / 218   (no tiles)
 //   4000, 8190 (0)     47 / 423     85 / 427    161 / 605    312 / 1174  (no tiles)
 bool stream_ahead(int64_t M, int64_t K, int64_t N, bool tiles) {
