@@ -20,6 +20,13 @@
  *   omm_token_logprobs   log probabilities of given tokens, entropy and top
  *                        alternatives; omm_token_logprobs_grad its gradient.
  *
+ * And those that train, balance and quantise the products' weights:
+ *   omm_quantize_rows    int8 with a scale for each row, from the data.
+ *   omm_int8_matmul      8-bit product with a scale for each token and channel.
+ *   omm_moe_balance      per-expert counts, balance and z losses of the router;
+ *   omm_moe_route_grad   the gradient of the router's logits.
+ *   omm_orthogonalize    an update orthogonalised by Newton-Schulz products.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Tensors are dense and row-major (the last dim is contiguous), described by
@@ -367,6 +374,111 @@ int omm_token_logprobs(const omm_tensor* logits, const omm_tensor* targets, int 
 int omm_token_logprobs_grad(const omm_tensor* logits, const omm_tensor* targets, const omm_tensor* lse,
                             const omm_tensor* entropy, const omm_tensor* grad_logprobs,
                             const omm_tensor* grad_entropy, omm_tensor* grad_logits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Training and quantising.  T, fp32 sums and workspaces as for the decode-side
+ * operators above.
+ */
+
+/* ------------------------------------------------------------------------
+ * Rows to int8 with a scale each:
+ *     amax = max_k |X[m, k]|,  scale[m] = amax / 127,  Q[m, k] = 127 X[m, k] / amax
+ * the latter to the nearest integer, ties to even, of the exact quotient.
+ *   X (M, K) of T; Q (M, K) OMM_I8 (-127 .. 127); scale (M) OMM_F32.
+ *   For activations a row is a token, for weights (N, K) an output channel.
+ *   A row of zeros has scale 0; a row that holds a NaN or an infinity has scale
+ *   NaN and values 0, so it makes its own results NaN and no others.
+ * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE, OMM_ERR_UNSUPPORTED.
+ */
+int omm_quantize_rows(const omm_tensor* X, omm_tensor* Q, omm_tensor* scale, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Product in 8-bit integers with a scale for each token and channel:
+ *     Y[m, n] = a_scale[m] b_scale[n] sum_k a[m, k] b[n, k]  (+ bias[n])
+ *   a (M, K) OMM_I8 with a_scale (M) OMM_F32; or a of any T, a_scale NULL: its
+ *   rows are quantised by the call as omm_quantize_rows does (workspace).
+ *   b (N, K) OMM_I8 (as linear layers store it) with b_scale (N) OMM_F32;
+ *   bias (N) of Y's type or NULL; Y (M, N) of any T, whatever a's.
+ *   The sum is exact (32-bit integers; K <= OMM_INT8_MAX_K, all of -128 .. 127
+ *   allowed), converted to fp32, times a_scale, times b_scale, plus bias, rounded
+ *   once to T.
+ *   A workspace is needed for an a of T only (0 bytes otherwise, NULL allowed).
+ * Errors: OMM_ERR_NULL (also an int8 a without a_scale), OMM_ERR_DTYPE,
+ * OMM_ERR_SHAPE (also a_scale with an a of T), OMM_ERR_UNSUPPORTED, OMM_ERR_WORKSPACE.
+ */
+#define OMM_INT8_MAX_K 131071
+size_t omm_int8_matmul_workspace_size(int64_t M, int64_t K, int64_t N, int32_t a_dtype);
+int omm_int8_matmul(const omm_tensor* a, const omm_tensor* a_scale, const omm_tensor* b, const omm_tensor* b_scale,
+                    const omm_tensor* bias, omm_tensor* Y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The router's load: how often each expert was selected, and the two losses that
+ * keep the router even and its logits small.  With p[m] = softmax(logits[m]) and
+ * n the number of tokens counted:
+ *     counts[e] = number of (m, s) with indices[m, s] = e
+ *     losses[0] = E sum_e (counts[e] / sum counts) (1 / n) sum_m p[m, e]
+ *     losses[1] = (1 / n) sum_m lse[m]^2,  lse[m] = ln sum_e e^logits[m, e]
+ *     tokens[0] = n
+ *   logits (M, E) of T; indices (M, top_k) OMM_I32 / OMM_I64 as omm_moe_route
+ *   leaves them; token_mask (M) OMM_U8 or NULL: tokens of 0 (padding) are left
+ *   out of everything, whatever their logits hold.
+ *   losses (2) OMM_F32; counts (E), tokens (1) OMM_I32.
+ *   An index outside [0, E) is not counted; every other one is, that of an
+ *   excluded expert (logit -inf) too.  A token whose logits are all -inf has
+ *   p = 0 and lse = 0.  A NaN or +inf logit makes the losses NaN (not the counts).
+ *   No token: losses 0; no selection: losses[0] = 0.
+ *   The same inputs give the same bits.  E <= OMM_MOE_MAX_EXPERTS, top_k <= OMM_MOE_MAX_TOP_K.
+ * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE (also E = 0), OMM_ERR_UNSUPPORTED, OMM_ERR_WORKSPACE.
+ */
+size_t omm_moe_balance_workspace_size(int64_t M, int64_t E);
+int omm_moe_balance(const omm_tensor* logits, const omm_tensor* indices, const omm_tensor* token_mask,
+                    omm_tensor* losses, omm_tensor* counts, omm_tensor* tokens, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* The gradient with respect to the router's logits of all that reads them: the
+ * weights of omm_moe_route (grad_weights, NULL: none) and the losses of
+ * omm_moe_balance (grad_losses, NULL: none; counts and tokens as that call left
+ * them, or summed over several processes' batches).  The selections and the
+ * counts are constants.  With f[e] = counts[e] / sum counts:
+ *     grad_logits[m, e] = grad_losses[0] (E / n) p[e] (f[e] - sum_j f[j] p[j])
+ *                       + grad_losses[1] (2 / n) lse p[e]  +  R[e]
+ *     R[e] = sum_s w[s] ([e = indices[m, s]] - p[e]) grad_weights[m, s]          (renormalize = 0)
+ *     R[e] = sum_s w[s] [e = indices[m, s]] (grad_weights[m, s] - sum_j w[j] grad_weights[m, j])   (else)
+ * w the weights as omm_moe_route gives them for indices.
+ *   grad_weights (M, top_k), grad_losses (2) OMM_F32; grad_logits (M, E) of T may
+ *   be the logits tensor itself.  token_mask as above: a token of 0 gets gradient 0,
+ *   and so does one whose logits are all -inf.  An index outside [0, E) adds nothing.
+ *   A NaN or +inf logit makes its own token's gradient NaN.
+ * Errors: OMM_ERR_NULL (also grad_losses without counts or tokens),
+ * OMM_ERR_DTYPE, OMM_ERR_SHAPE, OMM_ERR_UNSUPPORTED.
+ */
+int omm_moe_route_grad(const omm_tensor* logits, const omm_tensor* indices, const omm_tensor* grad_weights,
+                       int renormalize, const omm_tensor* token_mask, const omm_tensor* counts,
+                       const omm_tensor* tokens, const omm_tensor* grad_losses, omm_tensor* grad_logits,
+                       void* stream);
+
+/* ------------------------------------------------------------------------
+ * An update with its singular values brought near 1, by Newton-Schulz products
+ * (what the Muon optimiser does to the momentum of a weight matrix):
+ *     X = G / |G|  (Frobenius norm);  `steps` times:
+ *     A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
+ *   (for more rows than columns the same polynomial with A = X^T X on the right.)
+ *   G, out (m, n) or (batch, m, n) of T, each matrix of a batch on its own; out
+ *   may be G itself.  5 steps are usual; singular values then lie in about 0.7 .. 1.2
+ *   (those above 1/500 of |G|).
+ *   The products are exact to about 22 bits of their operands with fp32 sums,
+ *   whatever T; one rounding to T at the end.
+ *   A matrix of zeros gives zeros; one that holds a NaN or an infinity gives NaN
+ *   everywhere, and leaves the others of its batch alone.
+ *   1 <= steps <= OMM_ORTHOGONALIZE_MAX_STEPS; m, n <= OMM_ORTHOGONALIZE_MAX_SIDE.
+ * Errors: OMM_ERR_NULL, OMM_ERR_DTYPE, OMM_ERR_SHAPE, OMM_ERR_UNSUPPORTED, OMM_ERR_WORKSPACE.
+ */
+#define OMM_ORTHOGONALIZE_MAX_STEPS 64
+#define OMM_ORTHOGONALIZE_MAX_SIDE 65536
+#define OMM_ORTHOGONALIZE_MAX_BATCH 65535
+size_t omm_orthogonalize_workspace_size(int64_t batch, int64_t m, int64_t n);
+int omm_orthogonalize(const omm_tensor* G, int steps, omm_tensor* out, void* workspace, size_t workspace_bytes,
+                      void* stream);
 
 #ifdef __cplusplus
 }

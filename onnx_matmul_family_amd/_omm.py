@@ -74,6 +74,17 @@ def lib():
         L.omm_token_logprobs_workspace_size.argtypes = [i64] * 3
         L.omm_token_logprobs.argtypes = [vp, vp, ci, vp, vp, vp, vp, vp, vp, sz, vp]
         L.omm_token_logprobs_grad.argtypes = [vp] * 8
+        L.omm_quantize_rows.argtypes = [vp] * 4
+        L.omm_int8_matmul_workspace_size.restype = sz
+        L.omm_int8_matmul_workspace_size.argtypes = [i64] * 3 + [ctypes.c_int32]
+        L.omm_int8_matmul.argtypes = [vp] * 7 + [sz, vp]
+        L.omm_moe_balance_workspace_size.restype = sz
+        L.omm_moe_balance_workspace_size.argtypes = [i64] * 2
+        L.omm_moe_balance.argtypes = [vp] * 7 + [sz, vp]
+        L.omm_moe_route_grad.argtypes = [vp, vp, vp, ci, vp, vp, vp, vp, vp, vp]
+        L.omm_orthogonalize_workspace_size.restype = sz
+        L.omm_orthogonalize_workspace_size.argtypes = [i64] * 3
+        L.omm_orthogonalize.argtypes = [vp, ci, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -265,7 +276,8 @@ def _on(stream, f, *args):
     with torch.cuda.stream(stream):
         out = f(*args)
     for t in out if isinstance(out, tuple) else (out,):
-        t.record_stream(outer)
+        if t is not None:
+            t.record_stream(outer)
     return out
 
 
@@ -336,3 +348,77 @@ def token_logprobs_grad(logits, targets, lse, grad_logprobs, entropy=None, grad_
         return _on(stream, token_logprobs_grad, logits, targets, lse, grad_logprobs, entropy, grad_entropy, grad_logits)
     return (_native or native()).token_logprobs_grad(logits, targets, lse, entropy, grad_logprobs, grad_entropy,
                                                      grad_logits)
+
+
+# ---------------------------------------------------------------- training and quantising
+
+def quantize_rows(X, Q=None, scale=None, stream=None):
+    """Rows to int8 with a scale each: scale[m] = max|X[m]| / 127, Q[m, k] = 127 X[m, k] / max|X[m]| to the
+    nearest integer (ties to even).  Rows are tokens, or the output channels of weights (N, K).
+    Returns (Q, scale)."""
+    if stream is not None:
+        return _on(stream, quantize_rows, X, Q, scale)
+    return (_native or native()).quantize_rows(X, Q, scale)
+
+
+def int8_matmul_workspace_size(M, K, N, dtype):
+    """dtype: of a (torch.int8: 0 bytes)."""
+    return int(lib().omm_int8_matmul_workspace_size(int(M), int(K), int(N), _DT[dtype]))
+
+
+def int8_matmul(a, b, b_scale, a_scale=None, bias=None, dtype=None, Y=None, workspace=None, stream=None):
+    """Y[m, n] = a_scale[m] * b_scale[n] * sum_k a[m, k] b[n, k] (+ bias[n]), the sum exact in integers.
+
+    b (N, K) int8 with b_scale (N) float32, as quantize_rows gives them for a linear layer's weights.
+    a (M, K) int8 with a_scale (M); or of a floating type without a_scale: quantised by the call.
+    dtype: of Y, by default a's (int8 a: bias's, or bfloat16).  Returns (Y, workspace); the workspace is None
+    for an int8 a."""
+    if stream is not None:
+        return _on(stream, int8_matmul, a, b, b_scale, a_scale, bias, dtype, Y, workspace)
+    if dtype is None:
+        if Y is not None:
+            dtype = Y.dtype
+        elif a.dtype != torch.int8:
+            dtype = a.dtype
+        else:
+            dtype = bias.dtype if bias is not None else torch.bfloat16
+    return (_native or native()).int8_matmul(a, a_scale, b, b_scale, bias, _DT.get(dtype, -1), Y, workspace)
+
+
+def moe_balance_workspace_size(M, E):
+    return int(lib().omm_moe_balance_workspace_size(int(M), int(E)))
+
+
+def moe_balance(logits, indices, token_mask=None, workspace=None, stream=None):
+    """The router's load.  Returns (losses, counts, tokens): fp32 (2), the balance loss E sum_e f[e] mean_m p[m, e]
+    (f the experts' shares of the selections) and the z loss mean_m logsumexp(logits[m])^2; int32 (E), the
+    selections of each expert; int32 (1), the tokens counted.  token_mask (M), bool or uint8: padding is 0.
+    No autograd graph is recorded: for the gradient call moe_route_grad with counts and tokens."""
+    if stream is not None:
+        return _on(stream, moe_balance, logits, indices, token_mask, workspace)
+    return (_native or native()).moe_balance(logits, indices, token_mask, workspace)
+
+
+def moe_route_grad(logits, indices, grad_weights=None, renormalize=True, token_mask=None, counts=None, tokens=None,
+                   grad_losses=None, grad_logits=None, stream=None):
+    """Gradient with respect to the router's logits of moe_route's weights (grad_weights, as moe_route's
+    renormalize) and of moe_balance's losses (grad_losses (2), with its counts and tokens).
+    grad_logits may be the logits tensor itself."""
+    if stream is not None:
+        return _on(stream, moe_route_grad, logits, indices, grad_weights, renormalize, token_mask, counts, tokens,
+                   grad_losses, grad_logits)
+    return (_native or native()).moe_route_grad(logits, indices, grad_weights, int(renormalize), token_mask, counts,
+                                                tokens, grad_losses, grad_logits)
+
+
+def orthogonalize_workspace_size(batch, m, n):
+    return int(lib().omm_orthogonalize_workspace_size(int(batch), int(m), int(n)))
+
+
+def orthogonalize(G, steps=5, out=None, workspace=None, stream=None):
+    """G (m, n), or a batch (b, m, n), with its singular values brought near 1 by Newton-Schulz steps:
+    X = G / |G|, then X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X with A = X X^T.  out may be G itself.
+    Returns (out, workspace)."""
+    if stream is not None:
+        return _on(stream, orthogonalize, G, steps, out, workspace)
+    return (_native or native()).orthogonalize(G, steps, out, workspace)

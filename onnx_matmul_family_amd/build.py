@@ -23,7 +23,8 @@ NATIVE = os.path.join(HERE, "_native.so")
 BUILD = os.path.join(HERE, "_build")
 
 SOURCES = ["api.cpp", "dense16.hip", "dense_f32.hip", "dense_f64.hip", "qlinear.hip", "grouped.hip",
-           "moe.hip", "lora.hip", "lora_rows.hip", "token_logprobs.hip"]
+           "moe.hip", "lora.hip", "lora_rows.hip", "token_logprobs.hip", "int8.hip",
+           "moe_balance.hip", "orthogonal.hip"]
 COMMON = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-I", os.path.join(HERE, "..", "include")]

@@ -943,3 +943,178 @@ int omm_token_logprobs_grad(const omm_tensor* logits, const omm_tensor* targets,
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ training and quantising
+
+extern "C" {
+
+int omm_quantize_rows(const omm_tensor* X, omm_tensor* Q, omm_tensor* scale, void* stream) {
+    int rc, kind;
+    for (const omm_tensor* t : {X, (const omm_tensor*)Q, (const omm_tensor*)scale})
+        if ((rc = check_tensor(t))) return rc;
+    if ((rc = float_kind(X->dtype, &kind))) return rc;
+    if (Q->dtype != OMM_I8 || scale->dtype != OMM_F32) return OMM_ERR_DTYPE;
+    if (X->ndim != 2) return OMM_ERR_SHAPE;
+    const int64_t M = X->shape[0], K = X->shape[1];
+    if (!has_shape(Q, 2, M, K) || !has_shape(scale, 1, M)) return OMM_ERR_SHAPE;
+    if (M == 0) return OMM_OK;
+    if (K > kMaxIndex - 65536) return OMM_ERR_UNSUPPORTED;
+    return hip_status(omm::launch_quantize_rows(X->data, (int8_t*)Q->data, (float*)scale->data, M, K, kind,
+                                                (hipStream_t)stream));
+}
+
+size_t omm_int8_matmul_workspace_size(int64_t M, int64_t K, int64_t N, int32_t a_dtype) {
+    int kind;
+    if (M <= 0 || K < 0 || N <= 0 || K > OMM_INT8_MAX_K || (a_dtype != OMM_I8 && float_kind(a_dtype, &kind)) ||
+        M > (int64_t)1 << 40)
+        return 0;
+    return omm::int8_matmul_workspace_bytes(M, K, N, a_dtype != OMM_I8);
+}
+
+int omm_int8_matmul(const omm_tensor* a, const omm_tensor* a_scale, const omm_tensor* b, const omm_tensor* b_scale,
+                    const omm_tensor* bias, omm_tensor* Y, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc, kind, a_kind = -1;
+    for (const omm_tensor* t : {a, b, b_scale, (const omm_tensor*)Y})
+        if ((rc = check_tensor(t))) return rc;
+    if (bias && (rc = check_tensor(bias))) return rc;
+    if (a->dtype == OMM_I8 && !a_scale) return OMM_ERR_NULL;
+    if (a->dtype != OMM_I8 && (rc = float_kind(a->dtype, &a_kind))) return rc;
+    if (b->dtype != OMM_I8 || b_scale->dtype != OMM_F32) return OMM_ERR_DTYPE;
+    if ((rc = float_kind(Y->dtype, &kind))) return rc;
+    if (bias && bias->dtype != Y->dtype) return OMM_ERR_DTYPE;
+    if (a->ndim != 2 || b->ndim != 2 || b->shape[1] != a->shape[1]) return OMM_ERR_SHAPE;
+    const int64_t M = a->shape[0], K = a->shape[1], N = b->shape[0];
+    if (a_scale && a->dtype != OMM_I8) return OMM_ERR_SHAPE;  // (a is not quantised yet)
+    if ((rc = check_f32_vec(a_scale, M)) || (rc = check_f32_vec(b_scale, N))) return rc;
+    if ((bias && !has_shape(bias, 1, N)) || !has_shape(Y, 2, M, N)) return OMM_ERR_SHAPE;
+    if (M == 0 || N == 0) return OMM_OK;
+    if (K > OMM_INT8_MAX_K || M > kMaxIndex || N > kMaxIndex || blocks(M, 128) * blocks(N, 128) > kMaxBlocks)
+        return OMM_ERR_UNSUPPORTED;
+    if ((rc = check_workspace(workspace, workspace_bytes, omm::int8_matmul_workspace_bytes(M, K, N, a_kind >= 0))))
+        return rc;
+    omm::Int8Args x;
+    x.a = a->data;
+    x.a_kind = a_kind;
+    x.a_scale = a_scale ? (const float*)a_scale->data : nullptr;
+    x.b = b->data;
+    x.b_scale = (const float*)b_scale->data;
+    x.bias = bias ? bias->data : nullptr;
+    x.Y = Y->data;
+    x.M = M;
+    x.N = N;
+    x.K = K;
+    return hip_status(omm::launch_int8_matmul(x, kind, workspace, (hipStream_t)stream));
+}
+
+size_t omm_moe_balance_workspace_size(int64_t M, int64_t E) {
+    if (M <= 0 || E <= 0 || E > OMM_MOE_MAX_EXPERTS) return 0;
+    return omm::moe_balance_workspace_bytes(M, E);
+}
+
+// what the balance and the gradient have in common
+static int check_router(const omm_tensor* logits, const omm_tensor* indices, const omm_tensor* token_mask,
+                        const omm_tensor* counts, const omm_tensor* tokens, const omm_tensor* losses, int* kind) {
+    int rc;
+    if ((rc = check_tensor(logits)) || (rc = check_tensor(indices))) return rc;
+    for (const omm_tensor* t : {token_mask, counts, tokens, losses})
+        if (t && (rc = check_tensor(t))) return rc;
+    if ((rc = float_kind(logits->dtype, kind))) return rc;
+    if (!is_index(indices) || (token_mask && token_mask->dtype != OMM_U8)) return OMM_ERR_DTYPE;
+    if ((counts && counts->dtype != OMM_I32) || (tokens && tokens->dtype != OMM_I32)) return OMM_ERR_DTYPE;
+    if (losses && losses->dtype != OMM_F32) return OMM_ERR_DTYPE;
+    if (logits->ndim != 2 || indices->ndim != 2) return OMM_ERR_SHAPE;
+    const int64_t M = logits->shape[0], E = logits->shape[1], k = indices->shape[1];
+    if (E < 1 || indices->shape[0] != M || (token_mask && !has_shape(token_mask, 1, M))) return OMM_ERR_SHAPE;
+    if ((counts && !has_shape(counts, 1, E)) || (tokens && !has_shape(tokens, 1, 1))) return OMM_ERR_SHAPE;
+    if (losses && !has_shape(losses, 1, 2)) return OMM_ERR_SHAPE;
+    if (E > OMM_MOE_MAX_EXPERTS || k > OMM_MOE_MAX_TOP_K || M > kMaxIndex / OMM_MOE_MAX_TOP_K)
+        return OMM_ERR_UNSUPPORTED;
+    return OMM_OK;
+}
+
+int omm_moe_balance(const omm_tensor* logits, const omm_tensor* indices, const omm_tensor* token_mask,
+                    omm_tensor* losses, omm_tensor* counts, omm_tensor* tokens, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    int rc, kind;
+    if (!losses || !counts || !tokens) return OMM_ERR_NULL;
+    if ((rc = check_router(logits, indices, token_mask, counts, tokens, losses, &kind))) return rc;
+    const int64_t M = logits->shape[0], E = logits->shape[1];
+    if ((rc = check_workspace(workspace, workspace_bytes, M ? omm::moe_balance_workspace_bytes(M, E) : 0))) return rc;
+    omm::MoeBalanceArgs a;
+    a.logits = logits->data;
+    a.ids = indices->data;
+    a.mask = token_mask ? (const uint8_t*)token_mask->data : nullptr;
+    a.losses = (float*)losses->data;
+    a.counts = (int32_t*)counts->data;
+    a.tokens = (int32_t*)tokens->data;
+    a.M = M;
+    a.E = E;
+    a.k = (int)indices->shape[1];
+    a.ids64 = indices->dtype == OMM_I64;
+    return hip_status(omm::launch_moe_balance(a, kind, workspace, (hipStream_t)stream));
+}
+
+int omm_moe_route_grad(const omm_tensor* logits, const omm_tensor* indices, const omm_tensor* grad_weights,
+                       int renormalize, const omm_tensor* token_mask, const omm_tensor* counts,
+                       const omm_tensor* tokens, const omm_tensor* grad_losses, omm_tensor* grad_logits,
+                       void* stream) {
+    int rc, kind;
+    if ((rc = check_tensor(grad_logits))) return rc;
+    if (grad_weights && (rc = check_tensor(grad_weights))) return rc;
+    if (grad_losses && (!counts || !tokens)) return OMM_ERR_NULL;
+    if ((rc = check_router(logits, indices, token_mask, counts, tokens, grad_losses, &kind))) return rc;
+    if (grad_logits->dtype != logits->dtype || (grad_weights && grad_weights->dtype != OMM_F32)) return OMM_ERR_DTYPE;
+    const int64_t M = logits->shape[0], E = logits->shape[1], k = indices->shape[1];
+    if (!has_shape(grad_logits, 2, M, E) || (grad_weights && !has_shape(grad_weights, 2, M, k))) return OMM_ERR_SHAPE;
+    if (M == 0) return OMM_OK;
+    omm::MoeRouteGradArgs a;
+    a.logits = logits->data;
+    a.ids = indices->data;
+    a.mask = token_mask ? (const uint8_t*)token_mask->data : nullptr;
+    a.g_weights = grad_weights && k ? (const float*)grad_weights->data : nullptr;
+    a.counts = grad_losses ? (const int32_t*)counts->data : nullptr;
+    a.tokens = grad_losses ? (const int32_t*)tokens->data : nullptr;
+    a.g_losses = grad_losses ? (const float*)grad_losses->data : nullptr;
+    a.dlogits = grad_logits->data;
+    a.M = M;
+    a.E = E;
+    a.k = (int)k;
+    a.ids64 = indices->dtype == OMM_I64;
+    a.renorm = renormalize != 0;
+    return hip_status(omm::launch_moe_route_grad(a, kind, (hipStream_t)stream));
+}
+
+size_t omm_orthogonalize_workspace_size(int64_t batch, int64_t m, int64_t n) {
+    if (batch <= 0 || m <= 0 || n <= 0 || batch > OMM_ORTHOGONALIZE_MAX_BATCH || m > OMM_ORTHOGONALIZE_MAX_SIDE ||
+        n > OMM_ORTHOGONALIZE_MAX_SIDE)
+        return 0;
+    return omm::orthogonalize_workspace_bytes(batch, m, n);
+}
+
+int omm_orthogonalize(const omm_tensor* G, int steps, omm_tensor* out, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+    int rc, kind;
+    for (const omm_tensor* t : {G, (const omm_tensor*)out})
+        if ((rc = check_tensor(t))) return rc;
+    if ((rc = float_kind(G->dtype, &kind))) return rc;
+    if (out->dtype != G->dtype) return OMM_ERR_DTYPE;
+    if ((G->ndim != 2 && G->ndim != 3) || !same_shape(G, out)) return OMM_ERR_SHAPE;
+    if (steps < 1 || steps > OMM_ORTHOGONALIZE_MAX_STEPS) return OMM_ERR_UNSUPPORTED;
+    const int d = G->ndim - 2;
+    const int64_t Z = d ? G->shape[0] : 1, m = G->shape[d], n = G->shape[d + 1];
+    if (Z == 0 || m == 0 || n == 0) return OMM_OK;
+    if (Z > OMM_ORTHOGONALIZE_MAX_BATCH || m > OMM_ORTHOGONALIZE_MAX_SIDE || n > OMM_ORTHOGONALIZE_MAX_SIDE ||
+        Z * blocks(m, 128) * blocks(n, 128) > kMaxBlocks)
+        return OMM_ERR_UNSUPPORTED;
+    if ((rc = check_workspace(workspace, workspace_bytes, omm::orthogonalize_workspace_bytes(Z, m, n)))) return rc;
+    omm::OrthoArgs a;
+    a.G = G->data;
+    a.out = out->data;
+    a.batch = Z;
+    a.m = m;
+    a.n = n;
+    a.steps = steps;
+    return hip_status(omm::launch_orthogonalize(a, kind, workspace, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,4 +1,5 @@
-// Python binding of the decode-side operators (include/omm.h): argument
+// Python binding of the decode-side operators and of those that train and
+// quantise (include/omm.h): argument
 // marshalling only, as _omm.py does it for the others, but without ctypes.
 // These operators run for a few microseconds, and describing seven tensors and
 // allocating the outputs from Python takes longer than that (moe_route of one
@@ -27,6 +28,14 @@ struct Lib {
     decltype(&omm_token_logprobs) token_logprobs;
     decltype(&omm_token_logprobs_workspace_size) token_logprobs_ws;
     decltype(&omm_token_logprobs_grad) token_logprobs_grad;
+    decltype(&omm_quantize_rows) quantize_rows;
+    decltype(&omm_int8_matmul) int8_matmul;
+    decltype(&omm_int8_matmul_workspace_size) int8_matmul_ws;
+    decltype(&omm_moe_balance) moe_balance;
+    decltype(&omm_moe_balance_workspace_size) moe_balance_ws;
+    decltype(&omm_moe_route_grad) moe_route_grad;
+    decltype(&omm_orthogonalize) orthogonalize;
+    decltype(&omm_orthogonalize_workspace_size) orthogonalize_ws;
 } L = {};
 PyObject* omm_error = nullptr;
 
@@ -245,6 +254,126 @@ PyObject* token_logprobs_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// The device of the first tensor, current while the call's memory and kernels are
+// made, and the only one that its other tensors may be on.
+struct On {
+    const at::Tensor& x;
+    c10::DeviceGuard guard;
+    On(PyObject* first, std::initializer_list<PyObject*> others) : x(gpu(first)), guard(x.device()) {
+        for (PyObject* o : others)
+            if (o != Py_None && tensor(o).device() != x.device()) fail(PyExc_ValueError, "tensors are on different devices");
+    }
+    static const at::Tensor& gpu(PyObject* o) {
+        const at::Tensor& x = tensor(o);
+        if (!x.is_cuda()) fail(PyExc_ValueError, "tensor must be on the GPU");
+        return x;
+    }
+};
+
+// a mask: bytes, or torch.bool, which is a byte of 0 or 1
+struct Mask {
+    omm_tensor t;
+    const omm_tensor* p = nullptr;
+    explicit Mask(PyObject* o) {
+        if (o == Py_None) return;
+        const at::Tensor& x = tensor(o);
+        t = describe(x.scalar_type() == at::kBool ? x.view(at::kByte) : x);
+        p = &t;
+    }
+    Mask(const Mask&) = delete;
+};
+
+// X, Q, scale
+PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 3, [&] {
+        const On on(a[0], {a[1], a[2]});
+        if (on.x.dim() != 2) fail(PyExc_ValueError, "X must be 2-d");
+        Arg x(a[0]);
+        Out q(a[1], on.x.sizes(), on.x, at::kChar), scale(a[2], {on.x.size(0)}, on.x, at::kFloat);
+        void* s = stream(on.x);
+        call("omm_quantize_rows", [&] { return L.quantize_rows(x.p, &q.t, &scale.t, s); });
+        return pack({q.x, scale.x});
+    });
+}
+
+// a, a_scale, b, b_scale, bias, dtype of Y, Y, workspace
+PyObject* int8_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&] {
+        const On on(a[0], {a[1], a[2], a[3], a[4], a[6], a[7]});
+        const at::Tensor &X = on.x, &W = tensor(a[2]);
+        if (X.dim() != 2 || W.dim() != 2) fail(PyExc_ValueError, "a and b must be 2-d");
+        Arg x(a[0]), xs(a[1]), w(a[2]), ws_(a[3]), bias(a[4]);
+        const int dt = integer(a[5]);
+        if (dt != OMM_F32 && dt != OMM_F16 && dt != OMM_BF16) fail(PyExc_ValueError, "Y is bfloat16, float16 or float32");
+        const at::ScalarType yt = dt == OMM_F32 ? at::kFloat : dt == OMM_F16 ? at::kHalf : at::kBFloat16;
+        const int64_t M = X.size(0), K = X.size(1), N = W.size(0);
+        Out y(a[6], {M, N}, X, yt);
+        if (x.t.dtype == OMM_I8 && a[7] == Py_None) {  // (no workspace)
+            void* s = stream(X);
+            call("omm_int8_matmul", [&] { return L.int8_matmul(x.p, xs.p, w.p, ws_.p, bias.p, &y.t, nullptr, 0, s); });
+            return pack({y.x, at::Tensor()});
+        }
+        const Workspace ws = workspace(a[7], X, [&] { return L.int8_matmul_ws(M, K, N, x.t.dtype); });
+        void* s = stream(X);
+        call("omm_int8_matmul",
+             [&] { return L.int8_matmul(x.p, xs.p, w.p, ws_.p, bias.p, &y.t, ws.ptr(), ws.bytes(), s); });
+        return pack({y.x, ws.x});
+    });
+}
+
+// logits, indices, token_mask, workspace
+PyObject* moe_balance(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 4, [&] {
+        const On on(a[0], {a[1], a[2], a[3]});
+        const at::Tensor& logits = on.x;
+        if (logits.dim() != 2) fail(PyExc_ValueError, "logits must be 2-d");
+        Arg x(a[0]), ids(a[1]);
+        Mask mask(a[2]);
+        const int64_t M = logits.size(0), E = logits.size(1);
+        Out losses(nullptr, {2}, logits, at::kFloat), counts(nullptr, {E}, logits, at::kInt),
+            tokens(nullptr, {1}, logits, at::kInt);
+        const Workspace ws = workspace(a[3], logits, [&] { return L.moe_balance_ws(M, E); });
+        void* s = stream(logits);
+        call("omm_moe_balance", [&] {
+            return L.moe_balance(x.p, ids.p, mask.p, &losses.t, &counts.t, &tokens.t, ws.ptr(), ws.bytes(), s);
+        });
+        return pack({losses.x, counts.x, tokens.x});
+    });
+}
+
+// logits, indices, grad_weights, renormalize, token_mask, counts, tokens, grad_losses, grad_logits
+PyObject* moe_route_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject* {
+        const On on(a[0], {a[1], a[2], a[4], a[5], a[6], a[7], a[8]});
+        Arg x(a[0]), ids(a[1]), gw(a[2]), counts(a[5]), tokens(a[6]), gl(a[7]);
+        Mask mask(a[4]);
+        const int renorm = integer(a[3]);
+        Out g(a[8], on.x.sizes(), on.x, on.x.scalar_type());
+        void* s = stream(on.x);
+        call("omm_moe_route_grad",
+             [&] { return L.moe_route_grad(x.p, ids.p, gw.p, renorm, mask.p, counts.p, tokens.p, gl.p, &g.t, s); });
+        return THPVariable_Wrap(g.x);
+    });
+}
+
+// G, steps, out, workspace
+PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 4, [&] {
+        const On on(a[0], {a[2], a[3]});
+        const at::Tensor& G = on.x;
+        const int steps = integer(a[1]);
+        if (G.dim() != 2 && G.dim() != 3) fail(PyExc_ValueError, "G must be 2-d, or 3-d for a batch");
+        Arg g(a[0]);
+        Out out(a[2], G.sizes(), G, G.scalar_type());
+        const int d = (int)G.dim() - 2;
+        const Workspace ws =
+            workspace(a[3], G, [&] { return L.orthogonalize_ws(d ? G.size(0) : 1, G.size(d), G.size(d + 1)); });
+        void* s = stream(G);
+        call("omm_orthogonalize", [&] { return L.orthogonalize(g.p, steps, &out.t, ws.ptr(), ws.bytes(), s); });
+        return pack({out.x, ws.x});
+    });
+}
+
 // load(path of libomm.so, OmmError)
 PyObject* load(PyObject*, PyObject* args) {
     const char* path;
@@ -267,6 +396,14 @@ PyObject* load(PyObject*, PyObject* args) {
         {(void**)&L.token_logprobs, "omm_token_logprobs"},
         {(void**)&L.token_logprobs_ws, "omm_token_logprobs_workspace_size"},
         {(void**)&L.token_logprobs_grad, "omm_token_logprobs_grad"},
+        {(void**)&L.quantize_rows, "omm_quantize_rows"},
+        {(void**)&L.int8_matmul, "omm_int8_matmul"},
+        {(void**)&L.int8_matmul_ws, "omm_int8_matmul_workspace_size"},
+        {(void**)&L.moe_balance, "omm_moe_balance"},
+        {(void**)&L.moe_balance_ws, "omm_moe_balance_workspace_size"},
+        {(void**)&L.moe_route_grad, "omm_moe_route_grad"},
+        {(void**)&L.orthogonalize, "omm_orthogonalize"},
+        {(void**)&L.orthogonalize_ws, "omm_orthogonalize_workspace_size"},
     };
     for (const auto& e : table)
         if (!(*e.f = dlsym(h, e.name))) {
@@ -286,6 +423,11 @@ PyMethodDef methods[] = {
     {"moe_layer", (PyCFunction)(void (*)())moe_layer, METH_FASTCALL, nullptr},
     {"token_logprobs", (PyCFunction)(void (*)())token_logprobs, METH_FASTCALL, nullptr},
     {"token_logprobs_grad", (PyCFunction)(void (*)())token_logprobs_grad, METH_FASTCALL, nullptr},
+    {"quantize_rows", (PyCFunction)(void (*)())quantize_rows, METH_FASTCALL, nullptr},
+    {"int8_matmul", (PyCFunction)(void (*)())int8_matmul, METH_FASTCALL, nullptr},
+    {"moe_balance", (PyCFunction)(void (*)())moe_balance, METH_FASTCALL, nullptr},
+    {"moe_route_grad", (PyCFunction)(void (*)())moe_route_grad, METH_FASTCALL, nullptr},
+    {"orthogonalize", (PyCFunction)(void (*)())orthogonalize, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

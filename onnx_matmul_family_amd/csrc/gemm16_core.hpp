@@ -731,9 +731,15 @@ __device__ __forceinline__ void wave_epilogue_lds(const f32x16_t (&acc)[4][4], f
 // last MFMA from the first read of its result.
 // Z: the first k-block, C = 0 (the accumulators are never zeroed by VALU
 // writes, which an MFMA must not read too soon after).
+// DT = 3: int8 operands (k contiguous, the same bytes a lane: 16 k-values for 8)
+// and int32 sums, as bits in the accumulators.
 template <int DT, bool Z>
 __device__ __forceinline__ void mfma16_tied(f32x4_t& acc, const u32x4_t& a, const u32x4_t& b) {
-    if constexpr (Z && DT == 0)
+    if constexpr (Z && DT == 3)
+        asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, 0" : "=a"(acc) : "v"(a), "v"(b));
+    else if constexpr (DT == 3)
+        asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    else if constexpr (Z && DT == 0)
         asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "=a"(acc) : "v"(a), "v"(b));
     else if constexpr (Z)
         asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, 0" : "=a"(acc) : "v"(a), "v"(b));

@@ -100,7 +100,7 @@ hipError_t launch_grouped(const GroupedArgs& a, int dt, void* ws, hipStream_t s)
 hipError_t launch_grouped_dq(const GroupedArgs& a, int dt, void* ws, hipStream_t s);
 hipError_t grouped_invalid_count(const void* ws, hipStream_t s, int64_t* count);
 
-// Decode-side operators.  dt: 0 = bf16, 1 = fp16, 2 = fp32.
+// Decode-side operators and those of training and quantising.  dt: 0 = bf16, 1 = fp16, 2 = fp32.
 struct TokenLogprobsArgs {
     const void* logits;     // (M, V)
     const void* targets;    // (M) int32 or int64
@@ -152,6 +152,44 @@ struct LoraArgs {
     int64_t M, K, N, R, G;
     int trans, idx64;
 };
+struct Int8Args {
+    const void* a;         // (M, K) int8, or bf16 / fp16 / fp32 (a_kind 0 / 1 / 2) to be quantised
+    int a_kind;            // -1: int8
+    const float* a_scale;  // (M), int8 a
+    const void* b;         // (N, K) int8
+    const float* b_scale;  // (N)
+    const void* bias;      // (N) or nullptr
+    void* Y;               // (M, N)
+    int64_t M, N, K;
+};
+struct MoeBalanceArgs {
+    const void* logits;   // (M, E)
+    const void* ids;      // (M, k) int32 or int64
+    const uint8_t* mask;  // (M) or nullptr
+    float* losses;        // (2)
+    int32_t* counts;      // (E)
+    int32_t* tokens;      // (1)
+    int64_t M, E;
+    int k, ids64;
+};
+struct MoeRouteGradArgs {
+    const void* logits;      // (M, E)
+    const void* ids;         // (M, k) int32 or int64
+    const uint8_t* mask;     // (M) or nullptr
+    const float* g_weights;  // (M, k) or nullptr
+    const int32_t* counts;   // (E), with g_losses
+    const int32_t* tokens;   // (1), with g_losses
+    const float* g_losses;   // (2) or nullptr
+    void* dlogits;           // (M, E)
+    int64_t M, E;
+    int k, ids64, renorm;
+};
+struct OrthoArgs {
+    const void* G;  // (batch, m, n)
+    void* out;
+    int64_t batch, m, n;
+    int steps;
+};
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R, int dt);
 hipError_t launch_lora(const LoraArgs& a, int dt, void* ws, hipStream_t s);
 size_t token_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k);
@@ -159,6 +197,15 @@ hipError_t launch_token_logprobs(const TokenLogprobsArgs& a, int dt, void* ws, h
 hipError_t launch_token_logprobs_grad(const TokenLogprobsGradArgs& a, int dt, hipStream_t s);
 hipError_t launch_moe_route(const MoeRouteArgs& a, int dt, hipStream_t s);
 size_t moe_layer_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t k);
+hipError_t launch_quantize_rows(const void* X, int8_t* Q, float* scale, int64_t M, int64_t K, int dt, hipStream_t s);
+// quantise: a is not int8 yet
+size_t int8_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, bool quantise);
+hipError_t launch_int8_matmul(const Int8Args& a, int dt, void* ws, hipStream_t s);
+size_t moe_balance_workspace_bytes(int64_t M, int64_t E);
+hipError_t launch_moe_balance(const MoeBalanceArgs& a, int dt, void* ws, hipStream_t s);
+hipError_t launch_moe_route_grad(const MoeRouteGradArgs& a, int dt, hipStream_t s);
+size_t orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n);
+hipError_t launch_orthogonalize(const OrthoArgs& a, int dt, void* ws, hipStream_t s);
 hipError_t launch_moe_layer(const MoeLayerArgs& a, int dt, int logits_kind, void* ws, hipStream_t s);
 
 }  // namespace omm
