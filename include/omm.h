@@ -402,7 +402,8 @@ int omm_quantize_rows(const omm_tensor* X, omm_tensor* Q, omm_tensor* scale, voi
  *   The sum is exact (32-bit integers; K <= OMM_INT8_MAX_K, all of -128 .. 127
  *   allowed), converted to fp32, times a_scale, times b_scale, plus bias, rounded
  *   once to T.
- *   A workspace is needed for an a of T only (0 bytes otherwise, NULL allowed).
+ *   The workspace holds an a of T in int8 and, where K is no multiple of 16, the
+ *   operands in rows that are (0 bytes where neither is needed: NULL allowed).
  * Errors: OMM_ERR_NULL (also an int8 a without a_scale), OMM_ERR_DTYPE,
  * OMM_ERR_SHAPE (also a_scale with an a of T), OMM_ERR_UNSUPPORTED, OMM_ERR_WORKSPACE.
  */

@@ -362,7 +362,7 @@ def quantize_rows(X, Q=None, scale=None, stream=None):
 
 
 def int8_matmul_workspace_size(M, K, N, dtype):
-    """dtype: of a (torch.int8: 0 bytes)."""
+    """dtype: of a (torch.int8: 0 bytes, unless K is no multiple of 16)."""
     return int(lib().omm_int8_matmul_workspace_size(int(M), int(K), int(N), _DT[dtype]))
 
 
@@ -372,7 +372,7 @@ def int8_matmul(a, b, b_scale, a_scale=None, bias=None, dtype=None, Y=None, work
     b (N, K) int8 with b_scale (N) float32, as quantize_rows gives them for a linear layer's weights.
     a (M, K) int8 with a_scale (M); or of a floating type without a_scale: quantised by the call.
     dtype: of Y, by default a's (int8 a: bias's, or bfloat16).  Returns (Y, workspace); the workspace is None
-    for an int8 a."""
+    where none is needed."""
     if stream is not None:
         return _on(stream, int8_matmul, a, b, b_scale, a_scale, bias, dtype, Y, workspace)
     if dtype is None:

@@ -966,7 +966,7 @@ int omm_quantize_rows(const omm_tensor* X, omm_tensor* Q, omm_tensor* scale, voi
 size_t omm_int8_matmul_workspace_size(int64_t M, int64_t K, int64_t N, int32_t a_dtype) {
     int kind;
     if (M <= 0 || K < 0 || N <= 0 || K > OMM_INT8_MAX_K || (a_dtype != OMM_I8 && float_kind(a_dtype, &kind)) ||
-        M > (int64_t)1 << 40)
+        M > kMaxIndex || N > kMaxIndex)
         return 0;
     return omm::int8_matmul_workspace_bytes(M, K, N, a_dtype != OMM_I8);
 }
@@ -988,7 +988,7 @@ int omm_int8_matmul(const omm_tensor* a, const omm_tensor* a_scale, const omm_te
     if ((rc = check_f32_vec(a_scale, M)) || (rc = check_f32_vec(b_scale, N))) return rc;
     if ((bias && !has_shape(bias, 1, N)) || !has_shape(Y, 2, M, N)) return OMM_ERR_SHAPE;
     if (M == 0 || N == 0) return OMM_OK;
-    if (K > OMM_INT8_MAX_K || M > kMaxIndex || N > kMaxIndex || blocks(M, 128) * blocks(N, 128) > kMaxBlocks)
+    if (K > OMM_INT8_MAX_K || M > kMaxIndex || N > kMaxIndex || blocks(M, 64) * blocks(N, 64) > kMaxBlocks)
         return OMM_ERR_UNSUPPORTED;
     if ((rc = check_workspace(workspace, workspace_bytes, omm::int8_matmul_workspace_bytes(M, K, N, a_kind >= 0))))
         return rc;
@@ -1104,7 +1104,7 @@ int omm_orthogonalize(const omm_tensor* G, int steps, omm_tensor* out, void* wor
     const int64_t Z = d ? G->shape[0] : 1, m = G->shape[d], n = G->shape[d + 1];
     if (Z == 0 || m == 0 || n == 0) return OMM_OK;
     if (Z > OMM_ORTHOGONALIZE_MAX_BATCH || m > OMM_ORTHOGONALIZE_MAX_SIDE || n > OMM_ORTHOGONALIZE_MAX_SIDE ||
-        Z * blocks(m, 128) * blocks(n, 128) > kMaxBlocks)
+        Z * blocks(m, 64) * blocks(n, 64) > kMaxBlocks)
         return OMM_ERR_UNSUPPORTED;
     if ((rc = check_workspace(workspace, workspace_bytes, omm::orthogonalize_workspace_bytes(Z, m, n)))) return rc;
     omm::OrthoArgs a;

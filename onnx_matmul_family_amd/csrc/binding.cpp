@@ -308,7 +308,7 @@ PyObject* int8_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::ScalarType yt = dt == OMM_F32 ? at::kFloat : dt == OMM_F16 ? at::kHalf : at::kBFloat16;
         const int64_t M = X.size(0), K = X.size(1), N = W.size(0);
         Out y(a[6], {M, N}, X, yt);
-        if (x.t.dtype == OMM_I8 && a[7] == Py_None) {  // (no workspace)
+        if (a[7] == Py_None && L.int8_matmul_ws(M, K, N, x.t.dtype) == 0) {
             void* s = stream(X);
             call("omm_int8_matmul", [&] { return L.int8_matmul(x.p, xs.p, w.p, ws_.p, bias.p, &y.t, nullptr, 0, s); });
             return pack({y.x, at::Tensor()});

@@ -11,8 +11,8 @@
 
 #include <algorithm>
 
-#include "gemm16_core.hpp"
 #include "kernels.hpp"
+#include "row_loop.hpp"
 #include "stream_core.hpp"
 
 namespace omm {
@@ -35,30 +35,51 @@ struct QuantArgs {
 typedef u32x2_t u32x2_u1 __attribute__((aligned(1)));
 typedef uint32_t u32_u1 __attribute__((aligned(1)));
 
-// 127 x / amax to the nearest integer.  x * inv is within 1.6e-5 of it (two
-// roundings of values up to 127), so only what lies closer than that to the
-// border of two steps is divided in 64 bits.
-__device__ __forceinline__ float quantise(float x, float amax, float inv, bool tiny) {
-    const float t = x * inv, q = rintf(t);
-    if (tiny || fabsf(t - q) > 0.49996f) return (float)rint((double)x * 127.0 / (double)amax);
-    return q;
-}
+// 127 x / amax to the nearest integer, as bytes.  x * inv is within 1.6e-5 of it (two
+// roundings of values up to 127), so only what lies closer than that to the border
+// of two steps is divided in 64 bits; so is every value of a row whose inv is 0
+// (amax too small for one).
 template <int V>
-__device__ __forceinline__ void quantise_store(int8_t* q, const float* f, int n, float amax, float inv, bool tiny) {
-    uint32_t w[V / 4] = {};
+__device__ __forceinline__ void quantise(const float* f, float amax, float inv, uint32_t (&w)[V / 4]) {
+    float q[V];
+    bool exact = inv == 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) w[i / 4] |= ((uint32_t)(int)quantise(f[i], amax, inv, tiny) & 255u) << (8 * (i & 3));
-    if (n >= V) {
-        if constexpr (V == 8)
-            *(u32x2_u1*)q = u32x2_t{w[0], w[1]};
-        else
-            *(u32_u1*)q = w[0];
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < n) q[i] = (int8_t)(w[i / 4] >> (8 * (i & 3)));
+    for (int i = 0; i < V; ++i) {
+        const float t = f[i] * inv;
+        q[i] = rintf(t);
+        exact |= fabsf(t - q[i]) > 0.49996f;
     }
+    if (exact) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] = (float)rint((double)f[i] * 127.0 / (double)amax);
+    }
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i / 4] |= ((uint32_t)(int)q[i] & 255u) << (8 * (i & 3));
 }
+// What a row's largest magnitude (as bits) makes of it.  A row that holds a NaN or
+// an infinity: scale NaN and values 0.
+struct RowScale {
+    float amax, inv, scale;
+    bool zero;
+    __device__ __forceinline__ explicit RowScale(uint32_t mx) {
+        const bool finite = mx < 0x7f800000u;
+        amax = __uint_as_float(mx);
+        scale = finite ? amax / 127.0f : __builtin_nanf("");
+        zero = !finite || mx == 0;
+        inv = !zero && amax >= 0x1p-100f ? 127.0f / amax : 0.0f;
+    }
+    template <int V>
+    __device__ __forceinline__ void bytes(const float* f, uint32_t (&w)[V / 4]) const {
+        if (zero) {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) w[i] = 0;
+        } else {
+            quantise<V>(f, amax, inv, w);
+        }
+    }
+};
 
 // NW waves a row, C 16-byte chunks a lane (C = 0: rows of any length, read twice)
 template <int DT, int NW, int C>
@@ -95,21 +116,22 @@ __global__ __launch_bounds__(NW <= 4 ? 256 : 64 * NW) void quantise_kernel(Quant
         for (int w = 0; w < NW; ++w) mx = max(mx, part[w]);
     }
     if (!here) return;
-    // a row that holds a NaN or an infinity: its scale is NaN and its values 0
-    const bool finite = mx < 0x7f800000u;
-    const float amax = __uint_as_float(mx), s = finite ? amax / 127.0f : __builtin_nanf("");
-    const bool tiny = finite && mx && amax < 0x1p-100f;
-    const float inv = finite && mx && !tiny ? 127.0f / amax : 0.0f;
-    if (l == 0) a.scale[m] = s;
+    const RowScale rs(mx);
+    if (l == 0) a.scale[m] = rs.scale;
     int8_t* q = a.Q + m * a.ldq;
-    const auto out = [&](int64_t e, u32x4_t w) {
+    const auto out = [&](int64_t e, u32x4_t v) {
         float f[V];
-        unpack16<DT>(w, f);
-        if (!finite || !mx) {
+        uint32_t w[V / 4];
+        unpack16<DT>(v, f);
+        rs.bytes<V>(f, w);
+        if (a.ldq - e >= V) {
+            if constexpr (V == 8) *(u32x2_u1*)(q + e) = u32x2_t{w[0], w[1]};
+            else *(u32_u1*)(q + e) = w[0];
+        } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = 0.0f;
+            for (int i = 0; i < V; ++i)
+                if (e + i < a.ldq) q[e + i] = (int8_t)(w[i / 4] >> (8 * (i & 3)));
         }
-        quantise_store<V>(q + e, f, (int)min((int64_t)V, a.ldq - e), amax, inv, tiny);
     };
     if constexpr (C) {
 #pragma unroll
@@ -158,22 +180,46 @@ hipError_t quantise_dt(const QuantArgs& a, int dt, hipStream_t s) {
 // ------------------------------------------------------------------ product
 struct ProductArgs {
     const int8_t* a;       // (M, lda)
-    const int8_t* b;       // (N, K)
+    const int8_t* b;       // (N, ldb)
     const float* a_scale;  // (M)
     const float* b_scale;  // (N)
     const void* bias;      // (N) of T or nullptr
     void* Y;               // (M, N) of T
-    int64_t M, N, lda;
+    int64_t M, N, lda, ldb;
     int K;
 };
 
-// Four neighbouring results of a row
-template <int DT>
-__device__ __forceinline__ void scaled4(const i32x4_t& acc, float sa, const float (&sb)[4], const float (&bias)[4],
-                                        float (&v)[4]) {
+typedef u32x4_t u32x4_u1 __attribute__((aligned(1)));
+// 16 bytes at p, zeros from the n-th on
+__device__ __forceinline__ u32x4_t bytes16(const int8_t* p, int n) {
+    if (n >= 16) return *(const u32x4_u1*)p;
+    u32x4_t v = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (float)acc[e] * sa * sb[e] + bias[e];
+    for (int e = 0; e < 16; ++e)
+        if (e < n) v[e >> 2] |= (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
+    return v;
 }
+__device__ __forceinline__ i32x4_t mfma_i8(u32x4_t a, u32x4_t b, i32x4_t c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
+}
+
+// Scales and bias of four neighbouring columns (past the last: of the last)
+template <int DT>
+struct Columns {
+    float scale[4], bias[4];
+    __device__ __forceinline__ Columns(const ProductArgs& a, int64_t n) {
+        typedef typename elem_of<DT>::type E;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            scale[e] = a.b_scale[min(n + e, a.N - 1)];
+            bias[e] = a.bias ? elem_f32<DT>(((const E*)a.bias)[min(n + e, a.N - 1)]) : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void values(const i32x4_t& acc, float sa, float (&v)[4]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)acc[e] * sa * scale[e] + bias[e];
+    }
+};
 template <int DT>
 __device__ __forceinline__ void store4(void* Y, int64_t at, const float (&v)[4], int n) {
     typedef typename elem_of<DT>::type E;
@@ -193,100 +239,360 @@ __device__ __forceinline__ void store4(void* Y, int64_t at, const float (&v)[4],
     }
 }
 
-// BT x BT tiles, 4 waves of (BT / 2)^2.  MODE 0: whole tiles by DMA; 1: ragged
-// ones by DMA (16-byte aligned rows); 2: rows at any byte, through registers.
-template <int BT, int DT, int MODE>
-__global__ __launch_bounds__(NT, BT == 128 ? 2 : 1) void int8_tile_kernel(ProductArgs a, int tiles_m, int tiles_n) {
-    constexpr int TM = BT / 32, TN = BT / 32, OP = BT * 128, STAGE = 2 * OP;
-    __shared__ __attribute__((aligned(1024))) char smem0[STAGE];
-    __shared__ __attribute__((aligned(1024))) char smem1[STAGE];
+// ------------------------------------------------------------------ few rows
+// Up to 64 rows against 16 NF columns a workgroup at a time: one read of b, of which
+// each of 8 waves takes every 8th 128 bytes of k (the sums of integers join in LDS in
+// any order).  A wave loads 128 bytes of a row by 8 neighbouring lanes, 8 rows at a
+// time (in the operands' order every lane would be a line of its own), and the
+// operands take their places through LDS of the wave's own.  Any alignment, any K.
+// AK: -1, a is int8; else rows of that type (few), which every workgroup quantises
+// for itself while the first of b is on its way.
+struct FewArgs {
+    ProductArgs p;
+    const void* X;  // AK >= 0: (M, K)
+    int kpad;       // K to whole 128 bytes
+};
+constexpr int kFewWaves = 8;
+
+template <int DT, int NF, int MG, int U, int AK>
+__global__ __launch_bounds__(64 * kFewWaves) void int8_few_kernel(FewArgs f) {
+    constexpr int XG = AK < 0 ? MG : 0;  // groups of 16 rows that are loaded as b is
+    constexpr int UNIT = 128;            // 16-byte pieces of 16 rows
+    extern __shared__ u32x4_t smem[];
+    ProductArgs a = f.p;
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    if constexpr (AK < 0) {  // 16 MG rows of more
+        const int64_t m0 = (int64_t)blockIdx.y * (16 * MG);
+        a.a += m0 * a.lda;
+        a.a_scale += m0;
+        a.Y = (typename elem_of<DT>::type*)a.Y + m0 * a.N;
+        a.M = min(a.M - m0, (int64_t)(16 * MG));
+    }
+    const int M = (int)a.M, K = a.K;
+    const int lr = lane >> 3, lp = lane & 7;  // row of 8 and piece that the lane loads
+    const int nfull = K / 128;  // whole units; what is left of k is one more, of wave nfull % 8
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * NF);
+    const auto load = [&](u32x4_t (&w)[NF][2], u32x4_t (&x)[XG ? XG : 1][2], int u, auto piece) __attribute__((always_inline)) {
+        const int k = u * 128 + lp * 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int g = 0; g < NF; ++g)
+                w[g][i] = piece(a.b + min(n0 + 16 * g + 8 * i + lr, a.N - 1) * a.ldb, k);
+#pragma unroll
+            for (int g = 0; g < XG; ++g) x[g][i] = piece(a.a + (int64_t)min(16 * g + 8 * i + lr, M - 1) * a.lda, k);
+        }
+    };
+    u32x4_t w[2][U][NF][2], x[2][U][XG ? XG : 1][2], wt[NF][2], xt[XG ? XG : 1][2];
+    // step s: U units of each wave
+    constexpr int STEP = U * kFewWaves;
+    const auto loads = [&](auto set, int step) __attribute__((always_inline)) {
+        static_for<0, U>([&](auto u) {
+            const int at = step * STEP + u * kFewWaves + wave;
+            if (at < nfull) load(w[set][u], x[set][u], at, [](const int8_t* p, int k) { return *(const u32x4_u1*)(p + k); });
+        });
+    };
+    constexpr std::integral_constant<int, 0> first = {};
+    constexpr std::integral_constant<int, 1> second = {};
+    const bool tail = K % 128 != 0 && wave == nfull % kFewWaves;
+    const auto load_tail = [&]() __attribute__((always_inline)) {
+        if (tail)
+            load(wt, xt, nfull, [&](const int8_t* p, int k) { return bytes16(p + min(k, K), max(0, min(16, K - k))); });
+    };
+    // this wave's pieces: [NF + XG][16 rows][8], those of a row in the order piece ^ row
+    u32x4_t* own = smem + wave * ((NF + XG) * UNIT);
+    // AK >= 0: the rows' int8, [M][kpad / 16] (after what the waves' pieces and sums need)
+    u32x4_t* q_s = smem + kFewWaves * (NF * UNIT);
+    __shared__ float scale_s[kFewWaves];
+    if constexpr (AK >= 0) {
+        typedef typename elem_of<AK>::type E;
+        constexpr int V = kVec<AK>, KEEP = 4;
+        __shared__ uint32_t max_s[kFewWaves];
+        // 8 / (M to a power of two) waves a row, KEEP vectors a lane in registers
+        const int waves = M == 1 ? 8 : M == 2 ? 4 : M <= 4 ? 2 : 1, row = wave / waves, nl = 64 * waves;
+        const int l = (wave % waves) * 64 + lane;
+        const E* X = (const E*)f.X + (int64_t)min(row, M - 1) * K;
+        u32x4_t keep[KEEP];
+        uint32_t mx = 0;
+        const auto largest = [&](u32x4_t v) {
+            float e[V];
+            unpack16<AK>(v, e);
+#pragma unroll
+            for (int i = 0; i < V; ++i) mx = max(mx, __float_as_uint(e[i]) & 0x7fffffffu);
+        };
+        const auto vec = [&](int c) {
+            const int e = (c * nl + l) * V;
+            return load16_first(X + min(e, K), max(0, min(V, K - e)));
+        };
+#pragma unroll
+        for (int c = 0; c < KEEP; ++c) keep[c] = vec(c);
+        loads(first, 0);
+        load_tail();
+#pragma unroll
+        for (int c = 0; c < KEEP; ++c) largest(keep[c]);
+        for (int c = KEEP; c * nl * V < K; ++c) largest(vec(c));
+        mx = wave_max_u32(mx);
+        if (lane == 0) max_s[wave] = mx;
+        __syncthreads();
+        // (a row's waves are neighbours: lanes past them look at the first again)
+        mx = wave_max_u32(max_s[row * waves + (lane < waves ? lane : 0)]);
+        const RowScale rs(mx);
+        if (row < M) {
+            if (l == 0) scale_s[row] = rs.scale;
+            const auto out = [&](int c, u32x4_t v) {
+                const int e = (c * nl + l) * V;
+                if (e >= f.kpad) return;
+                float g[V];
+                uint32_t q[V / 4];
+                unpack16<AK>(v, g);
+                rs.bytes<V>(g, q);
+                char* d = (char*)(q_s + row * (f.kpad / 16) + ((e / 16) ^ (row & 7))) + e % 16;
+                if constexpr (V == 8) *(u32x2_t*)d = u32x2_t{q[0], q[1]};
+                else *(uint32_t*)d = q[0];
+            };
+#pragma unroll
+            for (int c = 0; c < KEEP; ++c) out(c, keep[c]);
+            for (int c = KEEP; c * nl * V < f.kpad; ++c) out(c, vec(c));
+        }
+        __syncthreads();
+    } else {
+        loads(first, 0);
+        load_tail();
+    }
+    i32x4_t acc[NF][MG] = {};
+    const int ir = lane & 15, ip = lane >> 4;  // the operand's row and 16 of 64 k
+    const auto mul = [&](const u32x4_t (&w)[NF][2], const u32x4_t (&x)[XG ? XG : 1][2], int u) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = (8 * i + lr) * 8 + (lp ^ lr);
+#pragma unroll
+            for (int g = 0; g < NF; ++g) own[g * UNIT + at] = w[g][i];
+#pragma unroll
+            for (int g = 0; g < XG; ++g) own[(NF + g) * UNIT + at] = x[g][i];
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int at = ir * 8 + ((4 * s + ip) ^ (ir & 7));
+            u32x4_t fx[MG];
+#pragma unroll
+            for (int g = 0; g < MG; ++g) {
+                if constexpr (AK < 0) fx[g] = own[(NF + g) * UNIT + at];
+                else fx[g] = ir < M ? q_s[ir * (f.kpad / 16) + ((u * 8 + 4 * s + ip) ^ (ir & 7))] : u32x4_t{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                const u32x4_t fw = own[j * UNIT + at];
+#pragma unroll
+                for (int g = 0; g < MG; ++g) acc[j][g] = mfma_i8(fw, fx[g], acc[j][g]);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    };
+    const auto muls = [&](auto set, int step) __attribute__((always_inline)) {
+        static_for<0, U>([&](auto u) {
+            const int at = step * STEP + u * kFewWaves + wave;
+            if (at < nfull) mul(w[set][u], x[set][u], at);
+        });
+    };
+    for (int step = 0; step * STEP < nfull; step += 2) {
+        loads(second, step + 1);
+        muls(first, step);
+        loads(first, step + 2);
+        muls(second, step + 1);
+    }
+    if (tail) mul(wt, xt, nfull);
+    // the waves' sums join: [wave][NF][MG][64]
+    __syncthreads();
+    i32x4_t* red = (i32x4_t*)smem;
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int g = 0; g < MG; ++g) red[((wave * NF + j) * MG + g) * 64 + lane] = acc[j][g];
+    __syncthreads();
+    for (int o = t; o < NF * MG * 64; o += 64 * kFewWaves) {
+        const int l = o & 63, g = (o >> 6) % MG, j = (o >> 6) / MG;
+        const int m = 16 * g + (l & 15);
+        const int64_t n = n0 + 16 * j + 4 * (l >> 4);
+        if (m >= M || n >= a.N) continue;
+        i32x4_t sum = red[o];
+#pragma unroll
+        for (int wv = 1; wv < kFewWaves; ++wv) sum += red[wv * (NF * MG * 64) + o];
+        float v[4];
+        Columns<DT>(a, n).values(sum, AK < 0 ? a.a_scale[m] : scale_s[AK < 0 ? 0 : m], v);
+        store4<DT>(a.Y, m * a.N + n, v, (int)min((int64_t)4, a.N - n));
+    }
+}
+
+// ------------------------------------------------------------------ tiles
+// acc = sum over nk stages of 128 k, two blocks of 64 each, NB stages in LDS
+// (row_loop.hpp).  During the first block the second's fragments are read; then the
+// barrier that retires the stage and publishes the next; during the second block the
+// next stage's first fragments, and the DMA of stage kt + NB.
+// KS groups of 4 waves take every KS-th stage each, in LDS of their own.
+template <int BT, int NB, int KS, class SA, class SB>
+struct Loop8 {
+    static constexpr int TM = BT / 32, NM = TM * TM, OPB = BT * 128, STAGE = 2 * OPB, LA = SA::PER_WAVE;
+    f32x4_t (&acc)[TM][TM];
+    char* smem;
+    const SA& sa;
+    const SB& sb;
+    int nk, lane, wave, group, rowa, rowb;
+    u32x4_t fa[2][TM], fb[2][TM];
+
+    __device__ __forceinline__ char* at(int kt) const { return smem + (group * NB + kt % NB) * STAGE; }
+    template <int s, int i>
+    __device__ __forceinline__ void read(const char* st) {
+        if constexpr (i % 2 == 0) fb[s][i / 2] = read_frag16<BT, true>(st + OPB, rowb + 8 * i, s, lane);
+        else fa[s][i / 2] = read_frag16<BT, true>(st, rowa + 8 * (i - 1), s, lane);
+    }
+    template <int d>
+    __device__ __forceinline__ void dma(const i32x4_t& ra, const i32x4_t& rb, uint32_t l, int kt) const {
+        if constexpr (d < LA) sa.one(ra, l, kt * KS + group, wave, d);
+        else sb.one(rb, l + OPB, kt * KS + group, wave, d - LA);
+    }
+    template <bool Z>
+    __device__ __forceinline__ void stage(int kt) {
+        const char *st = at(kt), *nx = at(kt + 1);
+        phase<3, TM, TM, Z>(acc, fa[0], fb[0], [&](auto xc) {
+            spread<NM, 2 * TM, decltype(xc)::value>([&](auto i) { read<1, decltype(i)::value>(st); });
+        });
+        wait_vm<(NB - 2) * 2 * LA>();  // this wave's DMA of stage kt + 1 has landed
+        __syncthreads();               // ... every wave's; and every read of stage kt is done
+        fence_sched();
+        const int next = (kt + NB) * KS + group;
+        const i32x4_t ra = sa.rsrc(next, nk), rb = sb.rsrc(next, nk);
+        const uint32_t l = lds_addr(st);
+        phase<3, TM, TM, false>(acc, fa[1], fb[1], [&](auto xc) {
+            constexpr int x = decltype(xc)::value;
+            spread<NM, 2 * LA, x>([&](auto d) { dma<decltype(d)::value>(ra, rb, l, kt + NB); });
+            spread<NM, 2 * TM, x>([&](auto i) { read<0, decltype(i)::value>(nx); });
+        });
+    }
+    __device__ __forceinline__ void run() {
+        for (int kt = 0; kt < NB; ++kt) {
+            const i32x4_t ra = sa.rsrc(kt * KS + group, nk), rb = sb.rsrc(kt * KS + group, nk);
+            const uint32_t l = lds_addr(at(kt));
+            static_for<0, 2 * LA>([&](auto d) { dma<decltype(d)::value>(ra, rb, l, kt); });
+        }
+        wait_vm<(NB - 1) * 2 * LA>();
+        __syncthreads();
+        static_for<0, 2 * TM>([&](auto i) { read<0, decltype(i)::value>(at(0)); });
+        stage<true>(0);
+        for (int kt = 1; kt * KS < nk; ++kt) stage<false>(kt);
+        wait_vm<0>();
+        acc_fence(acc);
+    }
+};
+
+// Results of a wave's H x H block at (wr, wc), from the accumulators' layout
+template <int DT, int TM>
+__device__ __forceinline__ void tile_store(const ProductArgs& a, const f32x4_t (&acc)[TM][TM], int64_t wr, int64_t wc, int lane) {
+    float sa[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sa[i] = a.a_scale[min(wr + 16 * i + (lane & 15), a.M - 1)];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+        const int64_t n = wc + 16 * j + 4 * (lane >> 4);
+        if (n >= a.N) continue;
+        const Columns<DT> col(a, n);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int64_t m = wr + 16 * i + (lane & 15);
+            float v[4];
+            col.values(__builtin_bit_cast(i32x4_t, acc[i][j]), sa[i], v);
+            if (m < a.M) store4<DT>(a.Y, m * a.N + n, v, (int)min((int64_t)4, a.N - n));
+        }
+    }
+}
+// ... through LDS of the wave's own (32 rows at a time), by whole rows of 16 bytes a
+// lane.  Whole blocks of a Y whose rows are 16-byte aligned.
+template <int DT, int TM>
+__device__ __forceinline__ void tile_store_rows(const ProductArgs& a, const f32x4_t (&acc)[TM][TM], int64_t wr, int64_t wc,
+                                                char* own, int lane) {
+    constexpr int H = 16 * TM, EB = DT == 2 ? 4 : 2, W = H * EB, CPR = W / 16, NCH = 32 * CPR / 64, SWZ = CPR < 8 ? CPR - 1 : 7;
+    const auto slot = [](int row, int piece) { return (piece ^ (row & SWZ)) << 4; };
+#pragma unroll
+    for (int h = 0; h < TM / 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            const int g = lane >> 4;
+            const Columns<DT> col(a, wc + 16 * j + 4 * g);
+#pragma unroll
+            for (int ii = 0; ii < 2; ++ii) {
+                const int row = 16 * ii + (lane & 15);
+                float v[4];
+                col.values(__builtin_bit_cast(i32x4_t, acc[2 * h + ii][j]), a.a_scale[wr + 32 * h + row], v);
+                const int byte = (16 * j + 4 * g) * EB;
+                char* d = own + row * W + slot(row, byte >> 4) + (byte & 15);
+                if constexpr (DT == 2) *(f32x4_t*)d = f32x4_t{v[0], v[1], v[2], v[3]};
+                else *(u32x2_t*)d = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < NCH; ++q) {
+            const int row = (q * 64 + lane) / CPR, ch = (q * 64 + lane) % CPR;
+            *(u32x4_t*)((char*)a.Y + ((wr + 32 * h + row) * a.N + wc) * EB + ch * 16) =
+                *(const u32x4_t*)(own + row * W + slot(row, ch));
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// BT x BT tiles, KS groups of 4 waves of (BT / 2)^2, operands of 16-byte aligned rows.
+// KT: K is not a multiple of 128; a's pieces past it are zeros, so b's need not be.
+template <int BT, int NB, int KS, int DT, bool KT>
+__global__ __launch_bounds__(NT * KS, KS * NB * BT * 256 <= 80 * 1024 ? 2 * KS : KS) void int8_tile_kernel(
+    ProductArgs a, int tiles_m, int tiles_n) {
+    typedef Loop8<BT, NB, KS, RowSrc<BT, KT>, RowSrc<BT, false>> L;
+    constexpr int TM = L::TM, H = BT / 2;
+    __shared__ __attribute__((aligned(1024))) char smem[KS * NB * L::STAGE];
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane((t >> 6) & 3);
+    const int group = __builtin_amdgcn_readfirstlane(t >> 8);
     const int wm = wave >> 1, wn = wave & 1;
     int tm, tn;
     grouped_order(xcd_remap((int)blockIdx.x, (int)gridDim.x), tiles_m, tiles_n, 4, tm, tn);
     const int64_t m0 = (int64_t)tm * BT, n0 = (int64_t)tn * BT;
-    const int nk = (a.K + 127) / 128;
-    f32x4_t acc[TM][TN];
-    if constexpr (MODE < 2) {
-        DmaSrc<BT, true, 1> sa, sb;
-        sa.init(a.a, a.lda, m0, a.M, a.K, lane);
-        sb.init(a.b, a.K, n0, a.N, a.K, lane);
-        mainloop_dma16<BT, BT, 3, true, true, MODE == 1>(acc, smem0, smem1, sa, sb, nk, lane, wm, wn, wave);
-    } else {
-        i32x4_t sum[TM][TN] = {};
-        constexpr int NC = BT * 8 / NT;  // 16-byte chunks of an operand a thread
-        u32x4_t r[2][NC];
-        const auto load = [&](int kt) {
+    RowSrc<BT, KT> sa;
+    RowSrc<BT, false> sb;
+    sa.init(a.a, (uint32_t)a.lda, (uint32_t)a.K, m0, a.M, lane);
+    sb.init(a.b, (uint32_t)a.ldb, (uint32_t)a.K, n0, a.N, lane);
+    f32x4_t acc[TM][TM];
+    L loop{acc, smem, sa, sb, (a.K + 127) / 128, lane, wave, group, wm * H, wn * H};
+    loop.run();
+    __syncthreads();  // every wave is done with the last stage
+    if constexpr (KS > 1) {
+        // the groups' sums join (integers: in any order), past what the results need of LDS
+        i32x4_t* red = (i32x4_t*)(smem + 4 * 32 * H * 4) + wave * (TM * TM * 64) + lane;
+        if (group) {
 #pragma unroll
-            for (int i = 0; i < 2 * NC; ++i) {
-                const int row = (t >> 3) + 32 * (i % NC);
-                const int k = kt * 128 + 16 * (t & 7), n = min(16, a.K - k);
-                const bool isb = i >= NC;
-                const int64_t at = (isb ? n0 : m0) + row;
-                u32x4_t v = {0, 0, 0, 0};
-                if (at < (isb ? a.N : a.M) && n > 0) {
-                    const int8_t* p = (isb ? a.b + at * a.K : a.a + at * a.lda) + k;
-                    if (n == 16) {
-                        typedef u32x4_t u32x4_u1 __attribute__((aligned(1)));
-                        v = *(const u32x4_u1*)p;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (e < n) v[e >> 2] |= (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
-                    }
-                }
-                r[i / NC][i % NC] = v;
-            }
-        };
-        load(0);
-        for (int kt = 0; kt < nk; ++kt) {
-            char* s = kt & 1 ? smem1 : smem0;
-#pragma unroll
-            for (int i = 0; i < 2 * NC; ++i)
-                *(u32x4_t*)(s + (i / NC) * OP + kmaj_off<BT>((t >> 3) + 32 * (i % NC), t & 7)) = r[i / NC][i % NC];
-            __syncthreads();  // (the other buffer's readers passed the barrier before)
-            if (kt + 1 < nk) load(kt + 1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4_t fa[TM], fb[TN];
-#pragma unroll
-                for (int i = 0; i < TM; ++i) fa[i] = read_frag16<BT, true>(s, wm * (BT / 2) + 16 * i, h, lane);
-#pragma unroll
-                for (int j = 0; j < TN; ++j) fb[j] = read_frag16<BT, true>(s + OP, wn * (BT / 2) + 16 * j, h, lane);
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int j = 0; j < TN; ++j)
-                        sum[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, fb[j]),
-                                                                          __builtin_bit_cast(i32x4_t, fa[i]), sum[i][j], 0, 0, 0);
-            }
+            for (int i = 0; i < TM * TM; ++i)
+                red[((group - 1) * 4 * TM * TM + i) * 64] = __builtin_bit_cast(i32x4_t, acc[i / TM][i % TM]);
         }
+        __syncthreads();
+        if (group) return;
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int g = 0; g < KS - 1; ++g)
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_bit_cast(f32x4_t, sum[i][j]);
+            for (int i = 0; i < TM * TM; ++i)
+                acc[i / TM][i % TM] = __builtin_bit_cast(
+                    f32x4_t, __builtin_bit_cast(i32x4_t, acc[i / TM][i % TM]) + red[(g * 4 * TM * TM + i) * 64]);
     }
-    typedef typename elem_of<DT>::type E;
-    float sa[TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = a.a_scale[min(m0 + wm * (BT / 2) + 16 * i + (lane & 15), a.M - 1)];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-        const int64_t n = n0 + wn * (BT / 2) + 16 * j + 4 * (lane >> 4);
-        if (n >= a.N) continue;
-        float sb[4], bias[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            sb[e] = a.b_scale[min(n + e, a.N - 1)];
-            bias[e] = a.bias ? elem_f32<DT>(((const E*)a.bias)[min(n + e, a.N - 1)]) : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int64_t m = m0 + wm * (BT / 2) + 16 * i + (lane & 15);
-            float v[4];
-            scaled4<DT>(__builtin_bit_cast(i32x4_t, acc[i][j]), sa[i], sb, bias, v);
-            if (m < a.M) store4<DT>(a.Y, m * a.N + n, v, (int)min((int64_t)4, a.N - n));
-        }
+    const int64_t wr = m0 + wm * H, wc = n0 + wn * H;
+    constexpr int EB = DT == 2 ? 4 : 2;
+    if (wr + H <= a.M && wc + H <= a.N && a.N * EB % 16 == 0 && ((uintptr_t)a.Y & 15) == 0)
+        tile_store_rows<DT, TM>(a, acc, wr, wc, smem + wave * (32 * H * EB), lane);
+    else
+        tile_store<DT, TM>(a, acc, wr, wc, lane);
+}
+
+// Rows of K bytes at any byte -> rows of ld, a multiple of 16, zeros past K
+__global__ __launch_bounds__(256) void int8_align_kernel(const int8_t* x, int8_t* y, int64_t rows, int K, int64_t ld) {
+    const int per = (int)(ld / 16);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
+        const int k = (int)(i % per) * 16;
+        *(u32x4_t*)(y + i * 16) = bytes16(x + i / per * K + k, K - k);
     }
 }
 
@@ -302,22 +608,86 @@ __global__ __launch_bounds__(256) void int8_bias_kernel(ProductArgs a) {
     }
 }
 
+template <int DT, int NF, int MG, int U, int AK>
+void few_go(const FewArgs& f, hipStream_t s) {
+    constexpr int XG = AK < 0 ? MG : 0;
+    const size_t pieces = (size_t)kFewWaves * (NF + XG) * 2048 + (AK < 0 ? 0 : (size_t)f.p.M * f.kpad);
+    const size_t lds = std::max(pieces, (size_t)kFewWaves * NF * MG * 1024);
+    const dim3 grid((unsigned)((f.p.N + 16 * NF - 1) / (16 * NF)), (unsigned)((f.p.M + 16 * MG - 1) / (16 * MG)));
+    log_choice("int8_matmul: %lld rows streamed, %d columns a workgroup%s", (long long)f.p.M, 16 * NF,
+               AK < 0 ? "" : ", quantised there");
+    int8_few_kernel<DT, NF, MG, U, AK><<<grid, 64 * kFewWaves, lds, s>>>(f);
+}
+// 16 columns a workgroup while that makes no more of them than there are CUs, or, of
+// rows up to 16, two a CU; 32 beyond (us, bf16, graph replays: 1 row, 4096 x 4096
+// 6.5 and 7.5, 4096 x 14336 19.2 and 16.9; 43 rows, 4096 x 4104 12.1 and 8.6).  Four
+// units of b a wave at once where one round of them is all there is (1 row, 4096 x
+// 4096: 6.5, by two 7.5), two where workgroups share a CU (8192 x 8192: 16.6, by four 19.2).
+template <int DT, int AK>
+void few_columns(const FewArgs& f, hipStream_t s) {
+    const int64_t n16 = (f.p.N + 15) / 16;
+    if constexpr (AK >= 0) {
+        if (n16 <= 512) few_go<DT, 1, 1, 4, AK>(f, s);
+        else few_go<DT, 2, 1, 2, AK>(f, s);
+    } else if (f.p.M <= 16) {
+        if (n16 <= 256) few_go<DT, 1, 1, 4, -1>(f, s);
+        else if (n16 <= 512) few_go<DT, 1, 1, 2, -1>(f, s);
+        else few_go<DT, 2, 1, 2, -1>(f, s);
+    } else if (f.p.M <= 32) {
+        if (n16 <= 256) few_go<DT, 1, 2, 2, -1>(f, s);
+        else few_go<DT, 2, 2, 1, -1>(f, s);
+    } else {
+        if (n16 <= 256) few_go<DT, 1, 4, 1, -1>(f, s);
+        else few_go<DT, 2, 4, 1, -1>(f, s);
+    }
+}
+
+// K = 4096 (32 stages, bf16, us by tiles of 64 / 128 / 256): 256 x 4096 10.7 / 20 / 46, 512 x 4096
+// 17 / 20.5 / 47, 2048 x 4096 58 / 36 / 50, 4096 x 4096 107 / 68 / 61, 8192 x 8192 423 /
+// 277 / 229; K = 8192: 4096 x 1024 53 / 39 / 81, 4096 x 128 15 / 34 / 79.
+constexpr TileTimes kTiles8[] = {{64, 512, 3, 0.2, 0.24, 0.45}, {128, 512, 6, 0.42, 0.45, 0.94},
+                                 {256, 256, 14, 0.9, 1.45, 1.45}};
+constexpr int kFewRows = 64;
+
+// what is streamed: few rows, or rows that the tiles cannot take
+bool streams(const ProductArgs& a, bool aligned) { return !aligned || a.M <= 16 || (a.M <= kFewRows && a.N <= 8192); }
+
 template <int DT>
 hipError_t product_run(const ProductArgs& a, hipStream_t s) {
     if (a.K == 0) {
         int8_bias_kernel<DT><<<dim3((unsigned)std::min<int64_t>((a.M * a.N + 255) / 256, 1 << 16)), 256, 0, s>>>(a);
         return hipGetLastError();
     }
-    const bool aligned = a.K % 16 == 0 && a.lda % 16 == 0 && (((uintptr_t)a.a | (uintptr_t)a.b) & 15) == 0;
-    const auto tiles = [&](auto kernel, int bt) {
-        const int64_t tm = (a.M + bt - 1) / bt, tn = (a.N + bt - 1) / bt;
-        kernel<<<dim3((unsigned)(tm * tn)), NT, 0, s>>>(a, (int)tm, (int)tn);
+    const bool aligned = a.lda % 16 == 0 && a.ldb % 16 == 0 && (((uintptr_t)a.a | (uintptr_t)a.b) & 15) == 0;
+    if (streams(a, aligned)) {
+        constexpr int64_t kMost = 65535 * kFewRows;  // rows a launch
+        for (int64_t m = 0; m < a.M; m += kMost) {
+            ProductArgs p = a;
+            p.a += m * a.lda;
+            p.a_scale += m;
+            p.Y = (typename elem_of<DT>::type*)a.Y + m * a.N;
+            p.M = std::min(a.M - m, kMost);
+            few_columns<DT, -1>({p, nullptr, 0}, s);
+        }
+        return hipGetLastError();
+    }
+    const auto count = [&](int bt) { return ((a.M + bt - 1) / bt) * ((a.N + bt - 1) / bt); };
+    const int bt = pick_tile(kTiles8, (a.K + 127) / 128, count);
+    const int64_t n = count(bt);
+    const auto tiles = [&](auto whole, auto ragged, int ks) {
+        const int tm = (int)((a.M + bt - 1) / bt), tn = (int)((a.N + bt - 1) / bt);
+        log_choice("int8_matmul: %lld x %lld x %d, tiles of %d%s", (long long)a.M, (long long)a.N, a.K, bt,
+                   ks > 1 ? ", two groups of waves" : "");
+        if (a.K % 128 == 0) whole<<<dim3((unsigned)n), NT * ks, 0, s>>>(a, tm, tn);
+        else ragged<<<dim3((unsigned)n), NT * ks, 0, s>>>(a, tm, tn);
     };
-    if (!aligned) tiles(int8_tile_kernel<128, DT, 2>, 128);
-    else if (a.M % 256 == 0 && a.N % 256 == 0 && a.K % 128 == 0 && (a.M / 256) * (a.N / 256) >= 256)
-        tiles(int8_tile_kernel<256, DT, 0>, 256);
-    else if (a.M % 128 == 0 && a.N % 128 == 0 && a.K % 128 == 0) tiles(int8_tile_kernel<128, DT, 0>, 128);
-    else tiles(int8_tile_kernel<128, DT, 1>, 128);
+    // where every tile has a CU of its own, two groups of waves take turns at the
+    // stages (1024 x 4096 x 4096: 25.9 -> 23.6 us)
+    if (bt == 64 && n <= 256) tiles(int8_tile_kernel<64, 4, 2, DT, false>, int8_tile_kernel<64, 4, 2, DT, true>, 2);
+    else if (bt == 64) tiles(int8_tile_kernel<64, 4, 1, DT, false>, int8_tile_kernel<64, 4, 1, DT, true>, 1);
+    else if (bt == 128 && n <= 256) tiles(int8_tile_kernel<128, 2, 2, DT, false>, int8_tile_kernel<128, 2, 2, DT, true>, 2);
+    else if (bt == 128) tiles(int8_tile_kernel<128, 2, 1, DT, false>, int8_tile_kernel<128, 2, 1, DT, true>, 1);
+    else tiles(int8_tile_kernel<256, 2, 1, DT, false>, int8_tile_kernel<256, 2, 1, DT, true>, 1);
     return hipGetLastError();
 }
 
@@ -330,23 +700,52 @@ hipError_t launch_quantize_rows(const void* X, int8_t* Q, float* scale, int64_t 
     return quantise_dt({X, Q, scale, M, K, (int)K}, dt, s);
 }
 
+// Operands whose K is no multiple of 16 are copied to rows that are, where the
+// tiles will take them: one read and one write, where streaming unaligned rows once
+// for every 64 rows of a costs more (300 x 2005 x 2048: 11 us, streamed 15).
+bool copies(int64_t M, int64_t K, int64_t N) { return K % 16 && M > 16 && !(M <= kFewRows && N <= 8192); }
+
 size_t int8_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, bool quantise) {
-    if (!quantise) return 0;
-    return align256((size_t)M * 4) + align256((size_t)M * (size_t)padded(K));
+    const size_t ld = (size_t)padded(K), copy = copies(M, K, N);
+    return (quantise ? align256((size_t)M * 4) : 0) + (quantise || copy ? align256((size_t)M * ld) : 0) +
+           (copy ? align256((size_t)N * ld) : 0);
 }
 
 hipError_t launch_int8_matmul(const Int8Args& x, int dt, void* ws, hipStream_t s) {
-    ProductArgs a = {(const int8_t*)x.a, (const int8_t*)x.b, x.a_scale, x.b_scale, x.bias, x.Y, x.M, x.N, x.K, (int)x.K};
+    ProductArgs a = {(const int8_t*)x.a, (const int8_t*)x.b, x.a_scale, x.b_scale, x.bias, x.Y, x.M, x.N, x.K, x.K, (int)x.K};
+    // one or two rows, which every workgroup of the product quantises for itself: 8.7 us for
+    // 1 row of 4096 x 4096, with a kernel before it 9.3 (8 rows: 12.8 and 9.4)
+    const int64_t kpad = (x.K + 127) / 128 * 128;
+    if (x.a_kind == dt && x.K > 0 && x.M <= 2 && kpad <= 16384) {
+        const FewArgs f = {a, x.a, (int)kpad};
+        if (dt == 0) few_columns<0, 0>(f, s);
+        else if (dt == 1) few_columns<1, 1>(f, s);
+        else few_columns<2, 2>(f, s);
+        return hipGetLastError();
+    }
+    const int64_t ld = padded(x.K);
+    const bool copy = copies(x.M, x.K, x.N);
+    char* w = (char*)ws;
+    const auto align = [&](const int8_t*& p, int64_t& stride, int64_t rows) {
+        int8_align_kernel<<<(unsigned)std::min<int64_t>((rows * (ld / 16) + 255) / 256, 8192), 256, 0, s>>>(
+            p, (int8_t*)w, rows, (int)x.K, ld);
+        p = (int8_t*)w;
+        stride = ld;
+        w += align256((size_t)rows * ld);
+    };
     if (x.a_kind >= 0) {
-        float* scale = (float*)ws;
-        int8_t* q = (int8_t*)ws + align256((size_t)x.M * 4);
-        const int64_t ld = padded(x.K);
-        const hipError_t e = quantise_dt({x.a, q, scale, x.M, ld, (int)x.K}, x.a_kind, s);
+        float* scale = (float*)w;
+        w += align256((size_t)x.M * 4);
+        const hipError_t e = quantise_dt({x.a, (int8_t*)w, scale, x.M, ld, (int)x.K}, x.a_kind, s);
         if (e != hipSuccess) return e;
-        a.a = q;
+        a.a = (int8_t*)w;
         a.lda = ld;
         a.a_scale = scale;
+        w += align256((size_t)x.M * ld);
+    } else if (copy) {
+        align(a.a, a.lda, x.M);
     }
+    if (copy) align(a.b, a.ldb, x.N);
     return dt == 0 ? product_run<0>(a, s) : dt == 1 ? product_run<1>(a, s) : product_run<2>(a, s);
 }
 
