@@ -11,9 +11,9 @@ namespace core16 {
 // tile.  Rows past the last are out of the buffer's range and read as zeros.
 // KT: so are the 16-byte pieces of a row past its end (ends: its bytes, a multiple of
 // 16); without it the last stage reads on into the next row.
-template <int R, bool KT = false>
+template <int R, bool KT = false, int WAVES = 4>
 struct RowSrc {
-    static constexpr int PER_WAVE = R / 32;
+    static constexpr int PER_WAVE = R / 8 / WAVES;
     static_assert(PER_WAVE % 2 == 0, "block parity == parity of the wave-local block index");
     const char* base;
     uint32_t ldb, bytes, ends;

@@ -45,6 +45,18 @@ def test_sizes(m, n, dt):
     check(G, got, 5, dt)
 
 
+@pytest.mark.parametrize("Z,m,n,dt", [(1, 4096, 4096, "f32"), (1, 2100, 3300, "bf16"), (6, 1000, 1024, "f32"),
+                                      (16, 1024, 1000, "bf16"), (1, 1500, 700, "f16")])
+def test_large(Z, m, n, dt):
+    """The larger tiles.  The definition on the GPU here, in 64 bits, by library products."""
+    G = torch.stack([draw(m, n, dt, rank=4, seed=z) for z in range(Z)]).cuda()
+    got, _ = om.orthogonalize(G)
+    for z in {0, Z - 1}:
+        want = orthogonalise(G[z], 5)
+        tol = orthogonalise_tol(G[z], want, 5, dt)
+        assert_within(got[z], want.cpu(), tol.cpu(), "%d of %d" % (z, Z))
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 8])
 @pytest.mark.parametrize("m,n", [(60, 90), (150, 70)])
 def test_steps(m, n, steps):

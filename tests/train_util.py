@@ -130,15 +130,40 @@ def orthogonalise(G, steps, dtype=torch.float64):
     return X.double()
 
 
+def _scalar_bound(x, steps):
+    """How far the steps may take one singular value x from its path, in units of e = 2^-22, which is what two
+    parts, or a product without lo lo, are off: A = x x is off by 2 e A, A A by 5 e A A, B = a + b A + c A A by
+    2 e |b| A + 5 e |c| A A + e |B|, and x' = B x by x times that plus 2 e |B x|, on top of |p'(x)| times what x
+    is off (to first order; one unit at the start)."""
+    a, b, c = COEFFICIENTS
+    off = torch.ones_like(x)
+    for _ in range(steps):
+        A = x * x
+        B = a + b * A + c * A * A
+        slope = (a + 3 * b * A + 5 * c * A * A).abs()
+        off = slope * off + x.abs() * (2 * abs(b) * A + 5 * abs(c) * A * A + 3 * B.abs())
+        x = B * x
+    return off
+
+
 def orthogonalise_tol(G, want, steps, dt):
     """The operands of a product are held to 22 bits where fp32 holds 24, so a rounding is up to 4 times one of
     the same steps in fp32, and the sums are alike.  Those steps' largest error, taken 4 times, twice over as
-    either one is a sample; and the rounding to T."""
-    worst = 0.0
-    for H in (G, -G.flip(0), G.flip(1)):  # (other orders of the same sums)
-        e = orthogonalise(H, steps, torch.float32) - orthogonalise(H, steps)
-        worst = max(worst, float(e.abs().max()))
-    tol = torch.full_like(want, 8 * worst + 2.0 ** -22 * float(want.abs().max()))
+    either one is a sample; and the rounding to T.
+
+    Where every row and column holds one value, or there is one row or column, the steps in fp32 are paths of
+    scalars, which may meet next to no error; their bound is counted instead (_scalar_bound)."""
+    nz = G != 0
+    if min(G.shape) == 1 or (int(nz.sum(0).max()) <= 1 and int(nz.sum(1).max()) <= 1):
+        X = G.double() / torch.linalg.vector_norm(G.double())
+        tol = 2.0 ** -22 * (_scalar_bound(X.abs(), steps) if min(G.shape) > 1
+                            else _scalar_bound(torch.ones_like(X), steps))
+    else:
+        worst = 0.0
+        for H in (G, -G.flip(0), G.flip(1)):  # (other orders of the same sums)
+            e = orthogonalise(H, steps, torch.float32) - orthogonalise(H, steps)
+            worst = max(worst, float(e.abs().max()))
+        tol = torch.full_like(want, 8 * worst + 2.0 ** -22 * float(want.abs().max()))
     return tol + half_step(dt, want.abs() + tol)
 
 
