@@ -332,12 +332,16 @@ PyObject* moe_balance(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t M = logits.size(0), E = logits.size(1);
         Out losses(nullptr, {2}, logits, at::kFloat), counts(nullptr, {E}, logits, at::kInt),
             tokens(nullptr, {1}, logits, at::kInt);
-        const Workspace ws = workspace(a[3], logits, [&] { return L.moe_balance_ws(M, E); });
         void* s = stream(logits);
-        call("omm_moe_balance", [&] {
-            return L.moe_balance(x.p, ids.p, mask.p, &losses.t, &counts.t, &tokens.t, ws.ptr(), ws.bytes(), s);
-        });
-        return pack({losses.x, counts.x, tokens.x});
+        const auto run = [&](void* ws, size_t bytes) {
+            call("omm_moe_balance", [&] {
+                return L.moe_balance(x.p, ids.p, mask.p, &losses.t, &counts.t, &tokens.t, ws, bytes, s);
+            });
+            return pack({losses.x, counts.x, tokens.x});
+        };
+        if (a[3] == Py_None && L.moe_balance_ws(M, E) == 0) return run(nullptr, 0);
+        const Workspace ws = workspace(a[3], logits, [&] { return L.moe_balance_ws(M, E); });
+        return run(ws.ptr(), ws.bytes());
     });
 }
 

@@ -587,12 +587,43 @@ __global__ __launch_bounds__(NT * KS, KS * NB * BT * 256 <= 80 * 1024 ? 2 * KS :
         tile_store<DT, TM>(a, acc, wr, wc, lane);
 }
 
-// Rows of K bytes at any byte -> rows of ld, a multiple of 16, zeros past K
-__global__ __launch_bounds__(256) void int8_align_kernel(const int8_t* x, int8_t* y, int64_t rows, int K, int64_t ld) {
-    const int per = (int)(ld / 16);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
-        const int k = (int)(i % per) * 16;
-        *(u32x4_t*)(y + i * 16) = bytes16(x + i / per * K + k, K - k);
+// Rows of K bytes at any byte -> rows of ld, a multiple of 16, zeros past K; of up to
+// two operands.  A piece is read as the five words around it and shifted into place
+// (16-byte loads at odd bytes run at a fraction of the rate).
+struct AlignArgs {
+    const int8_t* x[2];
+    int8_t* y[2];
+    int64_t rows[2];
+    int64_t ld;
+    int K;
+};
+// A wave takes a row.
+__global__ __launch_bounds__(256) void int8_align_kernel(AlignArgs a) {
+    const int64_t all = a.rows[0] + a.rows[1];
+    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < all; r += (int64_t)gridDim.x * 4) {
+        const int o = r >= a.rows[0];
+        const int64_t row = r - (o ? a.rows[0] : 0);
+        const int8_t *x = a.x[o], *from = x + row * a.K, *end = x + a.rows[o] * a.K;
+        int8_t* to = a.y[o] + row * a.ld;
+        const uint32_t by = (uint32_t)((uintptr_t)from & 3);
+        for (int k = (threadIdx.x & 63) * 16; k < a.ld; k += 1024) {
+            const int n = a.K - k;
+            const int8_t* p = from + k;
+            u32x4_t v;
+            if (p - by >= x && p + 20 <= end) {
+                const uint32_t* w = (const uint32_t*)(p - by);
+                const u32x4_t q = *(const u32x4_u4*)w;
+                const uint32_t e = w[4];
+                v = u32x4_t{__builtin_amdgcn_alignbyte(q.y, q.x, by), __builtin_amdgcn_alignbyte(q.z, q.y, by),
+                            __builtin_amdgcn_alignbyte(q.w, q.z, by), __builtin_amdgcn_alignbyte(e, q.w, by)};
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    if (n < 4 * d + 4) v[d] &= n <= 4 * d ? 0u : (1u << (8 * (n - 4 * d))) - 1u;
+            } else {
+                v = bytes16(p, n);
+            }
+            *(u32x4_t*)(to + k) = v;
+        }
     }
 }
 
@@ -726,13 +757,9 @@ hipError_t launch_int8_matmul(const Int8Args& x, int dt, void* ws, hipStream_t s
     const int64_t ld = padded(x.K);
     const bool copy = copies(x.M, x.K, x.N);
     char* w = (char*)ws;
-    const auto align = [&](const int8_t*& p, int64_t& stride, int64_t rows) {
-        int8_align_kernel<<<(unsigned)std::min<int64_t>((rows * (ld / 16) + 255) / 256, 8192), 256, 0, s>>>(
-            p, (int8_t*)w, rows, (int)x.K, ld);
-        p = (int8_t*)w;
-        stride = ld;
-        w += align256((size_t)rows * ld);
-    };
+    AlignArgs al = {};
+    al.ld = ld;
+    al.K = (int)x.K;
     if (x.a_kind >= 0) {
         float* scale = (float*)w;
         w += align256((size_t)x.M * 4);
@@ -743,9 +770,21 @@ hipError_t launch_int8_matmul(const Int8Args& x, int dt, void* ws, hipStream_t s
         a.a_scale = scale;
         w += align256((size_t)x.M * ld);
     } else if (copy) {
-        align(a.a, a.lda, x.M);
+        al.x[0] = a.a;
+        al.y[0] = (int8_t*)w;
+        al.rows[0] = x.M;
+        a.a = (int8_t*)w;
+        a.lda = ld;
+        w += align256((size_t)x.M * ld);
     }
-    if (copy) align(a.b, a.ldb, x.N);
+    if (copy) {
+        al.x[1] = a.b;
+        al.y[1] = (int8_t*)w;
+        al.rows[1] = x.N;
+        a.b = (int8_t*)w;
+        a.ldb = ld;
+        int8_align_kernel<<<(unsigned)std::min<int64_t>((al.rows[0] + al.rows[1] + 3) / 4, 1 << 16), 256, 0, s>>>(al);
+    }
     return dt == 0 ? product_run<0>(a, s) : dt == 1 ? product_run<1>(a, s) : product_run<2>(a, s);
 }
 

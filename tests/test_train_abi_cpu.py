@@ -81,8 +81,9 @@ def load(**change):
     (dict(ids=T((10,), I32)), -3), (dict(mask=T((4,), U8)), -3), (dict(losses=T((3,), F32)), -3),
     (dict(counts=T((9,), I32)), -3), (dict(tokens=T((2,), I32)), -3), (dict(x=T((5, 0), BF16), counts=T((0,), I32)), -3),
     (dict(x=T((5, 513), BF16), counts=T((513,), I32)), -5), (dict(ids=T((5, 17), I32)), -5),
-    (dict(x=T((2 ** 27, 8), BF16), ids=T((2 ** 27, 2), I32), mask=None), -5), (dict(ws=None), -6), (dict(n=64), -6),
-    (dict(ws=FAKE + 64), -6)])
+    (dict(x=T((2 ** 27, 8), BF16), ids=T((2 ** 27, 2), I32), mask=None), -5)] + [
+    (dict(x=T((300, 8), BF16), ids=T((300, 2), I32), mask=None, **ws), -6)
+    for ws in (dict(ws=None), dict(n=64), dict(ws=FAKE + 64))])
 def test_balance_refusals(change, code):
     assert load(**change) == code
 
@@ -107,7 +108,7 @@ def test_gradient_refusals(change, code):
 def test_router_empty():
     assert grad(x=T((0, 8), BF16), ids=T((0, 2), I64), g=None, mask=None, out=T((0, 8), BF16)) == 0
     size = om.lib().omm_moe_balance_workspace_size
-    assert size(0, 8) == 0 and size(5, 0) == 0 and size(5, 513) == 0 and size(5, 8) > 0
+    assert size(0, 8) == 0 and size(5, 0) == 0 and size(300, 513) == 0 and size(300, 8) > 0
 
 
 def ortho(G=T((6, 4), BF16), steps=5, out=T((6, 4), BF16), ws=FAKE, n=1 << 30):
