@@ -203,3 +203,44 @@ def test_nothing_outside_the_gradient():
     y = torch.full((37 * 21 + 512,), 7.0, device="cuda")
     om.moe_route_grad(x.cuda(), ids.cuda(), g.cuda(), grad_logits=y[256:256 + 37 * 21].view(37, 21))
     assert (y[:256] == 7).all() and (y[256 + 37 * 21:] == 7).all()
+
+
+@pytest.mark.parametrize("M,E,k,dt", [(45000, 72, 4, "bf16"), (30000, 200, 8, "f32"), (23000, 384, 6, "f16"), (21000, 333, 16, "bf16")])
+def test_several_turns(M, E, k, dt):
+    x, ids, mask, g = case(M, E, k, dt, 0.1, seed=E)
+    _, counts, tokens = check_balance(x, ids, mask)
+    check_grad(x, ids, mask, g, True, dt, torch.tensor([0.3 * M, 0.1 * M]), counts, tokens)
+
+
+@pytest.mark.parametrize("E", [40, 72, 160, 320, 512])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_wide_special_rows(E, dt, shift):
+    """The same expert in many selections, none, rows with hardly any expert left, rows that start on any element."""
+    x, ids, _, g = case(40, E, 16, dt, seed=E)
+    x[1, 1:] = -math.inf
+    x[2, : E - 1] = -math.inf
+    x[3, :] = -math.inf
+    ids[4, :] = E - 1
+    ids[5, ::2] = 3
+    ids[6, 1::2] = ids[6, 0]
+    ids[7, :], ids[8, 3:], ids[9, 5] = -1, E, -2 ** 31
+    mask = torch.ones((40,), dtype=torch.bool)
+    mask[11] = mask[38] = False
+    x[11, 0] = math.nan
+    buf = torch.zeros((40 * E + shift,), dtype=x.dtype)
+    buf[shift:] = x.reshape(-1)
+    y = buf.cuda()[shift:].view(40, E)
+    losses, counts, tokens = om.moe_balance(y, ids.cuda(), token_mask=mask.cuda())
+    (wl, wc, n), tol = balance(x, ids, mask)
+    assert torch.equal(counts.cpu().long(), wc) and int(tokens) == n
+    assert_within(losses, wl, tol + 1e-37, "losses")
+    gl = torch.tensor([12.0, 3.0])
+    for renorm in (False, True):
+        want, t = route_grad(x, ids, g, renorm, mask, counts.cpu().long(), n, gl, dt)
+        for inplace in (False, True):
+            z = y.clone() if not shift else torch.cat([y.new_zeros(shift), y.reshape(-1)])[shift:].view(40, E)
+            got = om.moe_route_grad(z, ids.cuda(), g.cuda(), renormalize=renorm, token_mask=mask.cuda(), counts=counts,
+                                    tokens=tokens, grad_losses=gl.cuda(), grad_logits=z if inplace else None)
+            assert_within(got, want, t, "gradient")
+            assert (got[11] == 0).all() and (got[38] == 0).all()
