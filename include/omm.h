@@ -408,6 +408,7 @@ int omm_quantize_rows(const omm_tensor* X, omm_tensor* Q, omm_tensor* scale, voi
  * OMM_ERR_SHAPE (also a_scale with an a of T), OMM_ERR_UNSUPPORTED, OMM_ERR_WORKSPACE.
  */
 #define OMM_INT8_MAX_K 131071
+#define OMM_INT8_MAX_N 134217728
 size_t omm_int8_matmul_workspace_size(int64_t M, int64_t K, int64_t N, int32_t a_dtype);
 int omm_int8_matmul(const omm_tensor* a, const omm_tensor* a_scale, const omm_tensor* b, const omm_tensor* b_scale,
                     const omm_tensor* bias, omm_tensor* Y, void* workspace, size_t workspace_bytes, void* stream);

@@ -988,7 +988,8 @@ int omm_int8_matmul(const omm_tensor* a, const omm_tensor* a_scale, const omm_te
     if ((rc = check_f32_vec(a_scale, M)) || (rc = check_f32_vec(b_scale, N))) return rc;
     if ((bias && !has_shape(bias, 1, N)) || !has_shape(Y, 2, M, N)) return OMM_ERR_SHAPE;
     if (M == 0 || N == 0) return OMM_OK;
-    if (K > OMM_INT8_MAX_K || M > kMaxIndex || N > kMaxIndex || blocks(M, 64) * blocks(N, 64) > kMaxBlocks)
+    if (K > OMM_INT8_MAX_K || M > kMaxIndex || N > kMaxIndex || blocks(M, 64) * blocks(N, 64) > kMaxBlocks ||
+        N > OMM_INT8_MAX_N)  // (512 threads for 32 columns, and fewer than 2^32 in a launch)
         return OMM_ERR_UNSUPPORTED;
     if ((rc = check_workspace(workspace, workspace_bytes, omm::int8_matmul_workspace_bytes(M, K, N, a_kind >= 0))))
         return rc;

@@ -129,3 +129,10 @@ def test_orthogonalize_refusals():
         assert ortho(G=T(shape, BF16), out=T(shape, BF16)) == 0
     size = om.lib().omm_orthogonalize_workspace_size
     assert size(1, 6, 4) > 0 and size(0, 6, 4) == 0 and size(1, 65537, 4) == 0 and size(1, 6, 0) == 0
+
+
+def test_product_columns_of_a_launch():
+    N = 2 ** 27 + 1
+    wide = dict(b=T((N, 32), I8), sb=T((N,), F32), bias=None)
+    assert product(Y=T((4, N), BF16), **wide) == -5
+    assert product(a=T((1, 32), BF16), sa=None, Y=T((1, N), BF16), ws=FAKE, n=1 << 40, **wide) == -5
