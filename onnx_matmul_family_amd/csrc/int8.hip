@@ -198,13 +198,21 @@ struct ProductArgs {
 };
 
 typedef u32x4_t u32x4_u1 __attribute__((aligned(1)));
-// 16 bytes at p, zeros from the n-th on
+// 16 bytes at p, zeros from the n-th on, as the whole words that hold them, shifted into
+// place: no branch, as every load by itself would be a round trip.  p is inside the operand
+// for any n.  (A word that holds a byte of the operand is of its memory.)
 __device__ __forceinline__ u32x4_t bytes16(const int8_t* p, int n) {
-    if (n >= 16) return *(const u32x4_u1*)p;
-    u32x4_t v = {0, 0, 0, 0};
+    const uint32_t by = (uint32_t)((uintptr_t)p & 3);
+    const int last = (int)by + max(min(n, 16), 1) - 1;  // byte of the last word, from the first word's start
+    uint32_t w[5];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (e < n) v[e >> 2] |= (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
+    for (int j = 0; j < 5; ++j) w[j] = *(const uint32_t*)(p - by + min(4 * j, last & ~3));
+    u32x4_t v;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        v[d] = __builtin_amdgcn_alignbyte(w[d + 1], w[d], by);
+        if (n < 4 * d + 4) v[d] &= n <= 4 * d ? 0u : (1u << (8 * (n - 4 * d))) - 1u;
+    }
     return v;
 }
 __device__ __forceinline__ i32x4_t mfma_i8(u32x4_t a, u32x4_t b, i32x4_t c) {
@@ -280,32 +288,40 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few_kernel(FewArgs f) {
     const int lr = lane >> 3, lp = lane & 7;  // row of 8 and piece that the lane loads
     const int nfull = K / 128;  // whole units; what is left of k is one more, of wave nfull % 8
     const int64_t n0 = (int64_t)blockIdx.x * (16 * NF);
-    const auto load = [&](u32x4_t (&w)[NF][2], u32x4_t (&x)[XG ? XG : 1][2], int u, auto piece) __attribute__((always_inline)) {
-        const int k = u * 128 + lp * 16;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int g = 0; g < NF; ++g)
-                w[g][i] = piece(a.b + min(n0 + 16 * g + 8 * i + lr, a.N - 1) * a.ldb, k);
-#pragma unroll
-            for (int g = 0; g < XG; ++g) x[g][i] = piece(a.a + (int64_t)min(16 * g + 8 * i + lr, M - 1) * a.lda, k);
-        }
-    };
+    const auto b_row = [&](int g, int i) { return a.b + min(n0 + 16 * g + 8 * i + lr, a.N - 1) * a.ldb; };
+    const auto a_row = [&](int g, int i) { return a.a + (int64_t)min(16 * g + 8 * i + lr, M - 1) * a.lda; };
     u32x4_t w[2][U][NF][2], x[2][U][XG ? XG : 1][2], wt[NF][2], xt[XG ? XG : 1][2];
     // step s: U units of each wave
     constexpr int STEP = U * kFewWaves;
     const auto loads = [&](auto set, int step) __attribute__((always_inline)) {
         static_for<0, U>([&](auto u) {
             const int at = step * STEP + u * kFewWaves + wave;
-            if (at < nfull) load(w[set][u], x[set][u], at, [](const int8_t* p, int k) { return *(const u32x4_u1*)(p + k); });
+            if (at < nfull) {
+                const int k = at * 128 + lp * 16;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int g = 0; g < NF; ++g) w[set][u][g][i] = *(const u32x4_u1*)(b_row(g, i) + k);
+#pragma unroll
+                    for (int g = 0; g < XG; ++g) x[set][u][g][i] = *(const u32x4_u1*)(a_row(g, i) + k);
+                }
+            }
         });
     };
     constexpr std::integral_constant<int, 0> first = {};
     constexpr std::integral_constant<int, 1> second = {};
     const bool tail = K % 128 != 0 && wave == nfull % kFewWaves;
     const auto load_tail = [&]() __attribute__((always_inline)) {
-        if (tail)
-            load(wt, xt, nfull, [&](const int8_t* p, int k) { return bytes16(p + min(k, K), max(0, min(16, K - k))); });
+        if (tail) {
+            const int k = nfull * 128 + lp * 16, n = max(0, min(16, K - k));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int g = 0; g < NF; ++g) wt[g][i] = bytes16(b_row(g, i) + min(k, K - 1), n);
+#pragma unroll
+                for (int g = 0; g < XG; ++g) xt[g][i] = bytes16(a_row(g, i) + min(k, K - 1), n);
+            }
+        }
     };
     // this wave's pieces: [NF + XG][16 rows][8], those of a row in the order piece ^ row
     u32x4_t* own = smem + wave * ((NF + XG) * UNIT);
@@ -676,7 +692,7 @@ void few_columns(const FewArgs& f, hipStream_t s) {
         if (n16 <= 256) few_go<DT, 1, 2, 2, -1>(f, s);
         else few_go<DT, 2, 2, 1, -1>(f, s);
     } else {
-        if (n16 <= 256) few_go<DT, 1, 4, 1, -1>(f, s);
+        if (n16 * ((f.p.M + 63) / 64) <= 256) few_go<DT, 1, 4, 1, -1>(f, s);
         else few_go<DT, 2, 4, 1, -1>(f, s);
     }
 }
@@ -739,10 +755,14 @@ hipError_t launch_quantize_rows(const void* X, int8_t* Q, float* scale, int64_t 
     return quantise_dt({X, Q, scale, M, K, (int)K}, dt, s);
 }
 
-// Operands whose K is no multiple of 16 are copied to rows that are, where the
-// tiles will take them: one read and one write, where streaming unaligned rows once
-// for every 64 rows of a costs more (300 x 2005 x 2048: 11 us, streamed 15).
-bool copies(int64_t M, int64_t K, int64_t N) { return K % 16 && M > 16 && !(M <= kFewRows && N <= 8192); }
+// Operands whose K is no multiple of 16 are copied to rows that are, where the tiles will
+// take them.  They are streamed up to 128 rows (100 x 2005 x 8192: 17.1 us, copied
+// 19.4) and where every CU has one workgroup of 64 rows and 32 columns at most (300 x 2005 x
+// 512: 7.6 and 11.9); beyond, streaming b for every 64 rows costs more (300 x 2005 x 8192:
+// 38 and 27).
+bool copies(int64_t M, int64_t K, int64_t N) {
+    return K % 16 && M > 128 && (M + 63) / 64 * ((N + 31) / 32) > 256;
+}
 
 size_t int8_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, bool quantise) {
     const size_t ld = (size_t)padded(K), copy = copies(M, K, N);
