@@ -13,7 +13,7 @@
 // in 128 tiles of 64, 1 MB each, 14.3 us).  Many tiles, the matrix unit: 8192 x 4096 x
 // 8192 in 237 us beside other work and 229 alone, 2.3 to 2.4 POP/s, where the library's
 // int8 product of 8192^3 reaches 2.5.  Quantising is one read and one write: 8192 x 4096 bf16
-// in 18.7 us, 5.4 TB/s of the 6.06 that a copy reaches.
+// in 17.6 us, 5.7 TB/s of the 6.06 that a copy reaches, 8192 x 4095 in 18.1.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -43,43 +43,79 @@ struct QuantArgs {
 typedef u32x2_t u32x2_u1 __attribute__((aligned(1)));
 typedef uint32_t u32_u1 __attribute__((aligned(1)));
 
-// 127 x / amax to the nearest integer, as bytes.  x * inv is within 1.6e-5 of it (two
-// roundings of values up to 127), so only what lies closer than that to the border
-// of two steps is divided in 64 bits; so is every value of a row whose inv is 0
-// (amax too small for one).
+// Largest magnitude, as bits of fp32; of 16-bit types as their own bits, two at a time
+template <int DT>
+struct RowMax {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    uint32_t m = 0;
+    __device__ __forceinline__ void add(u32x4_t v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == 2)
+                m = max(m, v[i] & 0x7fffffffu);
+            else
+                m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, m),
+                                                                           __builtin_bit_cast(u16x2_t, v[i] & 0x7fff7fffu)));
+        }
+    }
+    __device__ __forceinline__ uint32_t bits() const {
+        if constexpr (DT == 2) return m;
+        else return __float_as_uint(from_bits<DT>((uint16_t)max(m & 0xffffu, m >> 16)));
+    }
+};
+
+// 127 x / amax to the nearest integer, as bytes.  x * inv is within 7.6e-6 of it (127 /
+// amax is rounded once, the product not at all), and adding 1.5 2^23 rounds that to an
+// integer, whose two's complement is then the low bits.  What lies within 1e-5 of the
+// border h / 2 (h odd) of two steps is decided by the sign of 254 x - h amax, exactly: with
+// p = fp32(h amax), 254 x - p and h amax - p both fit fp32 (halves of 2^-8 of them
+// here, so that neither passes its range; amax is 2^-100 or more).
 template <int V>
 __device__ __forceinline__ void quantise(const float* f, float amax, float inv, uint32_t (&w)[V / 4]) {
-    float q[V];
-    bool exact = inv == 0.0f;
+    constexpr float kRound = 12582912.0f;
+    float r[V], off = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float t = f[i] * inv;
-        q[i] = rintf(t);
-        exact |= fabsf(t - q[i]) > 0.49996f;
+        r[i] = fmaf(f[i], inv, kRound);
+        off = fmaxf(off, fabsf(fmaf(f[i], inv, kRound - r[i])));
     }
-    if (exact) {
+    if (off > 0.49999f) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) q[i] = (float)rint((double)f[i] * 127.0 / (double)amax);
+        for (int i = 0; i < V; ++i) {
+            const float q = r[i] - kRound, d = fmaf(f[i], inv, -q);
+            const float h = 2.0f * q + (d > 0.0f ? 1.0f : -1.0f), p = h * 0x1p-9f * amax;
+            const float x = fmaf(f[i], 254.0f * 0x1p-9f, -p), y = fmaf(h * 0x1p-9f, amax, -p);
+            const float below = 0.5f * h - 0.5f, even = 2.0f * rintf(0.25f * h);
+            if (fabsf(d) > 0.49999f) r[i] = kRound + (x > y ? below + 1.0f : x < y ? below : even);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) w[i / 4] |= ((uint32_t)(int)q[i] & 255u) << (8 * (i & 3));
+    for (int i = 0; i < V / 4; ++i) {
+        const float* b = r + 4 * i;
+        w[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(__float_as_uint(b[3]), __float_as_uint(b[2]), 0x0400u),
+                                     __builtin_amdgcn_perm(__float_as_uint(b[1]), __float_as_uint(b[0]), 0x0400u), 0x05040100u);
+    }
 }
 // What a row's largest magnitude (as bits) makes of it.  A row that holds a NaN or
 // an infinity: scale NaN and values 0.
 struct RowScale {
     float amax, inv, scale;
-    bool zero;
+    bool zero, tiny;
     __device__ __forceinline__ explicit RowScale(uint32_t mx) {
         const bool finite = mx < 0x7f800000u;
         amax = __uint_as_float(mx);
         scale = finite ? amax / 127.0f : __builtin_nanf("");
         zero = !finite || mx == 0;
-        inv = !zero && amax >= 0x1p-100f ? 127.0f / amax : 0.0f;
+        tiny = amax < 0x1p-100f;  // then 2^60 times all of it, which no fp32 is too small for
+        if (tiny) amax *= 0x1p60f;
+        inv = 127.0f / amax;
     }
     template <int V>
-    __device__ __forceinline__ void bytes(const float* f, uint32_t (&w)[V / 4]) const {
+    __device__ __forceinline__ void bytes(float* f, uint32_t (&w)[V / 4]) const {
+        if (tiny) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] *= 0x1p60f;
+        }
         if (zero) {
 #pragma unroll
             for (int i = 0; i < V / 4; ++i) w[i] = 0;
@@ -89,7 +125,8 @@ struct RowScale {
     }
 };
 
-// NW waves a row, C 16-byte chunks a lane (C = 0: rows of any length, read twice)
+// NW waves a row, C 16-byte chunks a lane (C = 0: rows of any length, read twice).  The
+// last chunk ends with the row (its first values are the one's before it too, and written twice).
 template <int DT, int NW, int C>
 __global__ __launch_bounds__(NW <= 4 ? 256 : 64 * NW) void quantise_kernel(QuantArgs a) {
     typedef typename elem_of<DT>::type E;
@@ -100,22 +137,17 @@ __global__ __launch_bounds__(NW <= 4 ? 256 : 64 * NW) void quantise_kernel(Quant
     const bool here = m < a.M;
     const E* row = (const E*)a.X + (here ? m : a.M - 1) * K;
     u32x4_t v[C ? C : 1];
-    uint32_t mx = 0;
-    const auto largest = [&](u32x4_t w) {
-        float f[V];
-        unpack16<DT>(w, f);
-#pragma unroll
-        for (int i = 0; i < V; ++i) mx = max(mx, __float_as_uint(f[i]) & 0x7fffffffu);
-    };
+    RowMax<DT> largest;
+    const auto load = [&](int64_t e) { return K >= V ? load16(row + min(e, (int64_t)(K - V))) : load16_first(row, K); };
     if constexpr (C) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) v[c] = load16_first(row + min((c * NL + l) * V, K), max(0, K - (c * NL + l) * V));
+        for (int c = 0; c < C; ++c) v[c] = load((c * NL + l) * V);
 #pragma unroll
-        for (int c = 0; c < C; ++c) largest(v[c]);
+        for (int c = 0; c < C; ++c) largest.add(v[c]);
     } else {
-        for (int64_t e = (int64_t)l * V; e < K; e += NL * V) largest(load16_first(row + e, (int)min((int64_t)V, K - e)));
+        for (int64_t e = (int64_t)l * V; e < K; e += NL * V) largest.add(load(e));
     }
-    mx = wave_max_u32(mx);
+    uint32_t mx = wave_max_u32(largest.bits());
     if constexpr (NW > 1) {
         if ((t & 63) == 0) part[t >> 6] = mx;
         __syncthreads();
@@ -132,27 +164,26 @@ __global__ __launch_bounds__(NW <= 4 ? 256 : 64 * NW) void quantise_kernel(Quant
         uint32_t w[V / 4];
         unpack16<DT>(v, f);
         rs.bytes<V>(f, w);
-        if (a.ldq - e >= V) {
-            if constexpr (V == 8) *(u32x2_u1*)(q + e) = u32x2_t{w[0], w[1]};
-            else *(u32_u1*)(q + e) = w[0];
+        if (K >= V) {
+            int8_t* d = q + min(e, (int64_t)(K - V));
+            if constexpr (V == 8) *(u32x2_u1*)d = u32x2_t{w[0], w[1]};
+            else *(u32_u1*)d = w[0];
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (e + i < a.ldq) q[e + i] = (int8_t)(w[i / 4] >> (8 * (i & 3)));
+                if (i < K) q[i] = (int8_t)(w[i / 4] >> (8 * (i & 3)));
         }
     };
     if constexpr (C) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int e = (c * NL + l) * V;
-            if (e < a.ldq) out(e, v[c]);
+            if (e < K) out(e, v[c]);
         }
     } else {
-        for (int64_t e = (int64_t)l * V; e < a.ldq; e += NL * V) {
-            const int n = (int)max((int64_t)0, min((int64_t)V, K - e));
-            out(e, load16_first(row + min(e, (int64_t)K), n));
-        }
+        for (int64_t e = (int64_t)l * V; e < K; e += NL * V) out(e, load(e));
     }
+    for (int64_t e = K + l; e < a.ldq; e += NL) q[e] = 0;
 }
 
 template <int DT>
@@ -170,7 +201,7 @@ hipError_t quantise_run(const QuantArgs& a, hipStream_t s) {
             kernel<<<dim3((unsigned)((p.M + rows - 1) / rows)), nw <= 4 ? 256 : 64 * nw, 0, s>>>(p);
         }
     };
-    const int64_t chunks = (a.ldq + V - 1) / V;  // of 16 bytes of X
+    const int64_t chunks = ((int64_t)a.K + V - 1) / V;  // of 16 bytes of X
     if (chunks <= 64) go(quantise_kernel<DT, 1, 1>, 1);
     else if (chunks <= 128) go(quantise_kernel<DT, 1, 2>, 1);
     else if (chunks <= 256) go(quantise_kernel<DT, 4, 1>, 4);
@@ -337,13 +368,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few_kernel(FewArgs f) {
         const int l = (wave % waves) * 64 + lane;
         const E* X = (const E*)f.X + (int64_t)min(row, M - 1) * K;
         u32x4_t keep[KEEP];
-        uint32_t mx = 0;
-        const auto largest = [&](u32x4_t v) {
-            float e[V];
-            unpack16<AK>(v, e);
-#pragma unroll
-            for (int i = 0; i < V; ++i) mx = max(mx, __float_as_uint(e[i]) & 0x7fffffffu);
-        };
+        RowMax<AK> largest;
         const auto vec = [&](int c) {
             const int e = (c * nl + l) * V;
             return load16_first(X + min(e, K), max(0, min(V, K - e)));
@@ -353,9 +378,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few_kernel(FewArgs f) {
         loads(first, 0);
         load_tail();
 #pragma unroll
-        for (int c = 0; c < KEEP; ++c) largest(keep[c]);
-        for (int c = KEEP; c * nl * V < K; ++c) largest(vec(c));
-        mx = wave_max_u32(mx);
+        for (int c = 0; c < KEEP; ++c) largest.add(keep[c]);
+        for (int c = KEEP; c * nl * V < K; ++c) largest.add(vec(c));
+        uint32_t mx = wave_max_u32(largest.bits());
         if (lane == 0) max_s[wave] = mx;
         __syncthreads();
         // (a row's waves are neighbours: lanes past them look at the first again)

@@ -215,3 +215,23 @@ def test_weights_by_rows_in_a_run():
         bound = 0.5 * (sx[:, None] * W.double().abs().sum(1)[None, :] + X.double().abs().sum(1)[:, None] * sv[None, :]) \
             + 0.25 * 320 * sx[:, None] * sv[None, :]
         assert ((y.double().cpu() - full).abs() <= bound + 2.0 ** -8 * full.abs() + 1e-3).all()
+
+
+@pytest.mark.parametrize("M,K,N", [(200, 257, 2080), (1100, 65, 500), (300, 2005, 2048), (130, 33, 4100)])
+@pytest.mark.parametrize("dt,bias", [("bf16", False), ("f16", True), ("f32", True)])
+def test_odd_rows_copied(M, K, N, dt, bias):
+    check_product(M, K, N, dt, bias, seed=M + K)
+
+
+@pytest.mark.parametrize("off", [1, 6])
+@pytest.mark.parametrize("M,K,N", [(1100, 65, 500), (700, 99, 512), (3, 131, 40), (64, 127, 8200)])
+def test_odd_rows_at_any_base(M, K, N, off):
+    """Streamed and copied rows of odd lengths that start anywhere, between other data."""
+    gen = torch.Generator().manual_seed(M + off)
+    buf_a = torch.randint(-128, 128, (M * K + off + 8,), generator=gen).to(torch.int8).cuda()
+    buf_b = torch.randint(-128, 128, (N * K + off + 9,), generator=gen).to(torch.int8).cuda()
+    a, b = buf_a[off:off + M * K].view(M, K), buf_b[off + 1:off + 1 + N * K].view(N, K)
+    sa, sb = torch.rand((M,), generator=gen).cuda(), torch.rand((N,), generator=gen).cuda()
+    got, _ = om.int8_matmul(a, b, sb, a_scale=sa, dtype=torch.float32)
+    want, tol = int8_product(a.cpu(), sa.cpu(), b.cpu(), sb.cpu(), None, "f32")
+    assert_within(got, want, tol, "product")
