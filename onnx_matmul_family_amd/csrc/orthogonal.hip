@@ -83,13 +83,14 @@ __device__ __forceinline__ u32x2_t transpose4(u32x2_t v, int lane) {
 }
 
 // ------------------------------------------------------------------ G / |G|
-// sum of the squares of one matrix, in 64 bits: parts[z][block]
+// sum of the squares of one matrix, in 64 bits: parts[z][block]; and the join's counters are cleared
 template <int DT>
-__global__ __launch_bounds__(256) void ortho_norm_kernel(const void* G, int64_t mn, double* parts) {
+__global__ __launch_bounds__(256) void ortho_norm_kernel(const void* G, int64_t mn, double* parts, uint32_t* joined, int njoined) {
     typedef typename elem_of<DT>::type E;
     constexpr int V = kVec<DT>;
     __shared__ double red[4];
     const E* g = (const E*)G + (int64_t)blockIdx.y * mn;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < njoined) joined[threadIdx.x] = 0;
     double s = 0.0;
     for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; e < mn; e += (int64_t)gridDim.x * 256 * V) {
         float f[V];
@@ -353,7 +354,12 @@ struct OrthoK {
     int m, n;           // of out: (rows, cols) without padding, or (cols, rows) of a tall G
     int tall;
     int tiles;          // of one matrix
+    // kGram of few tiles and a long contraction: `split` workgroups a tile, whose sums meet here
+    int split;
+    uint64_t* sums;     // [tile][split][wave][2 TM TM][64], pairs of fp32
+    uint32_t* joined;   // [tile]: workgroups whose sums are there; 0 before and after a launch
 };
+constexpr int kSplitPlaces = 256;  // workgroups of a launch that is split
 
 // DT: 3 = in two parts, else T of the last step's result
 // H: side of a wave's block
@@ -364,7 +370,9 @@ __global__ __launch_bounds__(BT == 32 ? 512 : NT, NB * BT * 256 <= 80 * 1024 ? 2
     __shared__ __attribute__((aligned(1024))) char smem[SMALL ? SmallLoop::LDS : NB * BT * 256];
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = SMALL ? 0 : wave >> 1, wn = SMALL ? 0 : wave & 1;
-    const int w = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+    constexpr bool SPLIT = OP == kGram && BT <= 64;
+    const int wall = xcd_remap((int)blockIdx.x, (int)gridDim.x), part = SPLIT ? wall % a.split : 0;
+    const int w = SPLIT ? wall / a.split : wall;
     const int z = w / a.tiles;
     int tm, tn, i = w - z * a.tiles;
     const int T = (a.rows + BT - 1) / BT;
@@ -403,12 +411,17 @@ __global__ __launch_bounds__(BT == 32 ? 512 : NT, NB * BT * 256 <= 80 * 1024 ? 2
     };
     if constexpr (OP == kPoly && AHEAD) load_c(wr);
     f32x4_t acc[TM][TM];
-    const int nk = a.K / 32;
+    const int from = SPLIT ? part * (a.K / 32) / a.split : 0;  // stages of this part
+    const int nk = (SPLIT ? (part + 1) * (a.K / 32) / a.split : a.K / 32) - from;
     const uint16_t *A = a.A + (int64_t)z * 2 * a.rows * a.K, *B = a.B + (int64_t)z * 2 * a.cols * a.K;
     if constexpr (SMALL) {
         SmallLoop::S sa, sb;
         sa.init(A, a.K * 4, a.K * 4, m0, a.rows, lane);
         sb.init(B, a.K * 4, a.K * 4, n0, a.cols, lane);
+        if constexpr (SPLIT) {
+            sa.skip(from);
+            sb.skip(from);
+        }
         SmallLoop::run(acc, smem, sa, sb, nk, lane, wave);
     } else {
         typedef typename std::conditional<SYM, RowSrc<BT>, ColSrc<BT>>::type SB;
@@ -417,6 +430,10 @@ __global__ __launch_bounds__(BT == 32 ? 512 : NT, NB * BT * 256 <= 80 * 1024 ? 2
         sa.init(A, a.K * 4, a.K * 4, m0, a.rows, lane);
         if constexpr (SYM) sb.init(B, a.K * 4, a.K * 4, n0, a.cols, lane);
         else sb.init(B, a.cols, a.K, n0, wave, lane);
+        if constexpr (SPLIT) {
+            sa.skip(from);
+            sb.skip(from);
+        }
         // B X: a x, the largest part of a result in the first steps, comes with the stages
         // of the diagonal; as the last ones, so that the other terms are summed by themselves
         // and not on top of it (1000 x 1000 in fp32: 2.0e-6 -> 1.7e-6 off)
@@ -426,6 +443,42 @@ __global__ __launch_bounds__(BT == 32 ? 512 : NT, NB * BT * 256 <= 80 * 1024 ? 2
     }
 
     __syncthreads();  // every wave is done with the last stage
+    if constexpr (SPLIT) {
+        // the last of a tile's workgroups to be here sums what all of them left, in their order
+        if (a.split > 1) {
+            constexpr int WAVES = SMALL ? 1 : 4, N = 2 * TM * TM;  // pairs of a lane
+            uint64_t* mine = a.sums + ((int64_t)w * a.split * WAVES + wave) * (N * 64) + lane;
+            constexpr int64_t PART = WAVES * N * 64;
+            if (wave < WAVES) {
+#pragma unroll
+                for (int x = 0; x < N; ++x) {
+                    const f32x4_t& v = acc[x / 2 / TM][x / 2 % TM];
+                    const float pair[2] = {v[x % 2 * 2], v[x % 2 * 2 + 1]};
+                    __hip_atomic_store(mine + part * PART + x * 64, __builtin_bit_cast(uint64_t, pair), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+                }
+            }
+            if (!part_last(a.joined + w, a.split, t)) return;
+            if (wave < WAVES) {
+                float sum[2 * N] = {};
+#pragma unroll 2
+                for (int p = 0; p < a.split; ++p) {
+                    uint64_t u[N];
+#pragma unroll
+                    for (int x = 0; x < N; ++x)
+                        u[x] = __hip_atomic_load(mine + p * PART + x * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+                    for (int x = 0; x < N; ++x) {
+                        sum[2 * x] += __uint_as_float((uint32_t)u[x]);
+                        sum[2 * x + 1] += __uint_as_float((uint32_t)(u[x] >> 32));
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 2 * N; ++x) acc[x / 4 / TM][x / 4 % TM][x % 4] = sum[x];
+            }
+            if (t == 0) __hip_atomic_store(a.joined + w, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
     if (SMALL && wave) return;
     if constexpr (OP == kPoly && !AHEAD) load_c(wr);
 #pragma unroll
@@ -545,13 +598,52 @@ int64_t tiles_of(const OrthoK& k, bool sym, int bt) {
     return sym ? tm * (tm + 1) / 2 : tm * tn;
 }
 
+// A = X X^T (p x p, contraction q) of tiles that leave CUs without one: by how many
+// workgroups a tile's contraction is split, and the tile.  (The whole call, us, with one
+// workgroup a tile and split: 64 x 2496 108 and 98, 96 x 4096 133 and 116, 384 x 3840 180 and
+// 166, 18 of 3200 x 192 327 and 290; the parts pass the L2, as a fence for every workgroup's
+// stores made the last 420.)
+struct GramPlan {
+    int bt, split;
+    int64_t tiles;  // of the batch
+    size_t sums_bytes() const { return split > 1 ? (size_t)tiles * split * bt * bt * 4 : 0; }
+};
+GramPlan gram_plan(int64_t Z, int64_t p, int64_t q) {
+    constexpr double kJoin = 5.0;  // us, as measured (3: 512 x 1472 140 -> 142)
+    OrthoK k = {};
+    k.rows = k.cols = (int)p;
+    const double stages = (double)(q / 32);
+    GramPlan best = {};
+    double least = 0.0;
+    for (const TileTimes& t : kSymTiles) {
+        const int64_t n = Z * tiles_of(k, true, t.bt);
+        for (int split = 1; split <= 16; split *= 2) {
+            if (split > 1 && (t.bt > 64 || n * split > kSplitPlaces || stages < 8 * split)) break;
+            const double time = tile_time(t, n * split, stages / split) + (split > 1 ? kJoin : 0.0);
+            if (!best.bt || time < least) {
+                best = {t.bt, split, n};
+                least = time;
+            }
+        }
+    }
+    return best;
+}
+
 template <int OP, int DT>
 void product(OrthoK k, int64_t Z, hipStream_t s) {
     const auto count = [&](int bt) { return Z * tiles_of(k, OP != kUpdate, bt); };
-    const int bt = OP == kUpdate ? pick_tile(kUpdateTiles, k.K / 32, count) : pick_tile(kSymTiles, k.K / 32, count);
-    log_choice("orthogonalize: %d x %d x %d, tiles of %d", k.rows, k.cols, k.K, bt);
+    int bt;
+    k.split = 1;
+    if constexpr (OP == kGram) {
+        const GramPlan plan = gram_plan(Z, k.rows, k.K);
+        bt = plan.bt;
+        k.split = plan.split;
+    } else {
+        bt = OP == kUpdate ? pick_tile(kUpdateTiles, k.K / 32, count) : pick_tile(kSymTiles, k.K / 32, count);
+    }
+    log_choice("orthogonalize: %d x %d x %d, tiles of %d, %d workgroups each", k.rows, k.cols, k.K, bt, k.split);
     k.tiles = (int)tiles_of(k, OP != kUpdate, bt);
-    const unsigned grid = (unsigned)(k.tiles * Z);
+    const unsigned grid = (unsigned)(k.tiles * Z * k.split);
     if (bt == 32) {
         if constexpr (OP != kUpdate) ortho_kernel<OP, DT, 32, 2><<<grid, 512, 0, s>>>(k);
     } else if (bt == 64) ortho_kernel<OP, DT, 64, 4><<<grid, NT, 0, s>>>(k);
@@ -574,12 +666,17 @@ hipError_t ortho_run(const OrthoArgs& o, void* ws, hipStream_t s) {
     }
     uint16_t* A = (uint16_t*)w;
     uint16_t* B = (uint16_t*)(w + align256((size_t)Z * 4 * p * p));
+    w += 2 * align256((size_t)Z * 4 * p * p);
+    const GramPlan plan = gram_plan(Z, p, q);
+    OrthoK k;
+    k.joined = (uint32_t*)w;
+    k.sums = (uint64_t*)(w + kSplitPlaces * 4);
     const int nparts = (int)std::min<int64_t>(kNormBlocks, (mn + 8191) / 8192);
-    ortho_norm_kernel<DT><<<dim3(nparts, (unsigned)Z), 256, 0, s>>>(o.G, mn, parts);
+    ortho_norm_kernel<DT><<<dim3(nparts, (unsigned)Z), 256, 0, s>>>(o.G, mn, parts, k.joined,
+                                                                    plan.split > 1 ? (int)plan.tiles : 0);
     const int64_t tiles = ((p + 63) / 64) * ((q + 63) / 64);
     ortho_split_kernel<DT><<<dim3((unsigned)tiles, (unsigned)Z), 256, 0, s>>>(
         o.G, (int)o.m, (int)o.n, tall, (int)p, (int)q, parts, nparts, X[0]);
-    OrthoK k;
     k.m = (int)o.m;
     k.n = (int)o.n;
     k.tall = tall;
@@ -609,7 +706,8 @@ hipError_t ortho_run(const OrthoArgs& o, void* ws, hipStream_t s) {
 
 size_t orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n) {
     const int64_t mp = padded(m), np = padded(n), p = mp < np ? mp : np;
-    return align256((size_t)batch * kNormBlocks * 8) + 2 * align256((size_t)batch * 4 * mp * np) +
+    const size_t sums = gram_plan(batch, p, mp < np ? np : mp).sums_bytes();
+    return (sums ? kSplitPlaces * 4 + sums : 0) + align256((size_t)batch * kNormBlocks * 8) + 2 * align256((size_t)batch * 4 * mp * np) +
            2 * align256((size_t)batch * 4 * p * p);
 }
 

@@ -30,6 +30,11 @@ struct RowSrc {
             lane_off[q] = (uint32_t)(lane >> 3) * ldb + piece[q];
         }
     }
+    // begin with stage kt
+    __device__ __forceinline__ void skip(int kt) {
+        base += (int64_t)kt * 128;
+        bytes -= (uint32_t)kt * 128u;
+    }
     // (a stage past the last: an empty range)
     __device__ __forceinline__ i32x4_t rsrc(int kt, int nk) const {
         i32x4_t r = make_rsrc(base + (kt < nk ? kt * 128 : 0));
@@ -83,16 +88,20 @@ struct TileTimes {
     int bt, places;
     double own, idle, alone, full;
 };
+inline double tile_time(const TileTimes& t, int64_t n, double stages) {
+    const int64_t rest = n % t.places;
+    double time = (double)(n / t.places) * (t.own + stages * t.full);
+    if (rest > 256) time += t.own + stages * t.full;
+    else if (rest) time += t.own + stages * (t.idle + (t.alone - t.idle) * (double)rest / 256);
+    return time;
+}
 // tiles(bt): how many there are
 template <size_t N, class F>
 int pick_tile(const TileTimes (&times)[N], double stages, F&& tiles) {
     int best = 0;
     double least = 0.0;
     for (const TileTimes& t : times) {
-        const int64_t n = tiles(t.bt), rest = n % t.places;
-        double time = (double)(n / t.places) * (t.own + stages * t.full);
-        if (rest > 256) time += t.own + stages * t.full;
-        else if (rest) time += t.own + stages * (t.idle + (t.alone - t.idle) * (double)rest / 256);
+        const double time = tile_time(t, tiles(t.bt), stages);
         if (!best || time < least) {
             best = t.bt;
             least = time;

@@ -146,3 +146,44 @@ def test_unaligned_input():
 def test_empty():
     assert om.orthogonalize(torch.empty((0, 5), device="cuda"))[0].shape == (0, 5)
     assert om.orthogonalize(torch.empty((2, 5, 0), device="cuda"))[0].shape == (2, 5, 0)
+
+
+@pytest.mark.parametrize("Z,m,n,dt", [(1, 40, 4000, "f32"), (1, 64, 2496, "bf16"), (3, 128, 2500, "f32"), (18, 3200, 192, "bf16"),
+                                      (5, 1, 900, "f32"), (1, 4096, 96, "f16"), (1, 33, 513, "f32")])
+def test_long(Z, m, n, dt):
+    """Few tiles and a long contraction, in order and again: the same bits, whatever the workspace held."""
+    G = torch.stack([draw(m, n, dt, rank=2, seed=z) for z in range(Z)])
+    size = om.orthogonalize_workspace_size(Z, m, n)
+    first = None
+    for fill in (0, 255):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        got, _ = om.orthogonalize(G.cuda(), workspace=ws)
+        for z in range(Z):
+            check(G[z], got[z], 5, dt)
+        again, _ = om.orthogonalize(G.cuda(), workspace=ws)
+        first = got if first is None else first
+        assert torch.equal(got, first) and torch.equal(again, first)
+
+
+def test_long_in_a_graph():
+    """Replays with new inputs, eager calls on the same workspace between them."""
+    G = torch.stack([draw(96, 2000, "f32", rank=3, seed=z) for z in range(5)]).cuda()
+    ws = torch.empty((om.orthogonalize_workspace_size(1, 96, 2000),), dtype=torch.uint8, device="cuda")
+    src, out = G[0].clone(), torch.empty_like(G[0])
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        om.orthogonalize(src, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            om.orthogonalize(src, out=out, workspace=ws)
+    for z in range(1, 5):
+        src.copy_(G[z])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        eager, _ = om.orthogonalize(G[z], workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(got, eager)
+        check(G[z].cpu(), got, 5, "f32")
