@@ -428,7 +428,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(MoeRouteGradArgs a) {
     typedef Layout<NE> L;
     constexpr bool ROWS = NE > 4;  // selections through rows of LDS, which are zero between two tokens
     __shared__ int32_t count[16 * NE];
-    __shared__ int32_t wsum[4];
+    __shared__ float wsum[4];
     __shared__ float grow[ROWS ? 16 : 1][ROWS ? 16 * NE : 1];
     __shared__ uint32_t crow[ROWS ? 16 : 1][ROWS ? 4 * NE : 1];  // a byte an expert
     const int t = threadIdx.x, l = t & 15, E = (int)a.E, k = a.k;
@@ -467,23 +467,24 @@ __global__ __launch_bounds__(256) void route_grad_kernel(MoeRouteGradArgs a) {
         wave_lds();
     }
     if (a.g_losses) {
-        int c = 0;
+        // in fp32, as the counts of several processes may add up to more than int32 holds (exact up to 2^24)
+        float c = 0.0f;
         for (int e = t; e < 16 * NE; e += 256) {
             const int v = e < E ? a.counts[e] : 0;
             count[e] = v;
-            c += v;
+            c += (float)v;
         }
-        c = wave_sum_int(c);
+        c = wave_sum(c);
         if ((t & 63) == 0) wsum[t >> 6] = c;
         const int n = a.tokens[0];
         const float g0 = a.g_losses[0], g1 = a.g_losses[1];
         __syncthreads();
-        const int total = wsum[0] + wsum[1] + wsum[2] + wsum[3];
-        const float cb = n > 0 && total > 0 ? g0 * (float)E / (float)n : 0.0f;
+        const float total = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
+        const float cb = n > 0 && total > 0.0f ? g0 * (float)E / (float)n : 0.0f;
         cz = n > 0 ? g1 * 2.0f / (float)n : 0.0f;
         // f of the formula with its factor
 #pragma unroll
-        for (int i = 0; i < NE; ++i) f[i] = total > 0 ? cb * ((float)count[L::at(l, i)] / (float)total) : 0.0f;
+        for (int i = 0; i < NE; ++i) f[i] = total > 0.0f ? cb * ((float)count[L::at(l, i)] / total) : 0.0f;
     }
     for (int64_t m0 = (int64_t)blockIdx.x * 16; m0 < a.M; m0 += step) {
         float g[NE] = {}, sel[NE] = {};
