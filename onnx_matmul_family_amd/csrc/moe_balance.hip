@@ -421,6 +421,12 @@ __device__ __forceinline__ void wave_lds() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Selections need not be a token's largest logits (groups, random second choices).  Where
+// their probabilities add up to less than this, some may be below fp32's range: their
+// weights are then computed among themselves, lane s that of selection s.  Above it, what
+// has no probability in fp32 has less than 2^-66 of the weight.
+constexpr float kFarBelow = 0x1p-60f;
+
 template <int DT, int NE>
 __global__ __launch_bounds__(256) void route_grad_kernel(MoeRouteGradArgs a) {
     typedef typename elem_of<DT>::type T;
@@ -531,12 +537,30 @@ __global__ __launch_bounds__(256) void route_grad_kernel(MoeRouteGradArgs a) {
         pf = row16_sum(pf);
         pg = row16_sum(pg);
         pc = row16_sum(pc);
-        const float r = a.renorm ? (pc == 0.0f ? 0.0f : 1.0f / pc) : 1.0f, mean = pg * r, zl = cz * lse - pf;
+        const bool far = a.renorm && a.g_weights && keep && pc < kFarBelow;
+        const float r = a.renorm ? (pc < kFarBelow ? 0.0f : 1.0f / pc) : 1.0f, mean = pg * r, zl = cz * lse - pf;
         float d[NE];
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             const float w = a.renorm ? r * (g[i] - sel[i] * mean) : g[i] - mean;
             d[i] = keep ? x[i] * (f[i] + zl + w) : 0.0f;
+        }
+        if (far) {
+            // (read once more: nothing but a bit is carried this far for what hardly ever is)
+            const int64_t i = l < k ? index_of(a.ids, m * k + l, a.ids64) : -1;
+            const bool in = i >= 0 && i < E;
+            const float v = in ? a.g_weights[m * k + l] : 0.0f;
+            const float y = in ? elem_f32<DT>(((const T*)a.logits)[m * E + i]) : -__builtin_inff();
+            float mx = row16_maxf(y);
+            if (mx == -__builtin_inff()) mx = 0.0f;
+            const float q = exp_small(y - mx), qc = row16_sum(q), w = qc == 0.0f ? 0.0f : q / qc;
+            const float term = w * (v - row16_sum(w * v));
+            for (int s = 0; s < k; ++s) {
+                const int e = __shfl(in ? (int)i : -1, s, 16) - L::at(l, 0);
+                const float ts = __shfl(term, s, 16);
+#pragma unroll
+                for (int c = 0; c < NE; ++c) d[c] += e == L::at(0, c) ? ts : 0.0f;
+            }
         }
         const int64_t at = m;
         m += step;
