@@ -371,7 +371,7 @@ def int8_matmul(a, b, b_scale, a_scale=None, bias=None, dtype=None, Y=None, work
 
     b (N, K) int8 with b_scale (N) float32, as quantize_rows gives them for a linear layer's weights.
     a (M, K) int8 with a_scale (M); or of a floating type without a_scale: quantised by the call.
-    dtype: of Y, by default a's (int8 a: bias's, or bfloat16).  Returns (Y, workspace); the workspace is None
+    dtype: of Y, by default a's (int8 a: bias's, or bfloat16); with a given Y its own.  Returns (Y, workspace); the workspace is None
     where none is needed."""
     if stream is not None:
         return _on(stream, int8_matmul, a, b, b_scale, a_scale, bias, dtype, Y, workspace)
@@ -382,6 +382,8 @@ def int8_matmul(a, b, b_scale, a_scale=None, bias=None, dtype=None, Y=None, work
             dtype = a.dtype
         else:
             dtype = bias.dtype if bias is not None else torch.bfloat16
+    elif Y is not None and Y.dtype != dtype:
+        raise ValueError("dtype is %s, Y is %s" % (dtype, Y.dtype))
     return (_native or native()).int8_matmul(a, a_scale, b, b_scale, bias, _DT.get(dtype, -1), Y, workspace)
 
 
