@@ -468,8 +468,11 @@ int omm_moe_route_grad(const omm_tensor* logits, const omm_tensor* indices, cons
  *   G, out (m, n) or (batch, m, n) of T, each matrix of a batch on its own; out
  *   may be G itself.  5 steps are usual; singular values then lie in about 0.7 .. 1.2
  *   (those above 1/500 of |G|).
- *   The products are exact to about 22 bits of their operands with fp32 sums,
- *   whatever T; one rounding to T at the end.
+ *   Whatever T, the products' operands are held to 2^-22 of each value, but no finer
+ *   than 2^-39 of |G|; the sums are fp32, and one rounding to T comes at the end.  So
+ *   the result's error is that of the same steps in fp32 or less, but of parts of G far
+ *   below the rest, which get fewer bits (5e-5 of the result for a block of
+ *   entries of 1e-8 |G|, 6e-4 for 1e-9 |G|; what is below 2^-40 |G| may count as 0).
  *   A matrix of zeros gives zeros; one that holds a NaN or an infinity gives NaN
  *   everywhere, and leaves the others of its batch alone.
  *   1 <= steps <= OMM_ORTHOGONALIZE_MAX_STEPS; m, n <= OMM_ORTHOGONALIZE_MAX_SIDE.

@@ -371,8 +371,8 @@ def int8_matmul(a, b, b_scale, a_scale=None, bias=None, dtype=None, Y=None, work
 
     b (N, K) int8 with b_scale (N) float32, as quantize_rows gives them for a linear layer's weights.
     a (M, K) int8 with a_scale (M); or of a floating type without a_scale: quantised by the call.
-    dtype: of Y, by default a's (int8 a: bias's, or bfloat16); with a given Y its own.  Returns (Y, workspace); the workspace is None
-    where none is needed."""
+    dtype: of Y, by default a's (int8 a: bias's, or bfloat16); with a given Y its own.
+    Returns (Y, workspace); the workspace is None where none is needed."""
     if stream is not None:
         return _on(stream, int8_matmul, a, b, b_scale, a_scale, bias, dtype, Y, workspace)
     if dtype is None:
@@ -420,7 +420,7 @@ def orthogonalize_workspace_size(batch, m, n):
 def orthogonalize(G, steps=5, out=None, workspace=None, stream=None):
     """G (m, n), or a batch (b, m, n), with its singular values brought near 1 by Newton-Schulz steps:
     X = G / |G|, then X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X with A = X X^T.  out may be G itself.
-    Returns (out, workspace)."""
+    Values are held to 2^-22 of themselves, no finer than 2^-39 of |G|.  Returns (out, workspace)."""
     if stream is not None:
         return _on(stream, orthogonalize, G, steps, out, workspace)
     return (_native or native()).orthogonalize(G, steps, out, workspace)

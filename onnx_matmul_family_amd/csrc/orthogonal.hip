@@ -8,8 +8,12 @@
 // X, A and B are held to 22 bits: as two fp16 parts (value, and what its rounding
 // leaves), scaled by 2^14.  Singular values stay below 1.21, those of B between 0.6
 // and 3.4445, so no entry passes 3.4445 and the scaled ones stay below 56500 of
-// fp16's 65504, while the second part reaches down to 2^-38 of the largest.  A product
-// is hi hi + hi lo + lo hi on the matrix unit with fp32 sums (lo lo is 2^-22 of it).
+// fp16's 65504, while the second part's smallest step is 2^-38 of |G|: entries below 2^-17
+// of it have fewer bits (1e-8: 12).  A product is hi hi + hi lo + lo hi on the matrix unit
+// with fp32 sums (lo lo is 2^-22 of it).  Errors against 64 bits, of the largest value
+// (512 x 1024 in fp32; in brackets the same steps as torch's fp32 products): noise 2.4e-6
+// (6.9e-6), four directions 100 times above it 8.8e-6 (1.1e-5), a block of 1e-8 |G| beside
+// one of |G| 5.5e-5 of its own (1.6e-7).
 //
 // Layout: a row's 32 columns are 128 bytes, 64 of the first parts and 64 of the
 // second, so a 128-byte stage of the loop holds both parts of 32 k and gives three
