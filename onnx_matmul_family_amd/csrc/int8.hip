@@ -694,8 +694,8 @@ void few_go(const FewArgs& f, hipStream_t s) {
     const size_t pieces = (size_t)kFewWaves * (NF + XG) * 2048 + (AK < 0 ? 0 : (size_t)f.p.M * f.kpad);
     const size_t lds = std::max(pieces, (size_t)kFewWaves * NF * MG * 1024);
     const dim3 grid((unsigned)((f.p.N + 16 * NF - 1) / (16 * NF)), (unsigned)((f.p.M + 16 * MG - 1) / (16 * MG)));
-    log_choice("int8_matmul: %lld rows streamed, %d columns a workgroup%s", (long long)f.p.M, 16 * NF,
-               AK < 0 ? "" : ", quantised there");
+    log_choice("int8_matmul: %lld rows streamed, %d x %d a workgroup, %d units at once%s", (long long)f.p.M, 16 * MG,
+               16 * NF, U, AK < 0 ? "" : ", quantised there");
     int8_few_kernel<DT, NF, MG, U, AK><<<grid, 64 * kFewWaves, lds, s>>>(f);
 }
 // 16 columns a workgroup while that makes no more of them than there are CUs, or, of
@@ -756,8 +756,8 @@ hipError_t product_run(const ProductArgs& a, hipStream_t s) {
     const int64_t n = count(bt);
     const auto tiles = [&](auto whole, auto ragged, int ks) {
         const int tm = (int)((a.M + bt - 1) / bt), tn = (int)((a.N + bt - 1) / bt);
-        log_choice("int8_matmul: %lld x %lld x %d, tiles of %d%s", (long long)a.M, (long long)a.N, a.K, bt,
-                   ks > 1 ? ", two groups of waves" : "");
+        log_choice("int8_matmul: %lld x %lld x %d, tiles of %d%s%s", (long long)a.M, (long long)a.N, a.K, bt,
+                   ks > 1 ? ", two groups of waves" : "", a.K % 128 ? ", ragged" : "");
         if (a.K % 128 == 0) whole<<<dim3((unsigned)n), NT * ks, 0, s>>>(a, tm, tn);
         else ragged<<<dim3((unsigned)n), NT * ks, 0, s>>>(a, tm, tn);
     };
