@@ -470,7 +470,7 @@ int omm_moe_route_grad(const omm_tensor* logits, const omm_tensor* indices, cons
  *   (those above 1/500 of |G|).
  *   Whatever T, the products' operands are held to 2^-22 of each value, but no finer
  *   than 2^-39 of |G|; the sums are fp32, and one rounding to T comes at the end.  So
- *   the result's error is that of the same steps in fp32 or less, but of parts of G far
+ *   the result's error is near that of the same steps in fp32, but of parts of G far
  *   below the rest, which get fewer bits (5e-5 of the result for a block of
  *   entries of 1e-8 |G|, 6e-4 for 1e-9 |G|; what is below 2^-40 |G| may count as 0).
  *   A matrix of zeros gives zeros; one that holds a NaN or an infinity gives NaN

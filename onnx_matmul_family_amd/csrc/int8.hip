@@ -10,10 +10,11 @@
 // What bounds it: few rows, the one read of b (1 row, 4096 x 4096: 16.8 MB in 6.5 us,
 // 2.6 TB/s, as a launch and a first load take half of that; 1 row, 8192 x 8192: 4.0 TB/s).
 // Tiles that are few, what one CU fetches (73 GB/s measured, whatever the loop: 4096 x 8192 x 128
-// in 128 tiles of 64, 1 MB each, 14.3 us).  Many tiles, the matrix unit: 8192 x 4096 x
+// in 128 tiles of 64, 1 MB each, 14.3 us, half the CUs idle: K is not split over workgroups).  Many tiles, the matrix unit: 8192 x 4096 x
 // 8192 in 237 us beside other work and 229 alone, 2.3 to 2.4 POP/s, where the library's
 // int8 product of 8192^3 reaches 2.5.  Quantising is one read and one write: 8192 x 4096 bf16
-// in 17.6 us, 5.7 TB/s of the 6.06 that a copy reaches, 8192 x 4095 in 18.1.
+// in 17.6 us, 5.7 TB/s of the 6.06 that a plain copy kernel reaches (torch's of 1 GiB: 5.13),
+// 8192 x 4095 in 18.1.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -637,8 +638,9 @@ __global__ __launch_bounds__(NT * KS, KS * NB * BT * 256 <= 80 * 1024 ? 2 * KS :
 }
 
 // Rows of K bytes at any byte -> rows of ld, a multiple of 16, zeros past K; of up to
-// two operands.  A piece is read as the five words around it and shifted into place
-// (16-byte loads at odd bytes run at a fraction of the rate).
+// two operands.  A piece is read as the five words around it and shifted into place; by
+// 16-byte loads at odd bytes the call takes as long (300 x 2005 x 2048: 15.9 us both; 2000 x
+// 2005 x 8192: 53.0, so 53.7).
 struct AlignArgs {
     const int8_t* x[2];
     int8_t* y[2];
@@ -729,7 +731,12 @@ constexpr TileTimes kTiles8[] = {{64, 512, 3, 0.2, 0.24, 0.45}, {128, 512, 6, 0.
                                  {256, 256, 14, 0.9, 1.45, 1.45}};
 constexpr int kFewRows = 64;
 
-// what is streamed: few rows, or rows that the tiles cannot take
+// what is streamed: few rows, or rows that the tiles cannot take (aligned K, but a base on
+// an odd byte: 1024 x 4096 x 4096 69 us, where tiles take 23.5).  17 to 64 rows while a
+// workgroup of 32 columns each finds a CU of its own, as the tiles are ahead from the
+// second turn on (K = 4096, us streamed and by tiles of 64, 17 / 32 / 64 rows: 4096 columns
+// 8.3 9.2 / 8.3 8.8 / 8.8 9.6; 8192 10.1 11.4 / 10.5 11.8 / 12.6 13.6; 8208 13.7 12.4 / 13.7 12.7 / 17.5
+// 14.2; 14336 17.1 16.0 / 18.3 16.0 / 23.1 17.1; 28672 31 27 / 33 28 / 43 29).
 bool streams(const ProductArgs& a, bool aligned) { return !aligned || a.M <= 16 || (a.M <= kFewRows && a.N <= 8192); }
 
 template <int DT>

@@ -45,6 +45,20 @@ def test_calls_that_overlap():
         assert torch.equal(g, want[i]), SHAPES[i]
 
 
+@pytest.mark.parametrize("Z,m,n", [(3, 128, 2500), (18, 3200, 192)])
+def test_a_matrix_that_is_not_finite(Z, m, n):
+    """NaN and zeros in a batch stay in their matrices, and in the call that they came with."""
+    G = matrix(Z, m, n)
+    ws = torch.empty((om.orthogonalize_workspace_size(Z, m, n),), dtype=torch.uint8, device="cuda")
+    want = om.orthogonalize(G, workspace=ws)[0].clone()
+    bad = G.clone()
+    bad[0, 5, 7], bad[1] = float("nan"), 0.0
+    bad[2, m - 1, n - 1] = float("inf")
+    got = om.orthogonalize(bad, workspace=ws)[0]
+    assert got[0].isnan().all() and (got[1] == 0).all() and got[2].isnan().all() and torch.equal(got[3:], want[3:])
+    assert torch.equal(om.orthogonalize(G, workspace=ws)[0], want)
+
+
 def test_two_graphs_on_one_workspace():
     """One after the other, over what the other one left."""
     shapes = [(1, 96, 2000), (18, 3200, 192)]
