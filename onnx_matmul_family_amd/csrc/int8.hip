@@ -10,11 +10,11 @@
 // What bounds it: few rows, the one read of b (1 row, 4096 x 4096: 16.8 MB in 6.5 us,
 // 2.6 TB/s, as a launch and a first load take half of that; 1 row, 8192 x 8192: 4.0 TB/s).
 // Tiles that are few, what one CU fetches (73 GB/s measured, whatever the loop: 4096 x 8192 x 128
-// in 128 tiles of 64, 1 MB each, 14.3 us, half the CUs idle: K is not split over workgroups).  Many tiles, the matrix unit: 8192 x 4096 x
-// 8192 in 237 us beside other work and 229 alone, 2.3 to 2.4 POP/s, where the library's
-// int8 product of 8192^3 reaches 2.5.  Quantising is one read and one write: 8192 x 4096 bf16
-// in 17.6 us, 5.7 TB/s of the 6.06 that a plain copy kernel reaches (torch's of 1 GiB: 5.13),
-// 8192 x 4095 in 18.1.
+// in 128 tiles of 64, 1 MB each, 14.3 us, half the CUs idle: K is not split over workgroups).
+// Many tiles, the matrix unit: 8192 x 4096 x 8192 in 237 us beside other work and 229 alone,
+// 2.3 to 2.4 POP/s, where the library's int8 product of 8192^3 reaches 2.5.  Quantising is one
+// read and one write: 8192 x 4096 bf16 in 17.6 us, 5.7 TB/s of the 6.06 that a plain copy
+// kernel reaches (torch's of 1 GiB: 5.13), 8192 x 4095 in 18.1.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
